@@ -13,12 +13,13 @@ import ctypes
 from . import _abi
 from ._abi import (FP8_PATH_AUTO, FP8_PATH_NATIVE, FP8_PATH_PROMOTE,  # noqa: F401
                    FP8_DEBUG_WAIT_LIMIT_CYCLES, FP8_DEBUG_WITHHOLD_STAGE, FP8_DEBUG_TRACE_BUFFER,
-                   FP8_MAX_GROUPS_PER_LAUNCH, fp8_group_desc)
+                   FP8_MAX_GROUPS_PER_LAUNCH, FP8_MAX_EXPERTS, FP8_QUANT_POW2, fp8_group_desc)
 
 __all__ = ["fp8_gemm_blockscaled", "fp8_gemm_blockscaled_noalloc", "fp8_gemm_grouped", "group_descs",
            "fp8_gemm_grouped_device", "fp8_grouped_workspace_bytes", "group_table", "fp8_gemm_pertoken",
            "fp8_quantize_blocks", "fp8_gemm_rowcol", "fp8_gemm_blockscaled_residual",
-           "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0", "fp8_status_query", "fp8_strerror", "fp8_version", "fp8_debug_set", "fp8_lib_shutdown",
+           "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0", "fp8_gemm_block128", "fp8_gemm_experts",
+           "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens", "fp8_status_query", "fp8_strerror", "fp8_version", "fp8_debug_set", "fp8_lib_shutdown",
            "Fp8Error", "library"]
 
 
@@ -159,6 +160,105 @@ def fp8_quantize_blocks(x, q=None, s=None, stream=None):
         s = torch.empty((M + 31) // 32, K // 32, dtype=torch.float32, device=x.device)
     _check(library().fp8_quantize_blocks(_ptr(x), _ptr(q), _ptr(s), M, K, _stream(stream)),
            "fp8_quantize_blocks")
+    return q, s
+
+
+def _want(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _sized(what, *pairs):
+    """The C entry points see addresses only: a tensor of another element size is
+    refused here."""
+    for t, size in pairs:
+        if t.element_size() != size:
+            raise ValueError(f"{what}: a tensor of type {t.dtype} where {size}-byte elements are expected")
+
+
+def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
+    """C[M,N] (bf16) = sum over 128-K blocks of sA[m][kb] sB[n/128][kb] A B^T:
+    A [M,K] codes with fp32 scales sA [M, ceil(K/128)] (one per token and 128
+    values), B [N,K] codes with sB [ceil(N/128), ceil(K/128)] (128 x 128 blocks).
+    Codes are uint8 or float8_e4m3fn; every tensor contiguous.  mode: None (AUTO),
+    FP8_PATH_PROMOTE (each row's bits independent of M) or FP8_PATH_NATIVE
+    (power-of-two scales)."""
+    (M, K), N = A.shape, B.shape[0]
+    kb = (K + 127) // 128
+    _want(B.shape == (N, K) and C.shape == (M, N) and sA.shape == (M, kb) and sB.shape == ((N + 127) // 128, kb),
+          "fp8_gemm_block128: shapes of A, sA, B, sB, C do not match")
+    _want(A.is_contiguous() and sA.is_contiguous() and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous(),
+          "fp8_gemm_block128: tensors must be contiguous")
+    _sized("fp8_gemm_block128", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2))
+    _check(library().fp8_gemm_block128_ex(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C), M, N, K,
+                                          FP8_PATH_AUTO if mode is None else int(mode), _stream(stream)),
+           "fp8_gemm_block128")
+    return C
+
+
+def fp8_gemm_experts(A, sA, B, sB, C, offsets, stream=None, mode=None):
+    """The product of fp8_gemm_block128 grouped by expert: rows offsets[e] ..
+    offsets[e+1]-1 of A [T,K] times B[e] of B [E,N,K] into the same rows of
+    C [T,N]; sA [T, ceil(K/128)], sB [E, ceil(N/128), ceil(K/128)], offsets an
+    int32 CUDA tensor of E + 1 ascending row numbers, read on the device only.
+    Experts without rows cost nothing; rows outside the table are not written."""
+    (T, K), (E, N) = A.shape, B.shape[:2]
+    kb = (K + 127) // 128
+    _want(B.shape == (E, N, K) and C.shape == (T, N) and sA.shape == (T, kb)
+          and sB.shape == (E, (N + 127) // 128, kb) and offsets.shape == (E + 1,),
+          "fp8_gemm_experts: shapes of A, sA, B, sB, C, offsets do not match")
+    _want(A.is_contiguous() and sA.is_contiguous() and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous()
+          and offsets.is_contiguous(), "fp8_gemm_experts: tensors must be contiguous")
+    _sized("fp8_gemm_experts", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2), (offsets, 4))
+    _check(library().fp8_gemm_experts_ex(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C), _ptr(offsets), T, N, K, E,
+                                         FP8_PATH_AUTO if mode is None else int(mode), _stream(stream)),
+           "fp8_gemm_experts")
+    return C
+
+
+def _token_operands(M, K, q, s, device, what):
+    kb = (K + 127) // 128
+    if q is None or s is None:
+        import torch
+        q = torch.empty(M, K, dtype=torch.uint8, device=device) if q is None else q
+        s = torch.empty(M, kb, dtype=torch.float32, device=device) if s is None else s
+    _want(q.shape == (M, K) and s.shape == (M, kb) and q.is_contiguous() and s.is_contiguous(),
+          what + ": q [M, K] and s [M, ceil(K/128)] must match and be contiguous")
+    return q, s
+
+
+def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
+    """bf16 activations x [R, K] (rows may be strided) into E4M3 codes q [M, K]
+    and fp32 scales s [M, ceil(K/128)], one per 128 values of a token: the A and
+    sA operands of fp8_gemm_block128 and fp8_gemm_experts.  rows: None (M = R)
+    or an int32 CUDA tensor [M] of rows of x to take (outside of [0, R): a row of
+    zeros).  pow2: scales rounded up to powers of two.  Returns (q, s);
+    allocates them when not given."""
+    R, K = x.shape
+    M = R if rows is None else rows.shape[0]
+    _want(x.stride(1) == 1 or K <= 1, "fp8_quantize_tokens: the values of a row must be contiguous")
+    _want(rows is None or (rows.dim() == 1 and rows.is_contiguous()), "fp8_quantize_tokens: rows must be a contiguous vector")
+    q, s = _token_operands(M, K, q, s, x.device, "fp8_quantize_tokens")
+    _sized("fp8_quantize_tokens", (x, 2), (q, 1), (s, 4))
+    if rows is not None:
+        _sized("fp8_quantize_tokens", (rows, 4))
+    _check(library().fp8_quantize_tokens(_ptr(x), x.stride(0) if R > 1 else K, R, _ptr(rows), _ptr(q), _ptr(s), M, K,
+                                         FP8_QUANT_POW2 if pow2 else 0, _stream(stream)), "fp8_quantize_tokens")
+    return q, s
+
+
+def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
+    """fp8_quantize_tokens of silu(gate) * up, with gate = x[:, :K] and
+    up = x[:, K:] of bf16 x [M, 2K] (rows may be strided)."""
+    M, K2 = x.shape
+    _want(K2 % 2 == 0, "fp8_swiglu_quantize_tokens: x holds gate and up side by side")
+    K = K2 // 2
+    _want(x.stride(1) == 1 or K2 <= 1, "fp8_swiglu_quantize_tokens: the values of a row must be contiguous")
+    q, s = _token_operands(M, K, q, s, x.device, "fp8_swiglu_quantize_tokens")
+    _sized("fp8_swiglu_quantize_tokens", (x, 2), (q, 1), (s, 4))
+    _check(library().fp8_swiglu_quantize_tokens(_ptr(x), x.stride(0) if M > 1 else K2, _ptr(q), _ptr(s), M, K,
+                                                FP8_QUANT_POW2 if pow2 else 0, _stream(stream)),
+           "fp8_swiglu_quantize_tokens")
     return q, s
 
 

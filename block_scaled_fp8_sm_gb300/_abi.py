@@ -31,6 +31,8 @@ FP8_DEBUG_WITHHOLD_STAGE = 2
 FP8_DEBUG_TRACE_BUFFER = 3
 
 FP8_MAX_GROUPS_PER_LAUNCH = 64
+FP8_MAX_EXPERTS = 1024
+FP8_QUANT_POW2 = 1
 
 # every symbol include/bsfp8.h declares
 EXPORTS = (
@@ -40,6 +42,8 @@ EXPORTS = (
     "fp8_quantize_blocks", "fp8_gemm_rowcol", "fp8_gemm_blockscaled_residual",
     "fp8_gemm_grouped_device", "fp8_grouped_workspace_bytes", "fp8_gemm_pertoken", "fp8_gemm_pertoken_ex",
     "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0",
+    "fp8_gemm_block128", "fp8_gemm_block128_ex", "fp8_gemm_experts", "fp8_gemm_experts_ex",
+    "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens",
 )
 
 
@@ -90,6 +94,18 @@ def load(path: str = None) -> ctypes.CDLL:
     lib.fp8_gemm_grouped_device.restype = ci
     lib.fp8_grouped_workspace_bytes.argtypes = [i32]
     lib.fp8_grouped_workspace_bytes.restype = i64
+    lib.fp8_gemm_block128.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
+    lib.fp8_gemm_block128.restype = ci
+    lib.fp8_gemm_block128_ex.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
+    lib.fp8_gemm_block128_ex.restype = ci
+    lib.fp8_gemm_experts.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.fp8_gemm_experts.restype = ci
+    lib.fp8_gemm_experts_ex.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, ci, vp]
+    lib.fp8_gemm_experts_ex.restype = ci
+    lib.fp8_quantize_tokens.argtypes = [vp, i64, i64, vp, vp, vp, i64, i64, ci, vp]
+    lib.fp8_quantize_tokens.restype = ci
+    lib.fp8_swiglu_quantize_tokens.argtypes = [vp, i64, vp, vp, i64, i64, ci, vp]
+    lib.fp8_swiglu_quantize_tokens.restype = ci
     lib.fp8_status_query.argtypes = [vp, ctypes.POINTER(ci)]
     lib.fp8_status_query.restype = ci
     lib.fp8_strerror.argtypes = [ci]

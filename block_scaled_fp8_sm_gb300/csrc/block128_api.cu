@@ -1,0 +1,174 @@
+// block128_api.cu -- host side of the 128-granular entry points of
+// include/bsfp8.h: argument checks and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "block128_rows.cuh"
+#include "bsfp8.h"
+#include "host.h"
+#include "quant_tokens.cuh"
+
+namespace bsfp8 {
+
+int block128_setup() { return FP8_OK; }
+
+namespace {
+
+constexpr int64_t kLim = int64_t(1) << 30;   // 32-bit indices in the kernels keep room for a tile past the end
+
+int launched() { return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA; }
+
+// Shapes and pointers common to both products.  FP8_OK with *empty set: nothing to do.
+int check_product(const void *A, const float *sA, const void *B, const float *sB, const void *C, int64_t M,
+                  int64_t N, int64_t K, int mode, bool *empty) {
+    *empty = false;
+    if (mode != FP8_PATH_AUTO && mode != FP8_PATH_NATIVE && mode != FP8_PATH_PROMOTE) return FP8_ERR_MODE;
+    if (M < 0 || N < 0 || K < 0 || M >= kLim || N >= kLim || K >= kLim) return FP8_ERR_SHAPE;
+    if (N % 8 != 0 || K % 16 != 0) return FP8_ERR_SHAPE;
+    if (M == 0 || N == 0) {
+        *empty = true;
+        return FP8_OK;
+    }
+    if (!C) return FP8_ERR_NULL;
+    if (!aligned(C, 16)) return FP8_ERR_ALIGN;
+    if (K > 0) {
+        if (!A || !B || !sA || !sB) return FP8_ERR_NULL;
+        if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 4) || !aligned(sB, 4)) return FP8_ERR_ALIGN;
+    }
+    return FP8_OK;
+}
+
+template <int NT, int U>
+int launch_rows(const RowsArgs &a, int64_t groups, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>((a.N + ROWS_N - 1) / ROWS_N), static_cast<unsigned>(groups));
+    bsfp8_block128_rows<NT, U><<<grid, ROWS_WARPS * 32, 0, stream>>>(a);
+    return launched();
+}
+
+RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
+                   int64_t K) {
+    RowsArgs a{};
+    a.A = static_cast<const uint8_t *>(A);
+    a.sA = sA;
+    a.B = static_cast<const uint8_t *>(B);
+    a.sB = sB;
+    a.C = static_cast<__nv_bfloat16 *>(C);
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.KB = static_cast<int>((K + 127) / 128);
+    return a;
+}
+
+template <bool GATED>
+int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, void *q, float *s, int64_t M,
+             int64_t K, int flags, cudaStream_t stream) {
+    const int64_t width = GATED ? 2 * K : K;
+    if (M < 0 || K < 0 || x_rows < 0 || M >= kLim || width >= kLim || x_rows >= kLim) return FP8_ERR_SHAPE;
+    if (K % 16 != 0 || ldx < width || ldx % 8 != 0) return FP8_ERR_SHAPE;
+    if (flags & ~FP8_QUANT_POW2) return FP8_ERR_MODE;
+    if (M == 0 || K == 0) return FP8_OK;
+    if (!q || !s || (!x && x_rows > 0)) return FP8_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(s, 4) || !aligned(rows, 4)) return FP8_ERR_ALIGN;
+    if (!rows && x_rows < M) return FP8_ERR_SHAPE;
+    DeviceState *d = nullptr;
+    const int rc = device_setup(&d);
+    if (rc != FP8_OK) return rc;
+    QuantTokensArgs a{};
+    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.rows = rows;
+    a.q = static_cast<uint8_t *>(q);
+    a.s = s;
+    a.ldx = ldx;
+    a.x_rows = x_rows;
+    a.K = static_cast<int>(K);
+    a.KB = static_cast<int>((K + 127) / 128);
+    a.chunks = static_cast<int>((K + 255) / 256);
+    a.units = M * a.chunks;
+    const int64_t ctas = (a.units + QTOK_THREADS / 32 - 1) / (QTOK_THREADS / 32);
+    const int64_t most = static_cast<int64_t>(d->sm_count) * 8;
+    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
+    if (flags & FP8_QUANT_POW2)
+        bsfp8_quantize_tokens<GATED, true, 2><<<grid, QTOK_THREADS, 0, stream>>>(a);
+    else
+        bsfp8_quantize_tokens<GATED, false, 2><<<grid, QTOK_THREADS, 0, stream>>>(a);
+    return launched();
+}
+
+}  // namespace
+}  // namespace bsfp8
+
+using namespace bsfp8;
+
+extern "C" {
+
+int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M,
+                         int64_t N, int64_t K, int mode, cudaStream_t stream) {
+    bool empty;
+    int rc = check_product(A, sA, B, sB, C, M, N, K, mode, &empty);
+    if (rc != FP8_OK || empty) return rc;
+    DeviceState *d = nullptr;
+    rc = device_setup(&d);
+    if (rc != FP8_OK) return rc;
+    if (K == 0) return zero_fill(C, M * N, stream);
+    RowsArgs a = rows_args(A, sA, B, sB, C, M, N, K);
+    a.status = d->status;
+    // grid.y holds at most 65535 groups of 32 rows: larger M in several launches
+    const int64_t step = int64_t(65535) * 32;
+    for (int64_t m = 0; m < M; m += step) {
+        RowsArgs part = a;
+        const int64_t n = M - m < step ? M - m : step;
+        part.A += m * K;
+        part.sA += m * a.KB;
+        part.C += m * N;
+        part.M = static_cast<int>(n);
+        rc = n <= 8 ? launch_rows<1, 4>(part, 1, stream) : launch_rows<4, 1>(part, (n + 31) / 32, stream);
+        if (rc != FP8_OK) return rc;
+    }
+    return FP8_OK;
+}
+
+int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
+                      int64_t K, cudaStream_t stream) {
+    return fp8_gemm_block128_ex(A, sA, B, sB, C, M, N, K, FP8_PATH_AUTO, stream);
+}
+
+int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const float *sB, void *C,
+                        const int32_t *offsets, int64_t T, int64_t N, int64_t K, int32_t E, int mode,
+                        cudaStream_t stream) {
+    bool empty;
+    if (E < 0 || E > FP8_MAX_EXPERTS) return FP8_ERR_SHAPE;
+    int rc = check_product(A, sA, B, sB, C, T, N, K, mode, &empty);
+    if (rc != FP8_OK || empty || E == 0) return rc;
+    if (!offsets) return FP8_ERR_NULL;
+    if (!aligned(offsets, 4)) return FP8_ERR_ALIGN;
+    if (K == 0) return FP8_ERR_SHAPE;   // which rows belong to an expert is known on the device only
+    DeviceState *d = nullptr;
+    rc = device_setup(&d);
+    if (rc != FP8_OK) return rc;
+    RowsArgs a = rows_args(A, sA, B, sB, C, T, N, K);
+    a.offsets = offsets;
+    a.E = E;
+    a.status = d->status;
+    const int64_t slots = T < E ? T : E;
+    return T <= 4 * E ? launch_rows<1, 4>(a, slots, stream) : launch_rows<4, 1>(a, slots, stream);
+}
+
+int fp8_gemm_experts(const void *A, const float *sA, const void *B, const float *sB, void *C, const int32_t *offsets,
+                     int64_t T, int64_t N, int64_t K, int32_t E, cudaStream_t stream) {
+    return fp8_gemm_experts_ex(A, sA, B, sB, C, offsets, T, N, K, E, FP8_PATH_AUTO, stream);
+}
+
+int fp8_quantize_tokens(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, void *q, float *s,
+                        int64_t M, int64_t K, int flags, cudaStream_t stream) {
+    return quantize<false>(x, ldx, x_rows, rows, q, s, M, K, flags, stream);
+}
+
+int fp8_swiglu_quantize_tokens(const void *x, int64_t ldx, void *q, float *s, int64_t M, int64_t K, int flags,
+                               cudaStream_t stream) {
+    return quantize<true>(x, ldx, M, nullptr, q, s, M, K, flags, stream);
+}
+
+}  // extern "C"

@@ -12,19 +12,13 @@
 
 #include "bsfp8.h"
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "quant_kernel.cuh"
 
 namespace bsfp8 {
 namespace {
 
 constexpr int MAX_DEVICES = 64;
-
-struct DeviceState {
-    bool ready = false;
-    int error = FP8_OK;          // sticky set-up failure (e.g. wrong architecture)
-    int sm_count = 0;
-    uint32_t *status = nullptr;  // 256-byte device allocation, word 0 used
-};
 
 std::mutex g_mu;
 DeviceState g_dev[MAX_DEVICES];
@@ -87,7 +81,8 @@ int set_kernel_attrs() {
     return FP8_OK;
 }
 
-// One-time set-up of the current device.  Returns FP8_OK and fills *out.
+}  // namespace
+
 int device_setup(DeviceState **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
@@ -120,6 +115,8 @@ int device_setup(DeviceState **out) {
     }
     int rc = set_kernel_attrs<TILE_N>();
     if (rc != FP8_OK) return rc;
+    rc = block128_setup();
+    if (rc != FP8_OK) return rc;
     if (!d.status) {
         if (cudaMalloc(&d.status, 256) != cudaSuccess) return FP8_ERR_CUDA;
         // the clear lands before any kernel of a later call, whatever stream
@@ -135,6 +132,13 @@ int device_setup(DeviceState **out) {
     *out = &d;
     return FP8_OK;
 }
+
+long long wait_limit() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    return wait_limit_locked();
+}
+
+namespace {
 
 // 2-D K-major byte tensor [rows, K] with a (BK x box_rows) box, 128-byte swizzle.
 int encode_kmajor_raw(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows) {
@@ -236,10 +240,15 @@ int cached_map(CUtensorMap *m, const MapKey &k, Encode encode) {
     return FP8_OK;
 }
 
+}  // namespace
+
 int encode_kmajor(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows) {
     return cached_map(m, MapKey{0, box_rows, base, rows, K},
                       [&](CUtensorMap *o) { return encode_kmajor_raw(o, base, rows, K, box_rows); });
 }
+
+namespace {
+
 int encode_kmajor_halves(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows) {
     return cached_map(m, MapKey{1, box_rows, base, rows, K},
                       [&](CUtensorMap *o) { return encode_kmajor_halves_raw(o, base, rows, K, box_rows); });
@@ -250,8 +259,6 @@ int encode_out(CUtensorMap *m, void *C, int64_t M, int64_t N) {
 int encode_outq(CUtensorMap *m, void *Cq, int64_t M, int64_t N) {
     return cached_map(m, MapKey{3, BM, Cq, M, N}, [&](CUtensorMap *o) { return encode_outq_raw(o, Cq, M, N); });
 }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int check_shape(int64_t M, int64_t N, int64_t K) {
     const int64_t lim = int64_t(1) << 31;
@@ -267,6 +274,8 @@ int check_mode(int mode) {
                : FP8_ERR_MODE;
 }
 
+}  // namespace
+
 int zero_fill(void *C, int64_t elems, cudaStream_t stream) {
     const int64_t n16 = (elems * 2) / 16;
     const int64_t tail = (elems * 2) % 16;
@@ -281,6 +290,8 @@ int zero_fill(void *C, int64_t elems, cudaStream_t stream) {
     }
     return FP8_OK;
 }
+
+namespace {
 
 void fill_common(Common &c, int64_t M, int64_t N, int64_t K, int mode, DeviceState *d, int BN) {
     std::memset(&c, 0, sizeof c);

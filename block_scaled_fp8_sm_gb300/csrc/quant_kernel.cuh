@@ -132,7 +132,7 @@ __device__ __forceinline__ void store_codes(const uint32_t (&w)[4][4], float s, 
     }
 }
 
-__global__ void __launch_bounds__(QT_THREADS, QT_MIN_CTAS) bsfp8_quantize_blocks(const __nv_bfloat16 *__restrict__ x,
+static __global__ void __launch_bounds__(QT_THREADS, QT_MIN_CTAS) bsfp8_quantize_blocks(const __nv_bfloat16 *__restrict__ x,
                                                                                    uint8_t *__restrict__ q,
                                                                                    float *__restrict__ s, int64_t M,
                                                                                    int64_t K) {

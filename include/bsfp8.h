@@ -64,7 +64,7 @@ enum {
     FP8_ERR_MODE = -6,       /* unknown path mode or debug key */
     FP8_ERR_SCALE = -7,      /* device status: FP8_PATH_NATIVE with a scale that is not 2^e */
     FP8_ERR_TIMEOUT = -8,    /* device status: a bounded wait inside a kernel ran out */
-    FP8_ERR_RECORD = -9      /* device status: a device-resident group record was rejected */
+    FP8_ERR_RECORD = -9      /* device status: a device-resident group record or offset table was rejected */
 };
 
 /* Path selection.
@@ -305,6 +305,83 @@ int fp8_gemm_grouped_device(const fp8_group_desc *groups, const int32_t *Ms, int
 
 /* Workspace bytes fp8_gemm_grouped_device needs for G groups (0 for G < 0). */
 int64_t fp8_grouped_workspace_bytes(int32_t G);
+
+/* ------------------------------------------------ scales per 128 values ----
+ * The scale form of FP8 mixture-of-experts and dense weights: one fp32 scale
+ * for each 128 consecutive k of a row of A (a token), and one for each
+ * 128 x 128 block of B.  With KB = ceil(K/128) and NB = ceil(N/128):
+ *
+ *   C[m,n] = bf16( sum_kb sA[m][kb] * sB[n/128][kb] * sum_{k in kb} A[m,k]*B[n,k] )
+ *
+ *   A  [M, K] E4M3, sA [M, KB] fp32; B [N, K] E4M3, sB [NB, KB] fp32;
+ *   C  [M, N] bf16, fully overwritten.  All row-major and contiguous.
+ *
+ * N a multiple of 8, K a multiple of 16 (the last block of either may be
+ * partial), M any; all below 2^30.  A, B and C 16-byte aligned, sA and sB
+ * 4-byte aligned.  Execution, errors and status as described at the top.
+ *
+ * Modes: FP8_PATH_AUTO and FP8_PATH_PROMOTE take any finite scales: the
+ * products of a 128-K block are summed by the tensor cores in fp32, then
+ * acc = fma(sA * sB, sum, acc) in fp32, K ascending.  AUTO splits K between
+ * CTAs where the tiles alone would leave the GPU idle (few rows), and adds the
+ * parts in a fixed order: a call repeats bit for bit, but a row's last bits may
+ * differ between calls of different M.  PROMOTE never splits and uses one
+ * tile shape, so each row's bits are the same for every M.
+ * FP8_PATH_NATIVE promises power-of-two scales (FP8_QUANT_POW2 makes them). */
+
+/* Returns FP8_OK or FP8_ERR_SHAPE / FP8_ERR_NULL / FP8_ERR_ALIGN / FP8_ERR_CUDA
+ * (and FP8_ERR_MODE for an unknown mode).  M == 0 or N == 0: nothing is
+ * enqueued.  K == 0: C is zero-filled. */
+int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float *sB, void *C,
+                      int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const float *sB, void *C,
+                         int64_t M, int64_t N, int64_t K, int mode, cudaStream_t stream);
+
+/* The same product grouped by expert: the T rows of A are sorted by expert,
+ * rows offsets[e] .. offsets[e+1]-1 are multiplied by B[e].
+ *   A [T, K], sA [T, KB], C [T, N] as above; B [E, N, K], sB [E, NB, KB];
+ *   offsets: DEVICE int32 [E+1], ascending, within [0, T]; read by the kernels
+ *   only, so the routing may change between replays of a CUDA graph.
+ * An expert may have any number of rows, none included; its weights are then
+ * not read.  Rows of C outside [offsets[0], offsets[E]) are not written.  A
+ * table that decreases or leaves [0, T] is clamped into [0, T], never
+ * followed out of bounds, and reported as FP8_ERR_RECORD by fp8_status_query.
+ * E <= FP8_MAX_EXPERTS; T == 0, N == 0 or E == 0: nothing is enqueued; K == 0
+ * gives FP8_ERR_SHAPE.  Returns as fp8_gemm_block128(_ex). */
+#define FP8_MAX_EXPERTS 1024
+int fp8_gemm_experts(const void *A, const float *sA, const void *B, const float *sB, void *C,
+                     const int32_t *offsets, int64_t T, int64_t N, int64_t K, int32_t E, cudaStream_t stream);
+int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const float *sB, void *C,
+                        const int32_t *offsets, int64_t T, int64_t N, int64_t K, int32_t E, int mode,
+                        cudaStream_t stream);
+
+/* Activations to the A and sA operands above: for each 128 consecutive values
+ * y of a token (the last piece of a row may be shorter)
+ *   s = max|y| / 448 (fp32 division; 1 when all are zero),
+ *   q = E4M3(y / s) (fp32 division, nearest even, saturating at +-448).
+ * flags: 0, or FP8_QUANT_POW2: s is rounded up to a power of two (at least
+ * 2^-126), as FP8_PATH_NATIVE needs it.
+ * x: bf16, rows of ldx values (ldx a multiple of 8, 16-byte aligned base),
+ *    x_rows of them, read only.
+ * rows: DEVICE int32 [M], or NULL.  Row m of the result is row rows[m] of x
+ *    (a router's order; a token may come any number of times), or row m
+ *    without rows (then x_rows >= M).  An index outside [0, x_rows) gives
+ *    a row of zeros with scales 1 (a padding slot).
+ * q: E4M3 [M, K] (16-byte aligned), s: fp32 [M, KB]; both fully overwritten.
+ * K a multiple of 16; M, x_rows < 2^30, K < 2^29.  M = 0 or K = 0: nothing is
+ * enqueued.  NaN or infinite values give undefined codes in their own piece.
+ * Returns FP8_OK or FP8_ERR_SHAPE / FP8_ERR_NULL / FP8_ERR_ALIGN /
+ * FP8_ERR_MODE (flags) / FP8_ERR_CUDA. */
+#define FP8_QUANT_POW2 1
+int fp8_quantize_tokens(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, void *q, float *s,
+                        int64_t M, int64_t K, int flags, cudaStream_t stream);
+
+/* The same of the gated activation between an expert's two products:
+ * y = silu(gate) * up = gate / (1 + exp(-gate)) * up, in fp32, with gate in
+ * columns [0, K) and up in columns [K, 2K) of x (M rows, ldx >= 2K).  A piece
+ * whose largest |y| is below 2^-100 counts as all zero. */
+int fp8_swiglu_quantize_tokens(const void *x, int64_t ldx, void *q, float *s, int64_t M, int64_t K, int flags,
+                               cudaStream_t stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status
  * words: the one the regular entry points write (including FP8_ERR_RECORD
