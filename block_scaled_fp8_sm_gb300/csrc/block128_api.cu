@@ -6,13 +6,31 @@
 #include <cstdint>
 
 #include "block128_rows.cuh"
+#include "block128_tile.cuh"
 #include "bsfp8.h"
 #include "host.h"
 #include "quant_tokens.cuh"
 
 namespace bsfp8 {
 
-int block128_setup() { return FP8_OK; }
+namespace {
+
+template <int BN, bool SPLIT>
+int set_tile_attrs() {
+    return cudaFuncSetAttribute(bsfp8_block128_tile<BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem128<BN>()) == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_CUDA;
+}
+
+}  // namespace
+
+int block128_setup() {
+    if (set_tile_attrs<256, false>() != FP8_OK || set_tile_attrs<128, false>() != FP8_OK ||
+        set_tile_attrs<128, true>() != FP8_OK)
+        return FP8_ERR_CUDA;
+    return FP8_OK;
+}
 
 namespace {
 
@@ -60,6 +78,74 @@ RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *s
     a.K = static_cast<int>(K);
     a.KB = static_cast<int>((K + 127) / 128);
     return a;
+}
+
+template <int BN, bool SPLIT>
+int launch_tile(const RowsArgs &r, int split, DeviceState *d, cudaStream_t stream) {
+    Tile128Args a{};
+    const int64_t brows = static_cast<int64_t>(r.N) * (r.offsets ? r.E : 1);
+    int rc = encode_kmajor(&a.tmA, r.A, r.M, r.K, T128_BM);
+    if (rc != FP8_OK) return rc;
+    rc = encode_kmajor(&a.tmB, r.B, brows, r.K, BN);
+    if (rc != FP8_OK) return rc;
+    a.sA = r.sA;
+    a.sB = r.sB;
+    a.C = r.C;
+    a.offsets = r.offsets;
+    a.status = d->status;
+    a.wait_limit = wait_limit();
+    a.withhold = withheld_stage();
+    a.M = r.M;
+    a.N = r.N;
+    a.K = r.K;
+    a.KB = r.KB;
+    a.NB = (r.N + 127) / 128;
+    a.E = r.E;
+    a.mt = (r.M + T128_BM - 1) / T128_BM;
+    a.nt = (r.N + BN - 1) / BN;
+    if constexpr (SPLIT) {   // one tile per cluster
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(split);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(a.mt * a.nt * split));
+        cfg.blockDim = dim3(T128_THREADS);
+        cfg.dynamicSmemBytes = smem128<BN>();
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, bsfp8_block128_tile<BN, true>, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    } else {
+        const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt;
+        const unsigned grid = static_cast<unsigned>(!r.offsets && tiles < d->sm_count ? tiles : d->sm_count);
+        bsfp8_block128_tile<BN, false><<<grid, T128_THREADS, smem128<BN>(), stream>>>(a);
+        return launched();
+    }
+}
+
+// The form of one product: rows (M <= 8), or tiles of 128 x 256 where they fill the
+// GPU, else of 128 x 128 with K split over clusters.
+int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
+    const bool pinned = mode != FP8_PATH_AUTO;
+    if (!pinned && a.M <= 8) return launch_rows<1, 4>(a, 1, stream);
+    const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
+    const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
+    if (wide >= d->sm_count) return launch_tile<256, false>(a, 1, d, stream);
+    int split = 1;
+    while (!pinned && split < 8 && narrow * split * 2 <= d->sm_count && a.KB >= split * 4) split *= 2;
+    if (split > 1) return launch_tile<128, true>(a, split, d, stream);
+    return launch_tile<128, false>(a, 1, d, stream);
+}
+
+// Experts: the row counts are on the device, so the rule goes by the average.  A few
+// rows each: the rows form; else tiles, 256 columns wide where there are enough.
+int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
+    if (mode == FP8_PATH_AUTO && a.M <= 4 * static_cast<int64_t>(a.E))
+        return launch_rows<1, 4>(a, a.M < a.E ? a.M : a.E, stream);
+    const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
+    if (most * ((a.N + 255) / 256) >= 4 * d->sm_count) return launch_tile<256, false>(a, 1, d, stream);
+    return launch_tile<128, false>(a, 1, d, stream);
 }
 
 template <bool GATED>
@@ -115,19 +201,7 @@ int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const fl
     if (K == 0) return zero_fill(C, M * N, stream);
     RowsArgs a = rows_args(A, sA, B, sB, C, M, N, K);
     a.status = d->status;
-    // grid.y holds at most 65535 groups of 32 rows: larger M in several launches
-    const int64_t step = int64_t(65535) * 32;
-    for (int64_t m = 0; m < M; m += step) {
-        RowsArgs part = a;
-        const int64_t n = M - m < step ? M - m : step;
-        part.A += m * K;
-        part.sA += m * a.KB;
-        part.C += m * N;
-        part.M = static_cast<int>(n);
-        rc = n <= 8 ? launch_rows<1, 4>(part, 1, stream) : launch_rows<4, 1>(part, (n + 31) / 32, stream);
-        if (rc != FP8_OK) return rc;
-    }
-    return FP8_OK;
+    return launch_product(a, mode, d, stream);
 }
 
 int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
@@ -139,7 +213,7 @@ int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const flo
                         const int32_t *offsets, int64_t T, int64_t N, int64_t K, int32_t E, int mode,
                         cudaStream_t stream) {
     bool empty;
-    if (E < 0 || E > FP8_MAX_EXPERTS) return FP8_ERR_SHAPE;
+    if (E < 0 || E > FP8_MAX_EXPERTS || (N > 0 && N < kLim && E * N >= 2 * kLim)) return FP8_ERR_SHAPE;
     int rc = check_product(A, sA, B, sB, C, T, N, K, mode, &empty);
     if (rc != FP8_OK || empty || E == 0) return rc;
     if (!offsets) return FP8_ERR_NULL;
@@ -152,8 +226,7 @@ int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const flo
     a.offsets = offsets;
     a.E = E;
     a.status = d->status;
-    const int64_t slots = T < E ? T : E;
-    return T <= 4 * E ? launch_rows<1, 4>(a, slots, stream) : launch_rows<4, 1>(a, slots, stream);
+    return launch_experts(a, mode, d, stream);
 }
 
 int fp8_gemm_experts(const void *A, const float *sA, const void *B, const float *sB, void *C, const int32_t *offsets,

@@ -1,0 +1,398 @@
+// block128_tile.cuh -- the 128-granular product on the tensor cores (tcgen05,
+// tensor-memory partials, TMA operands), for one product or for the ragged rows
+// of many experts.
+//
+//   C[m,n] = bf16( sum_kb sA[m][kb] sB[n/128][kb] sum_{k in kb} A[m,k] B[n,k] )
+//
+// The inner sum of a 128-K block is four unscaled kind::f8f6f4 MMAs (K = 32) into
+// one tensor-memory partial.  The epilogue warps add it to fp32 registers:
+// acc = fma(s, partial, acc).  A thread owns one row of the tile and columns of one
+// 128-column block of B, so s = sA[m][kb] sB[nb][kb] is one number per thread and
+// block, and 128 K values cost one FMA per output.
+//
+// Roles (384 threads): warp 0 producer (one lane: one TMA box per operand and 128-K
+// stage, 128-byte swizzle); warp 1 MMA (one lane); warps 4-11 epilogue: warp w reads
+// the tensor-memory lanes (rows) 32 (w mod 4) .., columns of half (w - 4) / 4.  The
+// partials are double- (BN = 256) or quadruple-buffered (BN = 128).
+//
+// Without SPLIT a CTA is persistent over tiles; with SPLIT a cluster of CTAs shares
+// one tile, each taking a range of K blocks: the partial sums meet in the CTAs' own
+// shared memory and are added in rank order over distributed shared memory, so a
+// call repeats bit for bit.
+//
+// Every wait is bounded as in the other kernels: on expiry the status word is set,
+// the roles leave, loads and MMAs in flight are drained and the kernel returns.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "block128_rows.cuh"
+#include "ptx.cuh"
+
+namespace bsfp8 {
+
+constexpr int T128_BM = 128;
+constexpr int T128_THREADS = 384;
+constexpr int T128_EPI_WARPS = 8;
+constexpr int T128_GROUP_M = 16;   // m-tiles per group of the tile order (L2 reuse)
+constexpr int T128_MAX_EXPERTS = 1024;
+
+struct Tile128Args {
+    CUtensorMap tmA, tmB;
+    const float *sA, *sB;
+    __nv_bfloat16 *C;
+    const int32_t *offsets;   // [E + 1], or null: one product
+    uint32_t *status;
+    long long wait_limit;
+    int M, N, K, KB, NB, E, mt, nt;
+    int withhold;             // test hook: CTA 0 never loads this stage (-1: off)
+};
+
+template <int BN>
+struct Cfg128 {
+    static constexpr int A_BYTES = T128_BM * 128;
+    static constexpr int B_BYTES = BN * 128;
+    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int BUFS = 512 / BN;
+    static constexpr int COLS = BN / 2;   // columns per epilogue thread
+    static constexpr int STG = T128_EPI_WARPS * 32 * 64;   // 32 rows x 32 bf16 columns per epilogue warp
+};
+
+template <int BN>
+struct Ctrl128 {
+    uint64_t full[Cfg128<BN>::STAGES], empty[Cfg128<BN>::STAGES];
+    uint64_t tfull[Cfg128<BN>::BUFS], tempty[Cfg128<BN>::BUFS], drain;
+    uint32_t tmem;
+    int abort, tiles;
+    int start[T128_MAX_EXPERTS + 1];   // experts: first tile of each
+};
+
+template <int BN>
+constexpr int smem128() {
+    return 1024 + Cfg128<BN>::STAGES * (Cfg128<BN>::A_BYTES + Cfg128<BN>::B_BYTES) + Cfg128<BN>::STG +
+           static_cast<int>(sizeof(Ctrl128<BN>));
+}
+
+// Bounded wait: polls, and looks at the clock and the abort flag every 16 polls.
+template <typename Ctl>
+__device__ __forceinline__ bool wait128(uint64_t *bar, uint32_t parity, Ctl *ctl, const Tile128Args &a) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 15u) == 0u) {
+            if (*reinterpret_cast<volatile int *>(&ctl->abort)) return false;
+            if (clock64() - t0 > a.wait_limit) {
+                *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+                atomicOr(a.status, 1u);   // STATUS_TIMEOUT
+                return false;
+            }
+        }
+    }
+}
+
+struct Tile128 {
+    int m0, hi, n0, e;   // first row, end of its rows, first column, expert
+};
+
+// Tile t of the launch: experts in order, or groups of T128_GROUP_M m-tiles; m fastest.
+template <int BN, typename Ctl>
+__device__ __forceinline__ Tile128 tile128(const Tile128Args &a, const Ctl *ctl, int t) {
+    Tile128 r;
+    if (a.offsets) {
+        int e0 = 0, e1 = a.E;   // start[e0] <= t < start[e1]
+        while (e1 - e0 > 1) {
+            const int mid = (e0 + e1) >> 1;
+            if (ctl->start[mid] <= t) e0 = mid;
+            else e1 = mid;
+        }
+        int lo;
+        expert_rows(a.offsets, e0, a.M, lo, r.hi);
+        const int in = t - ctl->start[e0], mt = (ctl->start[e0 + 1] - ctl->start[e0]) / a.nt;
+        r.e = e0;
+        r.m0 = lo + (in % mt) * T128_BM;
+        r.n0 = in / mt * BN;
+    } else {
+        const int per = T128_GROUP_M * a.nt, grp = t / per, first = grp * T128_GROUP_M;
+        const int size = min(a.mt - first, T128_GROUP_M), in = t - grp * per;
+        r.e = 0;
+        r.m0 = (first + in % size) * T128_BM;
+        r.n0 = in / size * BN;
+        r.hi = a.M;
+    }
+    return r;
+}
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int BN, bool SPLIT>
+__global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __grid_constant__ Tile128Args a) {
+    using C = Cfg128<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm_a = smem, *sm_b = smem + C::STAGES * C::A_BYTES;
+    uint8_t *stg = sm_b + C::STAGES * C::B_BYTES;
+    Ctrl128<BN> *ctl = reinterpret_cast<Ctrl128<BN> *>(stg + C::STG);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank = 0, ranks = 1;
+    if constexpr (SPLIT) {
+        rank = cluster_ctarank();
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    }
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < C::BUFS; ++b) {
+            mbar_init(&ctl->tfull[b], 1);
+            mbar_init(&ctl->tempty[b], T128_EPI_WARPS);
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&a.tmA);
+        tma_prefetch_desc(&a.tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 2) {
+        if (a.offsets) {   // first tile of each expert: a running sum over the warp
+            int base = 0;
+            for (int e0 = 0; e0 < a.E; e0 += 32) {
+                const int e = e0 + lane;
+                int lo = 0, hi = 0;
+                if (e < a.E) {
+                    expert_rows(a.offsets, e, a.M, lo, hi);
+                    if (blockIdx.x == 0 && (lo != __ldg(a.offsets + e) || hi != __ldg(a.offsets + e + 1) || hi < lo))
+                        atomicOr(a.status, 4u);   // STATUS_RECORD
+                }
+                int n = hi > lo ? (hi - lo + T128_BM - 1) / T128_BM * a.nt : 0;
+                int sum = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                if (e < a.E) ctl->start[e] = base + sum - n;
+                base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            }
+            if (lane == 0) ctl->start[a.E] = ctl->tiles = base;
+        } else if (lane == 0) {
+            ctl->tiles = a.mt * a.nt;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const int tiles = ctl->tiles;
+    const int unit = static_cast<int>(blockIdx.x / ranks), units = static_cast<int>(gridDim.x / ranks);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(a.KB) * rank / ranks);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(a.KB) * (rank + 1) / ranks);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0, s = 0, withheld = -1;
+            uint32_t ph = 1;
+            bool ok = true;
+            for (int t = unit; t < tiles && ok; t += units) {
+                const Tile128 tt = tile128<BN>(a, ctl, t);
+                const int brow = tt.e * a.N + tt.n0;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait128(&ctl->empty[s], ph, ctl, a);
+                    if (!ok) break;
+                    if (it == a.withhold && blockIdx.x == 0) {
+                        withheld = s;
+                    } else {
+                        mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + C::B_BYTES);
+                        tma_load_2d(&a.tmA, &ctl->full[s], sm_a + s * C::A_BYTES, kb * 128, tt.m0);
+                        tma_load_2d(&a.tmB, &ctl->full[s], sm_b + s * C::B_BYTES, kb * 128, brow);
+                    }
+                    ++it;
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // no load is in flight when the CTA leaves
+            for (int d = max(0, it - C::STAGES); d < it; ++d) {
+                if (d % C::STAGES == withheld) continue;
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&ctl->full[d % C::STAGES], static_cast<uint32_t>(d / C::STAGES) & 1u))
+                    if (clock64() - t0 > a.wait_limit) break;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f8f6f4(T128_BM, BN);
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;
+            bool ok = true;
+            for (int t = unit; t < tiles && ok; t += units) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait128(&ctl->tempty[b], bph, ctl, a) && wait128(&ctl->full[s], ph, ctl, a);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_k_sw128(smem_u32(sm_a + s * C::A_BYTES));
+                    const uint64_t bd = sdesc_k_sw128(smem_u32(sm_b + s * C::B_BYTES));
+                    const uint32_t d = tmem + b * BN;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_f8(d, ad + 2 * i, bd + 2 * i, idesc, i > 0);
+                    mma_commit(&ctl->empty[s]);
+                    mma_commit(&ctl->tfull[b]);
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (++b == C::BUFS) {
+                        b = 0;
+                        bph ^= 1u;
+                    }
+                }
+            }
+            // all MMAs have completed before tensor memory is freed
+            mma_commit(&ctl->drain);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&ctl->drain, 0))
+                if (clock64() - t0 > a.wait_limit) break;
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int r = q * 32 + lane;   // row of the tile
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::COLS;
+        uint8_t *mine = stg + (warp - 4) * (32 * 64);
+        int b = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        for (int t = unit; t < tiles && ok; t += units) {
+            const Tile128 tt = tile128<BN>(a, ctl, t);
+            const int m = min(tt.m0 + r, tt.hi - 1);
+            const int nb = min((tt.n0 + h * C::COLS) / 128, a.NB - 1);
+            const float *psa = a.sA + static_cast<int64_t>(m) * a.KB;
+            const float *psb = a.sB + (static_cast<int64_t>(tt.e) * a.NB + nb) * a.KB;
+            float acc[C::COLS];
+#pragma unroll
+            for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+            float sa = 0.0f, sb = 0.0f;
+            if (kb0 < kb1) {
+                sa = __ldg(psa + kb0);
+                sb = __ldg(psb + kb0);
+            }
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const float sc = sa * sb;
+                const int next = min(kb + 1, kb1 - 1);
+                sa = __ldg(psa + next);
+                sb = __ldg(psb + next);
+                const uint64_t s2 = f32x2_pack(__float_as_uint(sc), __float_as_uint(sc));
+                ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->tfull[b], bph, ctl, a));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < C::COLS / 32; ++x) {
+                    uint32_t p[32];
+                    tmem_ld_x32(taddr + b * BN + 32 * x, p);
+                    tmem_ld_wait();
+                    if (x == C::COLS / 32 - 1) {   // the partial is in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->tempty[b]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        uint64_t v = f32x2_pack(__float_as_uint(acc[32 * x + 2 * j]), __float_as_uint(acc[32 * x + 2 * j + 1]));
+                        fma_f32x2(v, f32x2_pack(p[2 * j], p[2 * j + 1]), s2);
+                        uint32_t lo, hi;
+                        f32x2_unpack(v, lo, hi);
+                        acc[32 * x + 2 * j] = __uint_as_float(lo);
+                        acc[32 * x + 2 * j + 1] = __uint_as_float(hi);
+                    }
+                }
+                if (++b == C::BUFS) {
+                    b = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if constexpr (SPLIT) {
+                // the partial sums go to the operand ring's memory (nothing is in
+                // flight there any more: the last partial came after the last load),
+                // 16-byte pieces exchanged by row so that the eight rows of a
+                // quarter-warp hit different banks
+                float4 *red = reinterpret_cast<float4 *>(smem);
+#pragma unroll
+                for (int j = 0; j < C::COLS / 4; ++j)
+                    red[r * (BN / 4) + ((h * (C::COLS / 4) + j) ^ (r & 7))] =
+                        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < C::COLS / 32; ++x) {
+                    const int col = tt.n0 + h * C::COLS + 32 * x;
+                    uint4 *row = reinterpret_cast<uint4 *>(mine + lane * 64);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[32 * x + 8 * c + 2 * j],
+                                                                          acc[32 * x + 8 * c + 2 * j + 1]);
+                            w[j] = *reinterpret_cast<const uint32_t *>(&v);
+                        }
+                        row[c ^ ((lane >> 1) & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // eight rows of 64 bytes per store
+                        const int rr = i * 8 + (lane >> 2), c = lane & 3;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+                        const int mm = tt.m0 + q * 32 + rr;
+                        if (mm < tt.hi && col + 8 * c < a.N)
+                            *reinterpret_cast<uint4 *>(a.C + static_cast<int64_t>(mm) * a.N + col + 8 * c) = v;
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (SPLIT) {
+        cluster_sync();   // every CTA's partial sums are in its shared memory
+        if (unit < tiles) {
+            const Tile128 tt = tile128<BN>(a, ctl, unit);
+            const int rows = T128_BM / static_cast<int>(ranks), r0 = static_cast<int>(rank) * rows;
+            const uint32_t base = smem_u32(smem);
+            // pairs of columns of this CTA's share of the rows
+            for (int i = threadIdx.x; i < rows * (BN / 2); i += T128_THREADS) {
+                const int r = r0 + i / (BN / 2), c = (i % (BN / 2)) * 2;
+                const uint32_t off = static_cast<uint32_t>(r * BN + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3))) * 4u;
+                if (tt.m0 + r >= tt.hi || tt.n0 + c >= a.N) continue;
+                float v0 = 0.0f, v1 = 0.0f;
+                for (uint32_t k = 0; k < ranks; ++k) {
+                    uint32_t peer;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(base + off), "r"(k));
+                    v0 += ld_dsmem_f32(peer);
+                    v1 += ld_dsmem_f32(peer + 4u);
+                }
+                *reinterpret_cast<__nv_bfloat162 *>(a.C + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0 + c) =
+                    __floats2bfloat162_rn(v0, v1);
+            }
+        }
+        cluster_sync();   // no CTA leaves while a peer reads its shared memory
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace bsfp8

@@ -138,6 +138,11 @@ long long wait_limit() {
     return wait_limit_locked();
 }
 
+int withheld_stage() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    return g_withhold_stage;
+}
+
 namespace {
 
 // 2-D K-major byte tensor [rows, K] with a (BK x box_rows) box, 128-byte swizzle.

@@ -22,6 +22,9 @@ int device_setup(DeviceState **out);
 // SM cycles a device-side wait may spin (FP8_DEBUG_WAIT_LIMIT_CYCLES).
 long long wait_limit();
 
+// The pipeline stage CTA 0 never loads (FP8_DEBUG_WITHHOLD_STAGE), -1: none.
+int withheld_stage();
+
 // C (elems bf16 values, 16-byte multiples) = 0.
 int zero_fill(void *C, int64_t elems, cudaStream_t stream);
 

@@ -346,7 +346,7 @@ int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const fl
  * not read.  Rows of C outside [offsets[0], offsets[E]) are not written.  A
  * table that decreases or leaves [0, T] is clamped into [0, T], never
  * followed out of bounds, and reported as FP8_ERR_RECORD by fp8_status_query.
- * E <= FP8_MAX_EXPERTS; T == 0, N == 0 or E == 0: nothing is enqueued; K == 0
+ * E <= FP8_MAX_EXPERTS and E * N < 2^31; T == 0, N == 0 or E == 0: nothing is enqueued; K == 0
  * gives FP8_ERR_SHAPE.  Returns as fp8_gemm_block128(_ex). */
 #define FP8_MAX_EXPERTS 1024
 int fp8_gemm_experts(const void *A, const float *sA, const void *B, const float *sB, void *C,
