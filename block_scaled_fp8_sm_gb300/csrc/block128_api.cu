@@ -34,6 +34,7 @@ int block128_setup() {
 
 namespace {
 
+constexpr int QTOK_U = 2;   // pieces a group of eight lanes loads ahead
 constexpr int64_t kLim = int64_t(1) << 30;   // 32-bit indices in the kernels keep room for a tile past the end
 
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA; }
@@ -171,16 +172,34 @@ int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, vo
     a.x_rows = x_rows;
     a.K = static_cast<int>(K);
     a.KB = static_cast<int>((K + 127) / 128);
-    a.chunks = static_cast<int>((K + 255) / 256);
-    a.units = M * a.chunks;
-    const int64_t ctas = (a.units + QTOK_THREADS / 32 - 1) / (QTOK_THREADS / 32);
-    const int64_t most = static_cast<int64_t>(d->sm_count) * 8;
-    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-    if (flags & FP8_QUANT_POW2)
-        bsfp8_quantize_tokens<GATED, true, 2><<<grid, QTOK_THREADS, 0, stream>>>(a);
-    else
-        bsfp8_quantize_tokens<GATED, false, 2><<<grid, QTOK_THREADS, 0, stream>>>(a);
-    return launched();
+    // p / KB for p < 2^31: multiplier ceil(2^(31 + l) / KB) with l = ceil(log2 KB)
+    // (Granlund and Montgomery, PLDI 1994), below 2^32
+    int l = 0;
+    while ((int64_t(1) << l) < a.KB) ++l;
+    a.shift = static_cast<uint32_t>(31 + l);
+    a.mul = static_cast<uint32_t>(((uint64_t(1) << a.shift) + a.KB - 1) / a.KB);
+    const int64_t step = (kLim * 2 - 1) / a.KB;   // rows per launch: fewer than 2^31 pieces
+    for (int64_t m = 0; m < M; m += step) {
+        const int64_t n = M - m < step ? M - m : step;
+        a.pieces = static_cast<uint32_t>(n * a.KB);
+        const int64_t ctas = (n * a.KB + QTOK_GROUPS - 1) / QTOK_GROUPS;
+        const int64_t most = static_cast<int64_t>(d->sm_count) * 16;
+        const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
+        if (flags & FP8_QUANT_POW2)
+            bsfp8_quantize_tokens<GATED, true, QTOK_U><<<grid, QTOK_THREADS, 0, stream>>>(a);
+        else
+            bsfp8_quantize_tokens<GATED, false, QTOK_U><<<grid, QTOK_THREADS, 0, stream>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
+        if (rows) {
+            a.rows += n;
+        } else {
+            a.x += n * ldx;
+            a.x_rows -= n;
+        }
+        a.q += n * K;
+        a.s += n * a.KB;
+    }
+    return FP8_OK;
 }
 
 }  // namespace

@@ -4,10 +4,13 @@
 //   y = x[row]  or  silu(g) u,   s = max|y| / 448 (1 for an all-zero piece; with
 //   FP8_QUANT_POW2 rounded up to a power of two),   q = E4M3(y / s)
 //
-// HBM-bound: 2 bytes read (gated: 4) and 1 written per value.  A warp takes 256
-// columns of a row at a time, lane l the 16 bytes of columns 8l .. 8l+7, so the
-// sixteen lanes of a half-warp hold one 128-value piece and its maximum takes
-// four shuffles; U such units are loaded before the first is converted.
+// 2 bytes read (gated: 4) and 1 written per value: HBM sets the floor, and a value
+// may cost few instructions before the integer and conversion pipes set the time.
+// So eight lanes share a piece, sixteen values each (columns 8l .. 8l+7 and 64 + 8l ..
+// of the piece: every load of a warp is four runs of 128 bytes): the maximum takes
+// three shuffles for sixteen values.  The row of a piece comes from a multiplication
+// by the reciprocal of the pieces per row, and U pieces are loaded before the first
+// is converted.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -17,14 +20,17 @@
 namespace bsfp8 {
 
 constexpr int QTOK_THREADS = 256;
+constexpr int QTOK_GROUPS = QTOK_THREADS / 8;   // pieces a CTA converts at a time
 
 struct QuantTokensArgs {
     const __nv_bfloat16 *x;   // rows of ldx values; gated: gate in [0, K), up in [K, 2K)
     const int32_t *rows;      // [M] source rows, or null
     uint8_t *q;               // [M, K]
     float *s;                 // [M, KB]
-    int64_t ldx, x_rows, units;   // units: M * chunks
-    int K, KB, chunks;        // chunks of 256 columns per row
+    int64_t ldx, x_rows;
+    uint32_t pieces;          // M * KB < 2^31
+    uint32_t mul, shift;      // piece / KB = piece * mul >> shift, exact for pieces < 2^31
+    int K, KB;
 };
 
 // s rounded up to a power of two, at least 2^-126 (so that 1/s is exact).
@@ -32,77 +38,181 @@ __device__ __forceinline__ float pow2_up(float s) {
     return __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u);
 }
 
-// silu(gate) * up in fp32: the sigmoid from exp(-|gate|) <= 1, so that no
+__device__ __forceinline__ uint64_t f32x2_of(float lo, float hi) {
+    return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi));
+}
+
+// silu(g) u on two values.  exp(-|g|) = 2^t, t = -|g| log2(e): the product's rounding
+// error t_lo comes from an fma (Dekker's error-free product) and enters as
+// 2^t (1 + t_lo ln 2); the sigmoid is r = 1 / (1 + e), or e r for negative g, so no
 // exponential overflows and small results keep their relative precision.
-__device__ __forceinline__ float silu_mul(float gate, float up) {
-    const float e = expf(-fabsf(gate));
-    const float r = __frcp_rn(1.0f + e);
-    return gate * (gate >= 0.0f ? r : e * r) * up;
+__device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
+    constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
+    uint32_t g0, g1;
+    f32x2_unpack(g, g0, g1);
+    const uint64_t a = f32x2_pack(g0 | 0x80000000u, g1 | 0x80000000u);   // -|g|
+    const uint64_t l2 = f32x2_of(kL, kL);
+    const uint64_t t = mul_f32x2_rn(a, l2);
+    const uint64_t neg_t = t ^ 0x8000000080000000ull;
+    uint64_t lo = fma_f32x2_rn(a, l2, neg_t);
+    lo = fma_f32x2_rn(a, f32x2_of(kLlo, kLlo), lo);
+    uint32_t t0, t1;
+    f32x2_unpack(t, t0, t1);
+    float e0, e1;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(__uint_as_float(t0)));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(__uint_as_float(t1)));
+    uint64_t e = f32x2_of(e0, e1);
+    e = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(kLn2, kLn2)), e, e);
+    uint32_t b0, b1;
+    f32x2_unpack(e, b0, b1);
+    float r0, r1;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(1.0f + __uint_as_float(b0)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(1.0f + __uint_as_float(b1)));
+    const uint32_t n0 = static_cast<int32_t>(g0) < 0 ? b0 : 0x3F800000u;   // e for negative g, else 1
+    const uint32_t n1 = static_cast<int32_t>(g1) < 0 ? b1 : 0x3F800000u;
+    const uint64_t sig = mul_f32x2_rn(f32x2_pack(n0, n1), f32x2_of(r0, r1));
+    return mul_f32x2_rn(mul_f32x2_rn(g, sig), u);
+}
+
+// The E4M3 codes of eight values, in order.
+__device__ __forceinline__ uint2 pack_codes(const float (&v)[8]) {
+    return make_uint2(__byte_perm(e4m3x2(v[0], v[1]), e4m3x2(v[2], v[3]), 0x5410),
+                      __byte_perm(e4m3x2(v[4], v[5]), e4m3x2(v[6], v[7]), 0x5410));
+}
+
+// Codes of y / s for eight fp32 values (packed pairs): the quotient by the
+// correctly rounded reciprocal and its remainder, negated as in codes8.
+__device__ __forceinline__ uint2 codes8_f32(const uint64_t (&y)[4], float s, float nrc) {
+    const uint64_t n2 = f32x2_of(nrc, nrc), s2 = f32x2_of(s, s);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t q = mul_f32x2_rn(y[j], n2);
+        uint32_t lo, hi;
+        f32x2_unpack(fma_f32x2_rn(fma_f32x2_rn(q, s2, y[j]), n2, q), lo, hi);
+        v[2 * j] = __uint_as_float(lo);
+        v[2 * j + 1] = __uint_as_float(hi);
+    }
+    const uint2 c = pack_codes(v);
+    return make_uint2(c.x ^ 0x80808080u, c.y ^ 0x80808080u);
+}
+
+// Codes of y * inv, inv an exact power of two.
+__device__ __forceinline__ uint2 codes8_pow2(const uint64_t (&y)[4], float inv) {
+    const uint64_t i2 = f32x2_of(inv, inv);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t lo, hi;
+        f32x2_unpack(mul_f32x2_rn(y[j], i2), lo, hi);
+        v[2 * j] = __uint_as_float(lo);
+        v[2 * j + 1] = __uint_as_float(hi);
+    }
+    return pack_codes(v);
 }
 
 template <bool GATED, bool POW2, int U>
 __global__ void __launch_bounds__(QTOK_THREADS) bsfp8_quantize_tokens(const QuantTokensArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (QTOK_THREADS / 32);
-    const int64_t w0 = static_cast<int64_t>(blockIdx.x) * (QTOK_THREADS / 32) + (threadIdx.x >> 5);
-    for (int64_t base = w0; base < a.units; base += warps * U) {
-        uint4 v[U], up[GATED ? U : 1];
-        int64_t row[U];
-        int col[U];
-        bool in[U];
+    const int l = threadIdx.x & 7;
+    const uint32_t stride = gridDim.x * QTOK_GROUPS;
+    // the whole warp stays in the loop together (shuffles): the bound is the warp's
+    const uint32_t first = blockIdx.x * QTOK_GROUPS + (threadIdx.x >> 5) * 4, mine = (threadIdx.x >> 3) & 3;
+    for (uint32_t base = first; base < a.pieces; base += stride * U) {
+        uint4 v[U][2], up[GATED ? U : 1][2];
+        uint32_t row[U];
+        int kb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t unit = base + u * warps;
-            row[u] = unit / a.chunks;
-            col[u] = static_cast<int>(unit - row[u] * a.chunks) * 256 + 8 * lane;
-            in[u] = unit < a.units && col[u] < a.K;
+            const uint32_t p = base + u * stride + mine;
+            const bool in = p < a.pieces;
+            row[u] = static_cast<uint32_t>(static_cast<uint64_t>(p) * a.mul >> a.shift);
+            kb[u] = in ? static_cast<int>(p - row[u] * a.KB) : -1;
             int64_t src = row[u];
-            if (a.rows && in[u]) src = __ldg(a.rows + row[u]);
-            const bool ok = in[u] && src >= 0 && src < a.x_rows;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            const __nv_bfloat16 *p = a.x + src * a.ldx + col[u];
-            v[u] = ok ? __ldg(reinterpret_cast<const uint4 *>(p)) : zero;
-            if constexpr (GATED) up[u] = ok ? __ldg(reinterpret_cast<const uint4 *>(p + a.K)) : zero;
+            if (a.rows && in) src = __ldg(a.rows + row[u]);
+            const bool ok = in && src >= 0 && src < a.x_rows;
+            const __nv_bfloat16 *px = a.x + src * a.ldx + kb[u] * 128 + 8 * l;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool there = ok && kb[u] * 128 + 64 * j + 8 * l < a.K;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                v[u][j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + 64 * j)) : zero;
+                if constexpr (GATED) up[u][j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + a.K + 64 * j)) : zero;
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            float y[8];
-            float amax = 0.0f;
+            uint32_t w[2][4];
+            uint64_t y[2][4];
+            float amax;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[2 * j] = __uint_as_float(w[j] << 16);
-                y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            for (int j = 0; j < 2; ++j) {
+                w[j][0] = v[u][j].x;
+                w[j][1] = v[u][j].y;
+                w[j][2] = v[u][j].z;
+                w[j][3] = v[u][j].w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[j][i] = f32x2_pack(w[j][i] << 16, w[j][i] & 0xFFFF0000u);
             }
             if constexpr (GATED) {
-                const uint32_t h[4] = {up[u].x, up[u].y, up[u].z, up[u].w};
+                amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[2 * j] = silu_mul(y[2 * j], __uint_as_float(h[j] << 16));
-                    y[2 * j + 1] = silu_mul(y[2 * j + 1], __uint_as_float(h[j] & 0xFFFF0000u));
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t h[4] = {up[u][j].x, up[u][j].y, up[u][j].z, up[u][j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[j][i] = silu_mul2(y[j][i], f32x2_pack(h[i] << 16, h[i] & 0xFFFF0000u));
+                        uint32_t lo, hi;
+                        f32x2_unpack(y[j][i], lo, hi);
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(lo)), fabsf(__uint_as_float(hi))));
+                    }
+                }
+            } else {
+                uint32_t am2 = 0u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) am2 = absmax_bf16x2(am2, w[j][i]);
+                amax = fmaxf(__uint_as_float(am2 << 16), __uint_as_float(am2 & 0xFFFF0000u));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            float s, f;
+            uint2 codes[2];
+            if constexpr (GATED) {
+                const bool none = !(amax >= 0x1p-100f);   // below: the piece counts as all zero
+                s = block_scale(none ? 0.0f : amax);
+                if constexpr (POW2) s = pow2_up(s);
+                f = none ? 0.0f : POW2 ? __frcp_rn(s) : -__frcp_rn(s);
+                if (none) {
+                    codes[0] = codes[1] = make_uint2(0u, 0u);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) codes[j] = POW2 ? codes8_pow2(y[j], f) : codes8_f32(y[j], s, f);
+                }
+            } else if constexpr (POW2) {
+                s = pow2_up(block_scale(amax));
+                f = __uint_as_float(0x7F000000u - __float_as_uint(s));   // 1 / s
+#pragma unroll
+                for (int j = 0; j < 2; ++j) codes[j] = codes8_pow2(y[j], f);
+            } else {
+                s = block_scale(amax);
+                const bool recip = s >= 0x1p-100f && s <= 3.40282347e38f;
+                if (recip) {
+                    f = -__frcp_rn(s);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) codes[j] = codes8<true>(w[j], s, f);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) codes[j] = codes8<false>(w[j], s, 0.0f);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            if constexpr (GATED) {   // below the range of an exponential's fp32 precision: nothing
-                if (!(amax >= 0x1p-100f)) amax = 0.0f;
-                if (amax == 0.0f) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = 0.0f;
-                }
+            for (int j = 0; j < 2; ++j) {
+                const int col = kb[u] * 128 + 64 * j + 8 * l;
+                if (kb[u] >= 0 && col < a.K)
+                    *reinterpret_cast<uint2 *>(a.q + static_cast<int64_t>(row[u]) * a.K + col) = codes[j];
             }
-            float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-            if constexpr (POW2) s = pow2_up(s);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(y[j], s);
-            const uint2 codes = make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16,
-                                           e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
-            if (in[u]) {
-                *reinterpret_cast<uint2 *>(a.q + row[u] * a.K + col[u]) = codes;
-                if ((lane & 15) == 0) a.s[row[u] * a.KB + col[u] / 128] = s;
-            }
+            if (kb[u] >= 0 && l == 0) a.s[static_cast<int64_t>(row[u]) * a.KB + kb[u]] = s;
         }
     }
 }
