@@ -36,6 +36,13 @@ constexpr int T128_THREADS = 384;
 constexpr int T128_EPI_WARPS = 8;
 constexpr int T128_GROUP_M = 16;   // m-tiles per group of the tile order (L2 reuse)
 constexpr int T128_MAX_EXPERTS = 1024;
+// Registers per thread after the split: the launch holds 384 x 168 = 64512; the role
+// warpgroup keeps 128, the two epilogue warpgroups take 184 (128 x 128 + 256 x 184 =
+// 63488).  A thread holds 128 accumulators and 32 values of a partial: at 168 registers
+// (and with 96 / 200, where the compiler also spills) the K loop spilled, and 8192 x
+// 28672 x 8192 took 2423 us (1637 us); without spills 1550 us.
+constexpr int T128_ROLE_REGS = 128;
+constexpr int T128_EPI_REGS = 184;
 
 struct Tile128Args {
     CUtensorMap tmA, tmB;
@@ -123,6 +130,18 @@ __device__ __forceinline__ Tile128 tile128(const Tile128Args &a, const Ctl *ctl,
     return r;
 }
 
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -198,74 +217,78 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
     const int kb0 = static_cast<int>(static_cast<int64_t>(a.KB) * rank / ranks);
     const int kb1 = static_cast<int>(static_cast<int64_t>(a.KB) * (rank + 1) / ranks);
 
-    if (warp == 0) {
-        if (lane == 0) {
-            int it = 0, s = 0, withheld = -1;
-            uint32_t ph = 1;
-            bool ok = true;
-            for (int t = unit; t < tiles && ok; t += units) {
-                const Tile128 tt = tile128<BN>(a, ctl, t);
-                const int brow = tt.e * a.N + tt.n0;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = wait128(&ctl->empty[s], ph, ctl, a);
-                    if (!ok) break;
-                    if (it == a.withhold && blockIdx.x == 0) {
-                        withheld = s;
-                    } else {
-                        mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + C::B_BYTES);
-                        tma_load_2d(&a.tmA, &ctl->full[s], sm_a + s * C::A_BYTES, kb * 128, tt.m0);
-                        tma_load_2d(&a.tmB, &ctl->full[s], sm_b + s * C::B_BYTES, kb * 128, brow);
-                    }
-                    ++it;
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        ph ^= 1u;
+    if (warp < 4) {
+        setmaxnreg_dec<T128_ROLE_REGS>();
+        if (warp == 0) {
+            if (lane == 0) {
+                int it = 0, s = 0, withheld = -1;
+                uint32_t ph = 1;
+                bool ok = true;
+                for (int t = unit; t < tiles && ok; t += units) {
+                    const Tile128 tt = tile128<BN>(a, ctl, t);
+                    const int brow = tt.e * a.N + tt.n0;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        ok = wait128(&ctl->empty[s], ph, ctl, a);
+                        if (!ok) break;
+                        if (it == a.withhold && blockIdx.x == 0) {
+                            withheld = s;
+                        } else {
+                            mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + C::B_BYTES);
+                            tma_load_2d(&a.tmA, &ctl->full[s], sm_a + s * C::A_BYTES, kb * 128, tt.m0);
+                            tma_load_2d(&a.tmB, &ctl->full[s], sm_b + s * C::B_BYTES, kb * 128, brow);
+                        }
+                        ++it;
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
+                // no load is in flight when the CTA leaves
+                for (int d = max(0, it - C::STAGES); d < it; ++d) {
+                    if (d % C::STAGES == withheld) continue;
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(&ctl->full[d % C::STAGES], static_cast<uint32_t>(d / C::STAGES) & 1u))
+                        if (clock64() - t0 > a.wait_limit) break;
+                }
             }
-            // no load is in flight when the CTA leaves
-            for (int d = max(0, it - C::STAGES); d < it; ++d) {
-                if (d % C::STAGES == withheld) continue;
+        } else if (warp == 1) {
+            if (lane == 0) {
+                constexpr uint32_t idesc = idesc_f8f6f4(T128_BM, BN);
+                int s = 0, b = 0;
+                uint32_t ph = 0, bph = 1;
+                bool ok = true;
+                for (int t = unit; t < tiles && ok; t += units) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        ok = wait128(&ctl->tempty[b], bph, ctl, a) && wait128(&ctl->full[s], ph, ctl, a);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t ad = sdesc_k_sw128(smem_u32(sm_a + s * C::A_BYTES));
+                        const uint64_t bd = sdesc_k_sw128(smem_u32(sm_b + s * C::B_BYTES));
+                        const uint32_t d = tmem + b * BN;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_f8(d, ad + 2 * i, bd + 2 * i, idesc, i > 0);
+                        mma_commit(&ctl->empty[s]);
+                        mma_commit(&ctl->tfull[b]);
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                        if (++b == C::BUFS) {
+                            b = 0;
+                            bph ^= 1u;
+                        }
+                    }
+                }
+                // all MMAs have completed before tensor memory is freed
+                mma_commit(&ctl->drain);
                 const long long t0 = clock64();
-                while (!mbar_try_wait(&ctl->full[d % C::STAGES], static_cast<uint32_t>(d / C::STAGES) & 1u))
+                while (!mbar_try_wait(&ctl->drain, 0))
                     if (clock64() - t0 > a.wait_limit) break;
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f8f6f4(T128_BM, BN);
-            int s = 0, b = 0;
-            uint32_t ph = 0, bph = 1;
-            bool ok = true;
-            for (int t = unit; t < tiles && ok; t += units) {
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = wait128(&ctl->tempty[b], bph, ctl, a) && wait128(&ctl->full[s], ph, ctl, a);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t ad = sdesc_k_sw128(smem_u32(sm_a + s * C::A_BYTES));
-                    const uint64_t bd = sdesc_k_sw128(smem_u32(sm_b + s * C::B_BYTES));
-                    const uint32_t d = tmem + b * BN;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_f8(d, ad + 2 * i, bd + 2 * i, idesc, i > 0);
-                    mma_commit(&ctl->empty[s]);
-                    mma_commit(&ctl->tfull[b]);
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                    if (++b == C::BUFS) {
-                        b = 0;
-                        bph ^= 1u;
-                    }
-                }
-            }
-            // all MMAs have completed before tensor memory is freed
-            mma_commit(&ctl->drain);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&ctl->drain, 0))
-                if (clock64() - t0 > a.wait_limit) break;
-        }
-    } else if (warp >= 4) {
+    } else {
+        setmaxnreg_inc<T128_EPI_REGS>();
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int r = q * 32 + lane;   // row of the tile
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::COLS;
@@ -279,9 +302,9 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             const int nb = min((tt.n0 + h * C::COLS) / 128, a.NB - 1);
             const float *psa = a.sA + static_cast<int64_t>(m) * a.KB;
             const float *psb = a.sB + (static_cast<int64_t>(tt.e) * a.NB + nb) * a.KB;
-            float acc[C::COLS];
+            uint64_t acc[C::COLS / 2];   // pairs of columns
 #pragma unroll
-            for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+            for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0ull;
             float sa = 0.0f, sb = 0.0f;
             if (kb0 < kb1) {
                 sa = __ldg(psa + kb0);
@@ -307,14 +330,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                         if (lane == 0) mbar_arrive(&ctl->tempty[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        uint64_t v = f32x2_pack(__float_as_uint(acc[32 * x + 2 * j]), __float_as_uint(acc[32 * x + 2 * j + 1]));
-                        fma_f32x2(v, f32x2_pack(p[2 * j], p[2 * j + 1]), s2);
-                        uint32_t lo, hi;
-                        f32x2_unpack(v, lo, hi);
-                        acc[32 * x + 2 * j] = __uint_as_float(lo);
-                        acc[32 * x + 2 * j + 1] = __uint_as_float(hi);
-                    }
+                    for (int j = 0; j < 16; ++j) fma_f32x2(acc[16 * x + j], f32x2_pack(p[2 * j], p[2 * j + 1]), s2);
                 }
                 if (++b == C::BUFS) {
                     b = 0;
@@ -331,7 +347,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
 #pragma unroll
                 for (int j = 0; j < C::COLS / 4; ++j)
                     red[r * (BN / 4) + ((h * (C::COLS / 4) + j) ^ (r & 7))] =
-                        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+                        make_float4(f32x2_lo(acc[2 * j]), f32x2_hi(acc[2 * j]), f32x2_lo(acc[2 * j + 1]),
+                                    f32x2_hi(acc[2 * j + 1]));
             } else {
 #pragma unroll
                 for (int x = 0; x < C::COLS / 32; ++x) {
@@ -342,8 +359,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[32 * x + 8 * c + 2 * j],
-                                                                          acc[32 * x + 8 * c + 2 * j + 1]);
+                            const uint64_t p = acc[16 * x + 4 * c + j];
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(f32x2_lo(p), f32x2_hi(p));
                             w[j] = *reinterpret_cast<const uint32_t *>(&v);
                         }
                         row[c ^ ((lane >> 1) & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
