@@ -59,10 +59,10 @@ int check_product(const void *A, const float *sA, const void *B, const float *sB
     return FP8_OK;
 }
 
-template <int NT, int U>
+template <int NT, int U, int WARPS, int CTAS>
 int launch_rows(const RowsArgs &a, int64_t groups, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.N + ROWS_N - 1) / ROWS_N), static_cast<unsigned>(groups));
-    bsfp8_block128_rows<NT, U><<<grid, ROWS_WARPS * 32, 0, stream>>>(a);
+    bsfp8_block128_rows<NT, U, WARPS, CTAS><<<grid, WARPS * 32, 0, stream>>>(a);
     return launched();
 }
 
@@ -129,7 +129,7 @@ int launch_tile(const RowsArgs &r, int split, DeviceState *d, cudaStream_t strea
 // GPU, else of 128 x 128 with K split over clusters.
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode != FP8_PATH_AUTO;
-    if (!pinned && a.M <= 8) return launch_rows<1, 4>(a, 1, stream);
+    if (!pinned && a.M <= 8) return launch_rows<1, 2, 8, 3>(a, 1, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
     if (wide >= d->sm_count) return launch_tile<256, false>(a, 1, d, stream);
@@ -143,7 +143,7 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
 // rows each: the rows form; else tiles, 256 columns wide where there are enough.
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     if (mode == FP8_PATH_AUTO && a.M <= 4 * static_cast<int64_t>(a.E))
-        return launch_rows<1, 4>(a, a.M < a.E ? a.M : a.E, stream);
+        return launch_rows<1, 2, 4, 8>(a, a.M < a.E ? a.M : a.E, stream);
     const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
     if (most * ((a.N + 255) / 256) >= 4 * d->sm_count) return launch_tile<256, false>(a, 1, d, stream);
     return launch_tile<128, false>(a, 1, d, stream);

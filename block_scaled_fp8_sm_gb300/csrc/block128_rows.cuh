@@ -8,8 +8,14 @@
 // loads 16-byte pieces of B (and of the tokens) straight into registers, which
 // are the operands of mma.m16n8k32 (B's 16 rows as its M side, 8 tokens as its
 // N side).  The products of a 128-K block are summed by four MMAs from zero in
-// fp32, then acc += (sA sB) * sum in fp32; the eight warps' sums are added in
+// fp32, then acc += (sA sB) * sum in fp32; the warps' sums are added in
 // warp order.  A row's bits do not depend on the other rows.
+//
+// One product has few CTAs (256 for 4096 columns): eight warps each, U = 2 blocks loaded
+// ahead, three CTAs on an SM (1 x 4096 x 7168: 6.1 us; U = 4, two CTAs 6.3; four warps,
+// eight CTAs 8.2).  Experts have many: four warps, eight CTAs on an SM, whose loads
+// cover one another's starts and sums (24 rows over 22 of 64 experts of 4096 x 7168:
+// 89 us; eight warps and three CTAs 97; U = 4, two CTAs 110).
 //
 // The K order inside a block is permuted alike on both sides: lane t of a
 // quad holds bytes 64 j + 16 t .. + 15 (j = 0, 1), so a load of a warp covers 64
@@ -33,7 +39,6 @@ struct RowsArgs {
     int M, N, K, KB, E;
 };
 
-constexpr int ROWS_WARPS = 8;
 constexpr int ROWS_N = 16;   // rows of B per CTA
 
 __device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -86,10 +91,10 @@ __device__ __forceinline__ int busy_expert(const int32_t *offsets, int E, int T,
     return *found;
 }
 
-template <int NT, int U>
-__global__ void __launch_bounds__(ROWS_WARPS * 32, 2) bsfp8_block128_rows(const RowsArgs a) {
-    __shared__ float red[ROWS_WARPS][NT][4][32];
-    __shared__ int counts[ROWS_WARPS];
+template <int NT, int U, int WARPS, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const RowsArgs a) {
+    __shared__ float red[WARPS][NT][4][32];
+    __shared__ int counts[WARPS];
     __shared__ int found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = static_cast<int>(blockIdx.x) * ROWS_N;
@@ -113,13 +118,13 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, 2) bsfp8_block128_rows(const 
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][c] = 0.0f;
-        for (int kb0 = warp; kb0 < a.KB; kb0 += ROWS_WARPS * U) {
+        for (int kb0 = warp; kb0 < a.KB; kb0 += WARPS * U) {
             uint4 w0[U][2], w1[U][2], x[U][NT][2];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int k = (kb0 + u * ROWS_WARPS) * 128 + 64 * j;   // sizes are below 2^30: no overflow
+                    const int k = (kb0 + u * WARPS) * 128 + 64 * j;   // sizes are below 2^30: no overflow
                     const bool in = k + 16 * t < a.K;
                     w0[u][j] = ldg16_if(B0 + k, in);
                     w1[u][j] = ldg16_if(B1 + k, in && ok1);
@@ -130,13 +135,13 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, 2) bsfp8_block128_rows(const 
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int k = (kb0 + u * ROWS_WARPS) * 128 + 64 * j + 16 * t;
+                        const int k = (kb0 + u * WARPS) * 128 + 64 * j + 16 * t;
                         const int m = m0 + 8 * n + g;
                         x[u][n][j] = ldg16_if(a.A + static_cast<int64_t>(m) * a.K + k, m < hi && k < a.K);
                     }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int kb = kb0 + u * ROWS_WARPS;
+                const int kb = kb0 + u * WARPS;
                 if (kb < a.KB) {
                     const float sb = __ldg(sB + kb);
 #pragma unroll
@@ -165,12 +170,12 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, 2) bsfp8_block128_rows(const 
             for (int c = 0; c < 4; ++c) red[warp][n][c][lane] = acc[n][c];
         __syncthreads();
         // output i: row r of the 16, token j of the 8 NT
-        for (int i = threadIdx.x; i < NT * 128; i += ROWS_WARPS * 32) {
+        for (int i = threadIdx.x; i < NT * 128; i += WARPS * 32) {
             const int r = i & 15, j = i >> 4, n = j >> 3, tok = j & 7;
             const int c = (r >> 3) * 2 + (tok & 1), l = (r & 7) * 4 + (tok >> 1);
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < ROWS_WARPS; ++w) v += red[w][n][c][l];
+            for (int w = 0; w < WARPS; ++w) v += red[w][n][c][l];
             if (m0 + j < hi && n0 + r < a.N)
                 a.C[static_cast<int64_t>(m0 + j) * a.N + n0 + r] = __float2bfloat16_rn(v);
         }
