@@ -37,12 +37,12 @@ constexpr int T128_EPI_WARPS = 8;
 constexpr int T128_GROUP_M = 16;   // m-tiles per group of the tile order (L2 reuse)
 constexpr int T128_MAX_EXPERTS = 1024;
 // Registers per thread after the split: the launch holds 384 x 168 = 64512; the role
-// warpgroup keeps 128, the two epilogue warpgroups take 184 (128 x 128 + 256 x 184 =
-// 63488).  A thread holds 128 accumulators and 32 values of a partial: at 168 registers
-// (and with 96 / 200, where the compiler also spills) the K loop spilled, and 8192 x
-// 28672 x 8192 took 2423 us (1637 us); without spills 1550 us.
-constexpr int T128_ROLE_REGS = 128;
-constexpr int T128_EPI_REGS = 184;
+// warpgroup keeps 80, the two epilogue warpgroups take 208 (128 x 80 + 256 x 208 =
+// 63488): a thread holds 128 sums and 16 values of a partial.  At 168 the K loop spilled
+// and 8192 x 28672 x 8192 took 2423 us, now 1445 us.  Scalar FMAs: packed pairs
+// (fma.rn.f32x2) need the partial's values moved into aligned pairs first (1500 us).
+constexpr int T128_ROLE_REGS = 80;
+constexpr int T128_EPI_REGS = 208;
 
 struct Tile128Args {
     CUtensorMap tmA, tmB;
@@ -139,8 +139,14 @@ __device__ __forceinline__ void setmaxnreg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+// One lane of a converged warp.  The role of a single thread is chosen this way and not
+// by lane == 0: the compiler then knows that one thread runs it, and issues the tcgen05
+// and TMA instructions without a loop over the active lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
 
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
     float v;
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
     if (warp < 4) {
         setmaxnreg_dec<T128_ROLE_REGS>();
         if (warp == 0) {
-            if (lane == 0) {
+            if (elect_one()) {
                 int it = 0, s = 0, withheld = -1;
                 uint32_t ph = 1;
                 bool ok = true;
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0) {
+            if (elect_one()) {
                 constexpr uint32_t idesc = idesc_f8f6f4(T128_BM, BN);
                 int s = 0, b = 0;
                 uint32_t ph = 0, bph = 1;
@@ -302,9 +308,9 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             const int nb = min((tt.n0 + h * C::COLS) / 128, a.NB - 1);
             const float *psa = a.sA + static_cast<int64_t>(m) * a.KB;
             const float *psb = a.sB + (static_cast<int64_t>(tt.e) * a.NB + nb) * a.KB;
-            uint64_t acc[C::COLS / 2];   // pairs of columns
+            float acc[C::COLS];
 #pragma unroll
-            for (int j = 0; j < C::COLS / 2; ++j) acc[j] = 0ull;
+            for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
             float sa = 0.0f, sb = 0.0f;
             if (kb0 < kb1) {
                 sa = __ldg(psa + kb0);
@@ -315,22 +321,21 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 const int next = min(kb + 1, kb1 - 1);
                 sa = __ldg(psa + next);
                 sb = __ldg(psb + next);
-                const uint64_t s2 = f32x2_pack(__float_as_uint(sc), __float_as_uint(sc));
                 ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->tfull[b], bph, ctl, a));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int x = 0; x < C::COLS / 32; ++x) {
-                    uint32_t p[32];
-                    tmem_ld_x32(taddr + b * BN + 32 * x, p);
+                for (int x = 0; x < C::COLS / 16; ++x) {
+                    uint32_t p[16];
+                    tmem_ld_x16(taddr + b * BN + 16 * x, p);
                     tmem_ld_wait();
-                    if (x == C::COLS / 32 - 1) {   // the partial is in registers
+                    if (x == C::COLS / 16 - 1) {   // the partial is in registers
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ctl->tempty[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma_f32x2(acc[16 * x + j], f32x2_pack(p[2 * j], p[2 * j + 1]), s2);
+                    for (int j = 0; j < 16; ++j) acc[16 * x + j] = fmaf(__uint_as_float(p[j]), sc, acc[16 * x + j]);
                 }
                 if (++b == C::BUFS) {
                     b = 0;
@@ -347,8 +352,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
 #pragma unroll
                 for (int j = 0; j < C::COLS / 4; ++j)
                     red[r * (BN / 4) + ((h * (C::COLS / 4) + j) ^ (r & 7))] =
-                        make_float4(f32x2_lo(acc[2 * j]), f32x2_hi(acc[2 * j]), f32x2_lo(acc[2 * j + 1]),
-                                    f32x2_hi(acc[2 * j + 1]));
+                        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
             } else {
 #pragma unroll
                 for (int x = 0; x < C::COLS / 32; ++x) {
@@ -359,8 +363,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint64_t p = acc[16 * x + 4 * c + j];
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(f32x2_lo(p), f32x2_hi(p));
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[32 * x + 8 * c + 2 * j],
+                                                                          acc[32 * x + 8 * c + 2 * j + 1]);
                             w[j] = *reinterpret_cast<const uint32_t *>(&v);
                         }
                         row[c ^ ((lane >> 1) & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
