@@ -81,11 +81,14 @@ RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *s
     return a;
 }
 
+// `tiles`: how many there are, or, for experts, can be.
 template <int BN, bool SPLIT>
-int launch_tile(const RowsArgs &r, int split, DeviceState *d, cudaStream_t stream) {
+int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cudaStream_t stream) {
     Tile128Args a{};
     const int64_t brows = static_cast<int64_t>(r.N) * (r.offsets ? r.E : 1);
     int rc = encode_kmajor(&a.tmA, r.A, r.M, r.K, T128_BM);
+    if (rc != FP8_OK) return rc;
+    rc = encode_kmajor(&a.tmA32, r.A, r.M, r.K, 32);
     if (rc != FP8_OK) return rc;
     rc = encode_kmajor(&a.tmB, r.B, brows, r.K, BN);
     if (rc != FP8_OK) return rc;
@@ -110,7 +113,7 @@ int launch_tile(const RowsArgs &r, int split, DeviceState *d, cudaStream_t strea
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = static_cast<unsigned>(split);
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(a.mt * a.nt * split));
+        cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
         cfg.blockDim = dim3(T128_THREADS);
         cfg.dynamicSmemBytes = smem128<BN>();
         cfg.stream = stream;
@@ -118,35 +121,46 @@ int launch_tile(const RowsArgs &r, int split, DeviceState *d, cudaStream_t strea
         cfg.numAttrs = 1;
         return cudaLaunchKernelEx(&cfg, bsfp8_block128_tile<BN, true>, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
     } else {
-        const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt;
-        const unsigned grid = static_cast<unsigned>(!r.offsets && tiles < d->sm_count ? tiles : d->sm_count);
+        const unsigned grid = static_cast<unsigned>(tiles < d->sm_count ? tiles : d->sm_count);
         bsfp8_block128_tile<BN, false><<<grid, T128_THREADS, smem128<BN>(), stream>>>(a);
         return launched();
     }
 }
 
-// The form of one product: rows (M <= 8), or tiles of 128 x 256 where they fill the
-// GPU, else of 128 x 128 with K split over clusters.
+// CTAs that share a tile's K: as many as the GPU still has room for, four K blocks
+// each at least.
+int split_of(int64_t tiles, int KB, int sms) {
+    int split = 1;
+    while (split < T128_MAX_SPLIT && tiles * split * 2 <= sms && KB >= split * 8) split *= 2;
+    return split;
+}
+
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode != FP8_PATH_AUTO;
     if (!pinned && a.M <= 8) return launch_rows<1, 2, 8, 3>(a, 1, stream);
+    const int64_t groups = (a.M + 15) / 16;
+    if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
+        return launch_rows<2, 1, 8, 3>(a, groups, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
-    if (wide >= d->sm_count) return launch_tile<256, false>(a, 1, d, stream);
-    int split = 1;
-    while (!pinned && split < 8 && narrow * split * 2 <= d->sm_count && a.KB >= split * 4) split *= 2;
-    if (split > 1) return launch_tile<128, true>(a, split, d, stream);
-    return launch_tile<128, false>(a, 1, d, stream);
+    if (wide >= d->sm_count) return launch_tile<256, false>(a, 1, 1, d, stream);
+    const int split = pinned ? 1 : split_of(narrow, a.KB, d->sm_count);
+    if (split > 1) return launch_tile<128, true>(a, narrow, split, d, stream);
+    return launch_tile<128, false>(a, narrow, 1, d, stream);
 }
 
-// Experts: the row counts are on the device, so the rule goes by the average.  A few
-// rows each: the rows form; else tiles, 256 columns wide where there are enough.
+// Experts: the row counts are on the device, so the rule goes by what is possible: at
+// most min(E, T) + T / 128 row tiles.
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
-    if (mode == FP8_PATH_AUTO && a.M <= 4 * static_cast<int64_t>(a.E))
+    const bool pinned = mode != FP8_PATH_AUTO;
+    if (!pinned && a.M <= 4 * static_cast<int64_t>(a.E))
         return launch_rows<1, 2, 4, 8>(a, a.M < a.E ? a.M : a.E, stream);
     const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
-    if (most * ((a.N + 255) / 256) >= 4 * d->sm_count) return launch_tile<256, false>(a, 1, d, stream);
-    return launch_tile<128, false>(a, 1, d, stream);
+    const int64_t wide = most * ((a.N + 255) / 256), narrow = most * ((a.N + 127) / 128);
+    if (wide >= d->sm_count) return launch_tile<256, false>(a, wide, 1, d, stream);
+    const int split = pinned ? 1 : split_of(narrow, a.KB, d->sm_count);
+    if (split > 1) return launch_tile<128, true>(a, narrow, split, d, stream);
+    return launch_tile<128, false>(a, narrow, 1, d, stream);
 }
 
 template <bool GATED>

@@ -36,6 +36,7 @@ constexpr int T128_THREADS = 384;
 constexpr int T128_EPI_WARPS = 8;
 constexpr int T128_GROUP_M = 16;   // m-tiles per group of the tile order (L2 reuse)
 constexpr int T128_MAX_EXPERTS = 1024;
+constexpr int T128_MAX_SPLIT = 4;   // CTAs of a cluster
 // Registers per thread after the split: the launch holds 384 x 168 = 64512; the role
 // warpgroup keeps 80, the two epilogue warpgroups take 208 (128 x 80 + 256 x 208 =
 // 63488): a thread holds 128 sums and 16 values of a partial.  At 168 the K loop spilled
@@ -45,7 +46,7 @@ constexpr int T128_ROLE_REGS = 80;
 constexpr int T128_EPI_REGS = 208;
 
 struct Tile128Args {
-    CUtensorMap tmA, tmB;
+    CUtensorMap tmA, tmA32, tmB;   // A in boxes of 128 rows and of 32
     const float *sA, *sB;
     __nv_bfloat16 *C;
     const int32_t *offsets;   // [E + 1], or null: one product
@@ -148,9 +149,14 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0u;
 }
 
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+// 16 bytes at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank));
     return v;
 }
 
@@ -182,6 +188,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         ctl->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&a.tmA);
+        tma_prefetch_desc(&a.tmA32);
         tma_prefetch_desc(&a.tmB);
     }
     if (warp == 1) {
@@ -233,14 +240,24 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 for (int t = unit; t < tiles && ok; t += units) {
                     const Tile128 tt = tile128<BN>(a, ctl, t);
                     const int brow = tt.e * a.N + tt.n0;
+                    // up to 64 rows come as boxes of 32: what a tile does not have is
+                    // not fetched (those rows of the slot keep old bytes, which feed
+                    // only sums that are never stored).  More would cost more requests
+                    // than one box of 128.
+                    const int rows = tt.hi - tt.m0, small = rows <= 64 ? (rows + 31) / 32 : 0;
+                    const uint32_t bytes = (small ? small * 4096 : C::A_BYTES) + C::B_BYTES;
                     for (int kb = kb0; kb < kb1; ++kb) {
                         ok = wait128(&ctl->empty[s], ph, ctl, a);
                         if (!ok) break;
                         if (it == a.withhold && blockIdx.x == 0) {
                             withheld = s;
                         } else {
-                            mbar_arrive_expect_tx(&ctl->full[s], C::A_BYTES + C::B_BYTES);
-                            tma_load_2d(&a.tmA, &ctl->full[s], sm_a + s * C::A_BYTES, kb * 128, tt.m0);
+                            mbar_arrive_expect_tx(&ctl->full[s], bytes);
+                            if (small == 0)
+                                tma_load_2d(&a.tmA, &ctl->full[s], sm_a + s * C::A_BYTES, kb * 128, tt.m0);
+                            for (int i = 0; i < small; ++i)
+                                tma_load_2d(&a.tmA32, &ctl->full[s], sm_a + s * C::A_BYTES + i * 4096, kb * 128,
+                                            tt.m0 + i * 32);
                             tma_load_2d(&a.tmB, &ctl->full[s], sm_b + s * C::B_BYTES, kb * 128, brow);
                         }
                         ++it;
@@ -390,22 +407,30 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         cluster_sync();   // every CTA's partial sums are in its shared memory
         if (unit < tiles) {
             const Tile128 tt = tile128<BN>(a, ctl, unit);
-            const int rows = T128_BM / static_cast<int>(ranks), r0 = static_cast<int>(rank) * rows;
             const uint32_t base = smem_u32(smem);
-            // pairs of columns of this CTA's share of the rows
-            for (int i = threadIdx.x; i < rows * (BN / 2); i += T128_THREADS) {
-                const int r = r0 + i / (BN / 2), c = (i % (BN / 2)) * 2;
-                const uint32_t off = static_cast<uint32_t>(r * BN + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3))) * 4u;
-                if (tt.m0 + r >= tt.hi || tt.n0 + c >= a.N) continue;
-                float v0 = 0.0f, v1 = 0.0f;
-                for (uint32_t k = 0; k < ranks; ++k) {
-                    uint32_t peer;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(base + off), "r"(k));
-                    v0 += ld_dsmem_f32(peer);
-                    v1 += ld_dsmem_f32(peer + 4u);
+            // the rows that exist, four columns a thread, shared out evenly; all
+            // ranks' pieces are in flight before the first is added
+            const int pieces = min(T128_BM, tt.hi - tt.m0) * (BN / 4);
+            const int per = (pieces + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
+            const int end = min(pieces, (static_cast<int>(rank) + 1) * per);
+            for (int i = static_cast<int>(rank) * per + threadIdx.x; i < end; i += T128_THREADS) {
+                const int r = i / (BN / 4), c = i % (BN / 4);
+                const uint32_t off = static_cast<uint32_t>(r * (BN / 4) + (c ^ (r & 7))) * 16u;
+                float4 v[T128_MAX_SPLIT];
+#pragma unroll
+                for (uint32_t k = 0; k < T128_MAX_SPLIT; ++k)
+                    v[k] = k < ranks ? ld_dsmem_f32x4(base + off, k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (uint32_t k = 1; k < T128_MAX_SPLIT; ++k) {
+                    v[0].x += v[k].x;
+                    v[0].y += v[k].y;
+                    v[0].z += v[k].z;
+                    v[0].w += v[k].w;
                 }
-                *reinterpret_cast<__nv_bfloat162 *>(a.C + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0 + c) =
-                    __floats2bfloat162_rn(v0, v1);
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0].x, v[0].y), hi = __floats2bfloat162_rn(v[0].z, v[0].w);
+                if (tt.n0 + 4 * c < a.N)
+                    *reinterpret_cast<uint2 *>(a.C + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0 + 4 * c) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             }
         }
         cluster_sync();   // no CTA leaves while a peer reads its shared memory
