@@ -172,17 +172,15 @@ def fp8_quantize_blocks(x, q=None, s=None, stream=None):
     return q, s
 
 
-def _want(ok, what):
-    if not ok:
-        raise ValueError(what)
+# The 128-granular calls check what the C entry points cannot see (they get addresses and
+# sizes).  A call of a few microseconds is bound by this marshalling: the checks are
+# written out, without helpers or tuples built per tensor.
 
-
-def _sized(what, *pairs):
-    """The C entry points see addresses only: a tensor of another element size is
-    refused here."""
-    for t, size in pairs:
+def _sizes_differ(what, *tensors):
+    for t, size in tensors:
         if t.element_size() != size:
-            raise ValueError(f"{what}: a tensor of type {t.dtype} where {size}-byte elements are expected")
+            return f"{what}: a tensor of type {t.dtype} where {size}-byte elements are expected"
+    return f"{what}: tensors must be contiguous"
 
 
 def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
@@ -191,17 +189,19 @@ def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
     values), B [N,K] codes with sB [ceil(N/128), ceil(K/128)] (128 x 128 blocks).
     Codes are uint8 or float8_e4m3fn; every tensor contiguous.  mode: None (AUTO),
     FP8_PATH_PROMOTE (each row's bits independent of M) or FP8_PATH_NATIVE
-    (power-of-two scales)."""
-    (M, K), N = A.shape, B.shape[0]
-    kb = (K + 127) // 128
-    _want(B.shape == (N, K) and C.shape == (M, N) and sA.shape == (M, kb) and sB.shape == ((N + 127) // 128, kb),
-          "fp8_gemm_block128: shapes of A, sA, B, sB, C do not match")
-    _want(A.is_contiguous() and sA.is_contiguous() and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous(),
-          "fp8_gemm_block128: tensors must be contiguous")
-    _sized("fp8_gemm_block128", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2))
-    _check(library().fp8_gemm_block128_ex(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C), M, N, K,
-                                          FP8_PATH_AUTO if mode is None else int(mode), _stream(stream)),
-           "fp8_gemm_block128")
+    (power-of-two scales).  N a multiple of 8, K of 16."""
+    M, K = A.shape
+    N, kb = B.shape[0], (K + 127) // 128
+    if (B.shape != (N, K) or C.shape != (M, N) or sA.shape != (M, kb) or sB.shape != ((N + 127) // 128, kb)):
+        raise ValueError("fp8_gemm_block128: shapes of A, sA, B, sB, C do not match")
+    if not (A.element_size() == B.element_size() == 1 and sA.element_size() == sB.element_size() == 4
+            and C.element_size() == 2 and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous()
+            and sB.is_contiguous() and C.is_contiguous()):
+        raise ValueError(_sizes_differ("fp8_gemm_block128", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2)))
+    rc = library().fp8_gemm_block128_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), M, N,
+                                        K, FP8_PATH_AUTO if mode is None else mode, _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_gemm_block128")
     return C
 
 
@@ -211,29 +211,23 @@ def fp8_gemm_experts(A, sA, B, sB, C, offsets, stream=None, mode=None):
     C [T,N]; sA [T, ceil(K/128)], sB [E, ceil(N/128), ceil(K/128)], offsets an
     int32 CUDA tensor of E + 1 ascending row numbers, read on the device only.
     Experts without rows cost nothing; rows outside the table are not written."""
-    (T, K), (E, N) = A.shape, B.shape[:2]
+    T, K = A.shape
+    E, N = B.shape[:2]
     kb = (K + 127) // 128
-    _want(B.shape == (E, N, K) and C.shape == (T, N) and sA.shape == (T, kb)
-          and sB.shape == (E, (N + 127) // 128, kb) and offsets.shape == (E + 1,),
-          "fp8_gemm_experts: shapes of A, sA, B, sB, C, offsets do not match")
-    _want(A.is_contiguous() and sA.is_contiguous() and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous()
-          and offsets.is_contiguous(), "fp8_gemm_experts: tensors must be contiguous")
-    _sized("fp8_gemm_experts", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2), (offsets, 4))
-    _check(library().fp8_gemm_experts_ex(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C), _ptr(offsets), T, N, K, E,
-                                         FP8_PATH_AUTO if mode is None else int(mode), _stream(stream)),
-           "fp8_gemm_experts")
+    if (B.shape != (E, N, K) or C.shape != (T, N) or sA.shape != (T, kb)
+            or sB.shape != (E, (N + 127) // 128, kb) or offsets.shape != (E + 1,)):
+        raise ValueError("fp8_gemm_experts: shapes of A, sA, B, sB, C, offsets do not match")
+    if not (A.element_size() == B.element_size() == 1
+            and sA.element_size() == sB.element_size() == offsets.element_size() == 4 and C.element_size() == 2
+            and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous() and sB.is_contiguous()
+            and C.is_contiguous() and offsets.is_contiguous()):
+        raise ValueError(_sizes_differ("fp8_gemm_experts", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2), (offsets, 4)))
+    rc = library().fp8_gemm_experts_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(),
+                                       offsets.data_ptr(), T, N, K, E, FP8_PATH_AUTO if mode is None else mode,
+                                       _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_gemm_experts")
     return C
-
-
-def _token_operands(M, K, q, s, device, what):
-    kb = (K + 127) // 128
-    if q is None or s is None:
-        import torch
-        q = torch.empty(M, K, dtype=torch.uint8, device=device) if q is None else q
-        s = torch.empty(M, kb, dtype=torch.float32, device=device) if s is None else s
-    _want(q.shape == (M, K) and s.shape == (M, kb) and q.is_contiguous() and s.is_contiguous(),
-          what + ": q [M, K] and s [M, ceil(K/128)] must match and be contiguous")
-    return q, s
 
 
 def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
@@ -245,14 +239,20 @@ def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
     allocates them when not given."""
     R, K = x.shape
     M = R if rows is None else rows.shape[0]
-    _want(x.stride(1) == 1 or K <= 1, "fp8_quantize_tokens: the values of a row must be contiguous")
-    _want(rows is None or (rows.dim() == 1 and rows.is_contiguous()), "fp8_quantize_tokens: rows must be a contiguous vector")
-    q, s = _token_operands(M, K, q, s, x.device, "fp8_quantize_tokens")
-    _sized("fp8_quantize_tokens", (x, 2), (q, 1), (s, 4))
-    if rows is not None:
-        _sized("fp8_quantize_tokens", (rows, 4))
-    _check(library().fp8_quantize_tokens(_ptr(x), x.stride(0) if R > 1 else K, R, _ptr(rows), _ptr(q), _ptr(s), M, K,
-                                         FP8_QUANT_POW2 if pow2 else 0, _stream(stream)), "fp8_quantize_tokens")
+    if q is None or s is None:
+        q, s = _token_operands(M, K, q, s, x.device)
+    if q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
+        raise ValueError("fp8_quantize_tokens: q must be [M, K] and s [M, ceil(K/128)]")
+    if not (x.element_size() == 2 and q.element_size() == 1 and s.element_size() == 4 and q.is_contiguous()
+            and s.is_contiguous() and (x.stride(1) == 1 or K <= 1)):
+        raise ValueError(_sizes_differ("fp8_quantize_tokens", (x, 2), (q, 1), (s, 4)))
+    if rows is not None and not (rows.element_size() == 4 and rows.dim() == 1 and rows.is_contiguous()):
+        raise ValueError(_sizes_differ("fp8_quantize_tokens: rows (a vector)", (rows, 4)))
+    rc = library().fp8_quantize_tokens(x.data_ptr(), x.stride(0) if R > 1 else K, R,
+                                       None if rows is None else rows.data_ptr(), q.data_ptr(), s.data_ptr(), M, K,
+                                       FP8_QUANT_POW2 if pow2 else 0, _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_quantize_tokens")
     return q, s
 
 
@@ -260,14 +260,25 @@ def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
     """fp8_quantize_tokens of silu(gate) * up, with gate = x[:, :K] and
     up = x[:, K:] of bf16 x [M, 2K] (rows may be strided)."""
     M, K2 = x.shape
-    _want(K2 % 2 == 0, "fp8_swiglu_quantize_tokens: x holds gate and up side by side")
     K = K2 // 2
-    _want(x.stride(1) == 1 or K2 <= 1, "fp8_swiglu_quantize_tokens: the values of a row must be contiguous")
-    q, s = _token_operands(M, K, q, s, x.device, "fp8_swiglu_quantize_tokens")
-    _sized("fp8_swiglu_quantize_tokens", (x, 2), (q, 1), (s, 4))
-    _check(library().fp8_swiglu_quantize_tokens(_ptr(x), x.stride(0) if M > 1 else K2, _ptr(q), _ptr(s), M, K,
-                                                FP8_QUANT_POW2 if pow2 else 0, _stream(stream)),
-           "fp8_swiglu_quantize_tokens")
+    if q is None or s is None:
+        q, s = _token_operands(M, K, q, s, x.device)
+    if K2 % 2 or q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
+        raise ValueError("fp8_swiglu_quantize_tokens: x is [M, 2K], q [M, K] and s [M, ceil(K/128)]")
+    if not (x.element_size() == 2 and q.element_size() == 1 and s.element_size() == 4 and q.is_contiguous()
+            and s.is_contiguous() and (x.stride(1) == 1 or K2 <= 1)):
+        raise ValueError(_sizes_differ("fp8_swiglu_quantize_tokens", (x, 2), (q, 1), (s, 4)))
+    rc = library().fp8_swiglu_quantize_tokens(x.data_ptr(), x.stride(0) if M > 1 else K2, q.data_ptr(), s.data_ptr(),
+                                              M, K, FP8_QUANT_POW2 if pow2 else 0, _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_swiglu_quantize_tokens")
+    return q, s
+
+
+def _token_operands(M, K, q, s, device):
+    import torch
+    q = torch.empty(M, K, dtype=torch.uint8, device=device) if q is None else q
+    s = torch.empty(M, (K + 127) // 128, dtype=torch.float32, device=device) if s is None else s
     return q, s
 
 

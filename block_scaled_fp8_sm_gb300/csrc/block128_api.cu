@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "block128_rows.cuh"
+#include "block128_native.cuh"
 #include "block128_tile.cuh"
 #include "bsfp8.h"
 #include "host.h"
@@ -29,12 +30,14 @@ int block128_setup() {
     if (set_tile_attrs<256, false>() != FP8_OK || set_tile_attrs<128, false>() != FP8_OK ||
         set_tile_attrs<128, true>() != FP8_OK)
         return FP8_ERR_CUDA;
-    return FP8_OK;
+    return cudaFuncSetAttribute(bsfp8_block128_native, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_n128()) ==
+                   cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_CUDA;
 }
 
 namespace {
 
-constexpr int QTOK_U = 2;   // pieces a group of eight lanes loads ahead
 constexpr int64_t kLim = int64_t(1) << 30;   // 32-bit indices in the kernels keep room for a tile past the end
 
 int launched() { return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA; }
@@ -81,10 +84,7 @@ RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *s
     return a;
 }
 
-// `tiles`: how many there are, or, for experts, can be.
-template <int BN, bool SPLIT>
-int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cudaStream_t stream) {
-    Tile128Args a{};
+int tile_args(Tile128Args &a, const RowsArgs &r, int BN, DeviceState *d) {
     const int64_t brows = static_cast<int64_t>(r.N) * (r.offsets ? r.E : 1);
     int rc = encode_kmajor(&a.tmA, r.A, r.M, r.K, T128_BM);
     if (rc != FP8_OK) return rc;
@@ -107,6 +107,15 @@ int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cud
     a.E = r.E;
     a.mt = (r.M + T128_BM - 1) / T128_BM;
     a.nt = (r.N + BN - 1) / BN;
+    return FP8_OK;
+}
+
+// `tiles`: how many there are, or, for experts, can be.
+template <int BN, bool SPLIT>
+int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cudaStream_t stream) {
+    Tile128Args a{};
+    const int rc = tile_args(a, r, BN, d);
+    if (rc != FP8_OK) return rc;
     if constexpr (SPLIT) {   // one tile per cluster
         cudaLaunchConfig_t cfg{};
         cudaLaunchAttribute attr{};
@@ -127,6 +136,15 @@ int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cud
     }
 }
 
+int launch_native(const RowsArgs &r, int64_t tiles, DeviceState *d, cudaStream_t stream) {
+    Tile128Args a{};
+    const int rc = tile_args(a, r, N128_BN, d);
+    if (rc != FP8_OK) return rc;
+    const unsigned grid = static_cast<unsigned>(tiles < d->sm_count ? tiles : d->sm_count);
+    bsfp8_block128_native<<<grid, T128_THREADS, smem_n128(), stream>>>(a);
+    return launched();
+}
+
 // CTAs that share a tile's K: as many as the GPU still has room for, four K blocks
 // each at least.
 int split_of(int64_t tiles, int KB, int sms) {
@@ -136,14 +154,15 @@ int split_of(int64_t tiles, int KB, int sms) {
 }
 
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
-    const bool pinned = mode != FP8_PATH_AUTO;
+    const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 8) return launch_rows<1, 2, 8, 3>(a, 1, stream);
     const int64_t groups = (a.M + 15) / 16;
     if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
         return launch_rows<2, 1, 8, 3>(a, groups, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
-    if (wide >= d->sm_count) return launch_tile<256, false>(a, 1, 1, d, stream);
+    if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
+    if (wide >= d->sm_count) return launch_tile<256, false>(a, wide, 1, d, stream);
     const int split = pinned ? 1 : split_of(narrow, a.KB, d->sm_count);
     if (split > 1) return launch_tile<128, true>(a, narrow, split, d, stream);
     return launch_tile<128, false>(a, narrow, 1, d, stream);
@@ -152,11 +171,12 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
 // Experts: the row counts are on the device, so the rule goes by what is possible: at
 // most min(E, T) + T / 128 row tiles.
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
-    const bool pinned = mode != FP8_PATH_AUTO;
+    const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 4 * static_cast<int64_t>(a.E))
         return launch_rows<1, 2, 4, 8>(a, a.M < a.E ? a.M : a.E, stream);
     const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
     const int64_t wide = most * ((a.N + 255) / 256), narrow = most * ((a.N + 127) / 128);
+    if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
     if (wide >= d->sm_count) return launch_tile<256, false>(a, wide, 1, d, stream);
     const int split = pinned ? 1 : split_of(narrow, a.KB, d->sm_count);
     if (split > 1) return launch_tile<128, true>(a, narrow, split, d, stream);
@@ -197,12 +217,12 @@ int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, vo
         const int64_t n = M - m < step ? M - m : step;
         a.pieces = static_cast<uint32_t>(n * a.KB);
         const int64_t ctas = (n * a.KB + QTOK_GROUPS - 1) / QTOK_GROUPS;
-        const int64_t most = static_cast<int64_t>(d->sm_count) * 16;
+        const int64_t most = static_cast<int64_t>(d->sm_count) * 64;
         const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
         if (flags & FP8_QUANT_POW2)
-            bsfp8_quantize_tokens<GATED, true, QTOK_U><<<grid, QTOK_THREADS, 0, stream>>>(a);
+            bsfp8_quantize_tokens<GATED, true><<<grid, QTOK_THREADS, 0, stream>>>(a);
         else
-            bsfp8_quantize_tokens<GATED, false, QTOK_U><<<grid, QTOK_THREADS, 0, stream>>>(a);
+            bsfp8_quantize_tokens<GATED, false><<<grid, QTOK_THREADS, 0, stream>>>(a);
         if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
         if (rows) {
             a.rows += n;

@@ -46,7 +46,10 @@ constexpr int T128_ROLE_REGS = 80;
 constexpr int T128_EPI_REGS = 208;
 
 struct Tile128Args {
-    CUtensorMap tmA, tmA32, tmB;   // A in boxes of 128 rows and of 32
+    // A in boxes of 128 rows, and of 32 for tiles of up to 64 rows: what such a tile does
+    // not have is not fetched (those rows of the slot keep old bytes, which feed only
+    // sums that are never stored); more boxes would cost more requests than one of 128.
+    CUtensorMap tmA, tmA32, tmB;
     const float *sA, *sB;
     __nv_bfloat16 *C;
     const int32_t *offsets;   // [E + 1], or null: one product
@@ -160,6 +163,76 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 32 bf16 columns (16 words) of each lane's row to C, through the warp's 2 KB of staging:
+// eight rows of 64 contiguous bytes per store.  16-byte pieces are exchanged so that the
+// rows of a quarter-warp hit different banks.  q: the warp's quarter of the tile's rows.
+__device__ __forceinline__ void store_rows32(uint8_t *mine, const Tile128Args &a, const Tile128 &tt, int q, int col,
+                                             const uint32_t (&w)[16]) {
+    const int lane = threadIdx.x & 31;
+    uint4 *row = reinterpret_cast<uint4 *>(mine + lane * 64);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        row[c ^ ((lane >> 1) & 3)] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2), c = lane & 3;
+        const uint4 v = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+        const int mm = tt.m0 + q * 32 + rr;
+        if (mm < tt.hi && col + 8 * c < a.N)
+            *reinterpret_cast<uint4 *>(a.C + static_cast<int64_t>(mm) * a.N + col + 8 * c) = v;
+    }
+    __syncwarp();
+}
+
+// First tile of each expert (a running sum over one warp), or the tile count of one
+// product.  Reports an offset table that decreases or leaves [0, M].
+template <typename Ctl>
+__device__ __forceinline__ void count_tiles(const Tile128Args &a, Ctl *ctl) {
+    const int lane = threadIdx.x & 31;
+    if (!a.offsets) {
+        if (lane == 0) ctl->tiles = a.mt * a.nt;
+        return;
+    }
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < a.E) {
+            expert_rows(a.offsets, e, a.M, lo, hi);
+            if (blockIdx.x == 0 && (lo != __ldg(a.offsets + e) || hi != __ldg(a.offsets + e + 1) || hi < lo))
+                atomicOr(a.status, 4u);   // STATUS_RECORD
+        }
+        const int n = hi > lo ? (hi - lo + T128_BM - 1) / T128_BM * a.nt : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (e < a.E) ctl->start[e] = base + sum - n;
+        base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) ctl->start[a.E] = ctl->tiles = base;
+}
+
+// The producer's loads of one 128-K stage (see Tile128Args: boxes of A).
+template <int BN>
+__device__ __forceinline__ void load_stage(const Tile128Args &a, uint64_t *full, uint8_t *da, uint8_t *db,
+                                           const Tile128 &tt, int kb) {
+    using C = Cfg128<BN>;
+    const int rows = tt.hi - tt.m0, small = rows <= 64 ? (rows + 31) / 32 : 0;
+    mbar_arrive_expect_tx(full, (small ? small * 4096 : C::A_BYTES) + C::B_BYTES);
+    if (small == 0) tma_load_2d(&a.tmA, full, da, kb * 128, tt.m0);
+    for (int i = 0; i < small; ++i) tma_load_2d(&a.tmA32, full, da + i * 4096, kb * 128, tt.m0 + i * 32);
+    tma_load_2d(&a.tmB, full, db, kb * 128, tt.e * a.N + tt.n0);
+}
+
 template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __grid_constant__ Tile128Args a) {
     using C = Cfg128<BN>;
@@ -196,30 +269,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         tmem_relinquish();
     }
     if (warp == 2) {
-        if (a.offsets) {   // first tile of each expert: a running sum over the warp
-            int base = 0;
-            for (int e0 = 0; e0 < a.E; e0 += 32) {
-                const int e = e0 + lane;
-                int lo = 0, hi = 0;
-                if (e < a.E) {
-                    expert_rows(a.offsets, e, a.M, lo, hi);
-                    if (blockIdx.x == 0 && (lo != __ldg(a.offsets + e) || hi != __ldg(a.offsets + e + 1) || hi < lo))
-                        atomicOr(a.status, 4u);   // STATUS_RECORD
-                }
-                int n = hi > lo ? (hi - lo + T128_BM - 1) / T128_BM * a.nt : 0;
-                int sum = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                    if (lane >= o) sum += v;
-                }
-                if (e < a.E) ctl->start[e] = base + sum - n;
-                base += __shfl_sync(0xFFFFFFFFu, sum, 31);
-            }
-            if (lane == 0) ctl->start[a.E] = ctl->tiles = base;
-        } else if (lane == 0) {
-            ctl->tiles = a.mt * a.nt;
-        }
+        count_tiles(a, ctl);
     }
     tc_fence_before();
     __syncthreads();
@@ -239,26 +289,13 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 bool ok = true;
                 for (int t = unit; t < tiles && ok; t += units) {
                     const Tile128 tt = tile128<BN>(a, ctl, t);
-                    const int brow = tt.e * a.N + tt.n0;
-                    // up to 64 rows come as boxes of 32: what a tile does not have is
-                    // not fetched (those rows of the slot keep old bytes, which feed
-                    // only sums that are never stored).  More would cost more requests
-                    // than one box of 128.
-                    const int rows = tt.hi - tt.m0, small = rows <= 64 ? (rows + 31) / 32 : 0;
-                    const uint32_t bytes = (small ? small * 4096 : C::A_BYTES) + C::B_BYTES;
                     for (int kb = kb0; kb < kb1; ++kb) {
                         ok = wait128(&ctl->empty[s], ph, ctl, a);
                         if (!ok) break;
                         if (it == a.withhold && blockIdx.x == 0) {
                             withheld = s;
                         } else {
-                            mbar_arrive_expect_tx(&ctl->full[s], bytes);
-                            if (small == 0)
-                                tma_load_2d(&a.tmA, &ctl->full[s], sm_a + s * C::A_BYTES, kb * 128, tt.m0);
-                            for (int i = 0; i < small; ++i)
-                                tma_load_2d(&a.tmA32, &ctl->full[s], sm_a + s * C::A_BYTES + i * 4096, kb * 128,
-                                            tt.m0 + i * 32);
-                            tma_load_2d(&a.tmB, &ctl->full[s], sm_b + s * C::B_BYTES, kb * 128, brow);
+                            load_stage<BN>(a, &ctl->full[s], sm_a + s * C::A_BYTES, sm_b + s * C::B_BYTES, tt, kb);
                         }
                         ++it;
                         if (++s == C::STAGES) {
@@ -373,29 +410,10 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             } else {
 #pragma unroll
                 for (int x = 0; x < C::COLS / 32; ++x) {
-                    const int col = tt.n0 + h * C::COLS + 32 * x;
-                    uint4 *row = reinterpret_cast<uint4 *>(mine + lane * 64);
+                    uint32_t w[16];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[32 * x + 8 * c + 2 * j],
-                                                                          acc[32 * x + 8 * c + 2 * j + 1]);
-                            w[j] = *reinterpret_cast<const uint32_t *>(&v);
-                        }
-                        row[c ^ ((lane >> 1) & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // eight rows of 64 bytes per store
-                        const int rr = i * 8 + (lane >> 2), c = lane & 3;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-                        const int mm = tt.m0 + q * 32 + rr;
-                        if (mm < tt.hi && col + 8 * c < a.N)
-                            *reinterpret_cast<uint4 *>(a.C + static_cast<int64_t>(mm) * a.N + col + 8 * c) = v;
-                    }
-                    __syncwarp();
+                    for (int j = 0; j < 16; ++j) w[j] = bf16_pair(acc[32 * x + 2 * j], acc[32 * x + 2 * j + 1]);
+                    store_rows32(mine, a, tt, q, tt.n0 + h * C::COLS + 32 * x, w);
                 }
             }
         }

@@ -9,8 +9,10 @@
 // So eight lanes share a piece, sixteen values each (columns 8l .. 8l+7 and 64 + 8l ..
 // of the piece: every load of a warp is four runs of 128 bytes): the maximum takes
 // three shuffles for sixteen values.  The row of a piece comes from a multiplication
-// by the reciprocal of the pieces per row, and U pieces are loaded before the first
-// is converted.
+// by the reciprocal of the pieces per row.  Loads in flight come from resident warps (64
+// of them an SM, 48 where the arithmetic needs 40 registers) and not from pieces loaded ahead: 16384 x 7168 gathered 39 us,
+// plain 54.6 (53.3 at the measured copy bandwidth), gated 16001 x 4096 61.6; two pieces
+// ahead with fewer warps 41 / 57 / 65, four 43 / 56 / 82.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -111,109 +113,101 @@ __device__ __forceinline__ uint2 codes8_pow2(const uint64_t (&y)[4], float inv) 
     return pack_codes(v);
 }
 
-template <bool GATED, bool POW2, int U>
-__global__ void __launch_bounds__(QTOK_THREADS) bsfp8_quantize_tokens(const QuantTokensArgs a) {
+template <bool GATED, bool POW2>
+__global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_quantize_tokens(const QuantTokensArgs a) {
     const int l = threadIdx.x & 7;
     const uint32_t stride = gridDim.x * QTOK_GROUPS;
     // the whole warp stays in the loop together (shuffles): the bound is the warp's
     const uint32_t first = blockIdx.x * QTOK_GROUPS + (threadIdx.x >> 5) * 4, mine = (threadIdx.x >> 3) & 3;
-    for (uint32_t base = first; base < a.pieces; base += stride * U) {
-        uint4 v[U][2], up[GATED ? U : 1][2];
-        uint32_t row[U];
-        int kb[U];
+    for (uint32_t base = first; base < a.pieces; base += stride) {
+        uint4 v[2], up[2];
+        const uint32_t p = base + mine;
+        const bool in = p < a.pieces;
+        const uint32_t row = static_cast<uint32_t>(static_cast<uint64_t>(p) * a.mul >> a.shift);
+        const int kb = in ? static_cast<int>(p - row * a.KB) : -1;
+        int64_t src = row;
+        if (a.rows && in) src = __ldg(a.rows + row);
+        const bool ok = in && src >= 0 && src < a.x_rows;
+        const __nv_bfloat16 *px = a.x + src * a.ldx + kb * 128 + 8 * l;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t p = base + u * stride + mine;
-            const bool in = p < a.pieces;
-            row[u] = static_cast<uint32_t>(static_cast<uint64_t>(p) * a.mul >> a.shift);
-            kb[u] = in ? static_cast<int>(p - row[u] * a.KB) : -1;
-            int64_t src = row[u];
-            if (a.rows && in) src = __ldg(a.rows + row[u]);
-            const bool ok = in && src >= 0 && src < a.x_rows;
-            const __nv_bfloat16 *px = a.x + src * a.ldx + kb[u] * 128 + 8 * l;
+        for (int j = 0; j < 2; ++j) {
+            const bool there = ok && kb * 128 + 64 * j + 8 * l < a.K;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            v[j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + 64 * j)) : zero;
+            if constexpr (GATED) up[j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + a.K + 64 * j)) : zero;
+        }
+        uint32_t w[2][4];
+        uint64_t y[2][4];
+        float amax;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            w[j][0] = v[j].x;
+            w[j][1] = v[j].y;
+            w[j][2] = v[j].z;
+            w[j][3] = v[j].w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[j][i] = f32x2_pack(w[j][i] << 16, w[j][i] & 0xFFFF0000u);
+        }
+        if constexpr (GATED) {
+            amax = 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool there = ok && kb[u] * 128 + 64 * j + 8 * l < a.K;
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                v[u][j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + 64 * j)) : zero;
-                if constexpr (GATED) up[u][j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + a.K + 64 * j)) : zero;
+                const uint32_t h[4] = {up[j].x, up[j].y, up[j].z, up[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[j][i] = silu_mul2(y[j][i], f32x2_pack(h[i] << 16, h[i] & 0xFFFF0000u));
+                    uint32_t lo, hi;
+                    f32x2_unpack(y[j][i], lo, hi);
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(lo)), fabsf(__uint_as_float(hi))));
+                }
+            }
+        } else {
+            uint32_t am2 = 0u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) am2 = absmax_bf16x2(am2, w[j][i]);
+            amax = fmaxf(__uint_as_float(am2 << 16), __uint_as_float(am2 & 0xFFFF0000u));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        float s, f;
+        uint2 codes[2];
+        if constexpr (GATED) {
+            const bool none = !(amax >= 0x1p-100f);   // below: the piece counts as all zero
+            s = block_scale(none ? 0.0f : amax);
+            if constexpr (POW2) s = pow2_up(s);
+            f = none ? 0.0f : POW2 ? __frcp_rn(s) : -__frcp_rn(s);
+            if (none) {
+                codes[0] = codes[1] = make_uint2(0u, 0u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) codes[j] = POW2 ? codes8_pow2(y[j], f) : codes8_f32(y[j], s, f);
+            }
+        } else if constexpr (POW2) {
+            s = pow2_up(block_scale(amax));
+            f = __uint_as_float(0x7F000000u - __float_as_uint(s));   // 1 / s
+#pragma unroll
+            for (int j = 0; j < 2; ++j) codes[j] = codes8_pow2(y[j], f);
+        } else {
+            s = block_scale(amax);
+            const bool recip = s >= 0x1p-100f && s <= 3.40282347e38f;
+            if (recip) {
+                f = -__frcp_rn(s);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) codes[j] = codes8<true>(w[j], s, f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) codes[j] = codes8<false>(w[j], s, 0.0f);
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            uint32_t w[2][4];
-            uint64_t y[2][4];
-            float amax;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                w[j][0] = v[u][j].x;
-                w[j][1] = v[u][j].y;
-                w[j][2] = v[u][j].z;
-                w[j][3] = v[u][j].w;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[j][i] = f32x2_pack(w[j][i] << 16, w[j][i] & 0xFFFF0000u);
-            }
-            if constexpr (GATED) {
-                amax = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t h[4] = {up[u][j].x, up[u][j].y, up[u][j].z, up[u][j].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[j][i] = silu_mul2(y[j][i], f32x2_pack(h[i] << 16, h[i] & 0xFFFF0000u));
-                        uint32_t lo, hi;
-                        f32x2_unpack(y[j][i], lo, hi);
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(lo)), fabsf(__uint_as_float(hi))));
-                    }
-                }
-            } else {
-                uint32_t am2 = 0u;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) am2 = absmax_bf16x2(am2, w[j][i]);
-                amax = fmaxf(__uint_as_float(am2 << 16), __uint_as_float(am2 & 0xFFFF0000u));
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            float s, f;
-            uint2 codes[2];
-            if constexpr (GATED) {
-                const bool none = !(amax >= 0x1p-100f);   // below: the piece counts as all zero
-                s = block_scale(none ? 0.0f : amax);
-                if constexpr (POW2) s = pow2_up(s);
-                f = none ? 0.0f : POW2 ? __frcp_rn(s) : -__frcp_rn(s);
-                if (none) {
-                    codes[0] = codes[1] = make_uint2(0u, 0u);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) codes[j] = POW2 ? codes8_pow2(y[j], f) : codes8_f32(y[j], s, f);
-                }
-            } else if constexpr (POW2) {
-                s = pow2_up(block_scale(amax));
-                f = __uint_as_float(0x7F000000u - __float_as_uint(s));   // 1 / s
-#pragma unroll
-                for (int j = 0; j < 2; ++j) codes[j] = codes8_pow2(y[j], f);
-            } else {
-                s = block_scale(amax);
-                const bool recip = s >= 0x1p-100f && s <= 3.40282347e38f;
-                if (recip) {
-                    f = -__frcp_rn(s);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) codes[j] = codes8<true>(w[j], s, f);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) codes[j] = codes8<false>(w[j], s, 0.0f);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = kb[u] * 128 + 64 * j + 8 * l;
-                if (kb[u] >= 0 && col < a.K)
-                    *reinterpret_cast<uint2 *>(a.q + static_cast<int64_t>(row[u]) * a.K + col) = codes[j];
-            }
-            if (kb[u] >= 0 && l == 0) a.s[static_cast<int64_t>(row[u]) * a.KB + kb[u]] = s;
+        for (int j = 0; j < 2; ++j) {
+            const int col = kb * 128 + 64 * j + 8 * l;
+            if (kb >= 0 && col < a.K)
+                *reinterpret_cast<uint2 *>(a.q + static_cast<int64_t>(row) * a.K + col) = codes[j];
         }
+        if (kb >= 0 && l == 0) a.s[static_cast<int64_t>(row) * a.KB + kb] = s;
     }
 }
 

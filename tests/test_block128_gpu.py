@@ -34,6 +34,8 @@ SHAPES = [
     (1, 8, 16), (1, 4096, 7168), (2, 136, 144), (7, 24, 128), (8, 128, 256), (9, 256, 1040), (16, 264, 400),
     (31, 512, 512), (33, 1000, 272), (64, 256, 4096), (65, 128, 2064), (127, 8, 1024), (128, 384, 128), (129, 264, 1168),
     (200, 520, 640), (257, 1288, 912), (384, 256, 2048), (1000, 776, 528), (2049, 264, 272),
+    # enough tiles for the 256-column kernels: every CTA several, ragged on both sides
+    (3333, 1800, 400), (5001, 1032, 2064), (19999, 136, 272), (9800, 520, 16), (2500, 2568, 1168),
 ]
 
 
@@ -49,6 +51,65 @@ def test_product(bs, M, N, K, mode):
     assert torch.all(whole[0] == -7.0) and torch.all(whole[-1] == -7.0), "a row outside of C was written"
     Cr, T = product(p.A, p.sA, p.B, p.sB)
     check(bf16_to_f64(C), Cr, T, f"block128 {mode} {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("M,N,K", [(3000, 1800, 272), (300, 264, 400)])
+def test_native_reports_other_scales(bs, M, N, K):
+    """Where the block-scaled MMA runs, a scale that is not a power of two is reported;
+    other forms multiply by it."""
+    p = Product(M, N, K, seed=3, pow2=True)
+    p.sA[M // 2, 0] = 3.0
+    C = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    bs.fp8_gemm_block128(*p.on(DEV), C, mode=bs.FP8_PATH_NATIVE)
+    torch.cuda.synchronize()
+    status = bs.fp8_status_query()
+    assert status == (bs._abi.FP8_ERR_SCALE if M == 3000 else 0)
+    keep = np.arange(M) != M // 2 if status else np.ones(M, bool)
+    Cr, T = product(p.A, p.sA, p.B, p.sB)
+    check(bf16_to_f64(C)[keep], Cr[keep], T[keep], f"native other scales {M}")
+
+
+def test_native_equals_promotion_on_exact_sums(bs):
+    """Codes and scales whose sums fp32 holds exactly: every path gives the same bits."""
+    M, N, K = 3000, 1800, 528
+    g = torch.Generator().manual_seed(6)
+    one = torch.tensor([0x00, 0x38, 0xB8], dtype=torch.uint8)   # 0, 1, -1
+    A = one[torch.randint(0, 3, (M, K), generator=g)].to(DEV)
+    B = one[torch.randint(0, 3, (N, K), generator=g)].to(DEV)
+    sA = torch.exp2(torch.randint(-2, 3, (M, 5), generator=g).float()).to(DEV)
+    sB = torch.exp2(torch.randint(-2, 3, (15, 5), generator=g).float()).to(DEV)
+    outs = [torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    for C, mode in zip(outs, (None, bs.FP8_PATH_NATIVE, bs.FP8_PATH_PROMOTE)):
+        bs.fp8_gemm_block128(A, sA, B, sB, C, mode=mode)
+    torch.cuda.synchronize()
+    assert bs.fp8_status_query() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("mode", ["auto", "native", "split"])
+def test_withheld_stage_runs_out(bs, mode):
+    """A load that never comes: the bounded wait is reported, the next call is right."""
+    M, N, K = (100, 264, 4112) if mode == "split" else (3000, 1800, 1040)
+    p = Product(M, N, K, seed=4, pow2=True)
+    ops = p.on(DEV)
+    m = bs.FP8_PATH_NATIVE if mode == "native" else None
+    C = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    bs.fp8_gemm_block128(*ops, C, mode=m)
+    torch.cuda.synchronize()
+    try:
+        bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 20_000_000)
+        bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, 5)
+        bs.fp8_gemm_block128(*ops, C, mode=m)
+        torch.cuda.synchronize()
+        assert bs.fp8_status_query() == bs._abi.FP8_ERR_TIMEOUT
+    finally:
+        bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, -1)
+        bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 0)
+    bs.fp8_gemm_block128(*ops, C, mode=m)
+    torch.cuda.synchronize()
+    assert bs.fp8_status_query() == 0
+    Cr, T = product(p.A, p.sA, p.B, p.sB)
+    check(bf16_to_f64(C), Cr, T, f"block128 after a timeout {mode}")
 
 
 def test_zero_inner_size(bs):
@@ -142,6 +203,7 @@ def _experts(bs, counts, N, K, mode=None, seed=1, lead=0, tail=0, pow2=False):
     ([1], 8, 16), ([0, 3, 0, 1, 0, 0, 9], 136, 272), ([5, 0, 64, 33], 264, 528), ([0, 0, 130, 1, 0, 257], 392, 400),
     ([128] * 4, 256, 512), ([300, 1, 0, 511, 129], 520, 656), ([1] * 40, 128, 144), ([0] * 9 + [2], 24, 128),
     ([2, 0, 900, 0, 0, 140], 1032, 272),
+    ([700, 0, 1, 2000, 129, 64, 33, 1500], 1288, 528), ([1] * 30 + [40] * 30, 1032, 272), ([9000, 11000], 264, 656),
 ])
 def test_experts(bs, counts, N, K, mode):
     _experts(bs, counts, N, K, mode=mode, pow2=mode == 1)
