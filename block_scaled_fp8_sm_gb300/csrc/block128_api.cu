@@ -107,6 +107,11 @@ int tile_args(Tile128Args &a, const RowsArgs &r, int BN, DeviceState *d) {
     a.E = r.E;
     a.mt = (r.M + T128_BM - 1) / T128_BM;
     a.nt = (r.N + BN - 1) / BN;
+    // tile order: B passes once for each group of m-tiles, whose A is read from L2 then;
+    // 32 MB is half of what one of the two L2 halves holds (8192 x 28672 x 8192, promotion /
+    // native: 32 MB 1406 / 1229 us, 16 MB 1396 / 1257, 64 MB 1496 / 1381)
+    const int64_t fit = (int64_t(32) << 20) / (static_cast<int64_t>(T128_BM) * r.K);
+    a.group = static_cast<int>(fit < 1 ? 1 : fit > a.mt ? a.mt : fit);
     return FP8_OK;
 }
 

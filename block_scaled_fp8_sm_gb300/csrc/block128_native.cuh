@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
                 uint32_t p[2][16];
                 tmem_ld_x16(taddr + 32 * x, p[0]);
                 tmem_ld_x16(taddr + 32 * x + 16, p[1]);
-                tmem_ld_wait();
+                tmem_ld_wait_for(p[0]);
+                tmem_ld_wait_for(p[1]);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     w[x][j] = bf16_pair(__uint_as_float(p[j >> 3][2 * (j & 7)]), __uint_as_float(p[j >> 3][2 * (j & 7) + 1]));

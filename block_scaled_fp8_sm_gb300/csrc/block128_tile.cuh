@@ -34,7 +34,6 @@ namespace bsfp8 {
 constexpr int T128_BM = 128;
 constexpr int T128_THREADS = 384;
 constexpr int T128_EPI_WARPS = 8;
-constexpr int T128_GROUP_M = 16;   // m-tiles per group of the tile order (L2 reuse)
 constexpr int T128_MAX_EXPERTS = 1024;
 constexpr int T128_MAX_SPLIT = 4;   // CTAs of a cluster
 // Registers per thread after the split: the launch holds 384 x 168 = 64512; the role
@@ -56,6 +55,7 @@ struct Tile128Args {
     uint32_t *status;
     long long wait_limit;
     int M, N, K, KB, NB, E, mt, nt;
+    int group;                // m-tiles whose A stays in L2 while B passes once
     int withhold;             // test hook: CTA 0 never loads this stage (-1: off)
 };
 
@@ -102,11 +102,21 @@ __device__ __forceinline__ bool wait128(uint64_t *bar, uint32_t parity, Ctl *ctl
     }
 }
 
+// Waits for this thread's tensor-memory loads; p passes through it, so that no use of p
+// can be moved before it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&p)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(p[0]), "+r"(p[1]), "+r"(p[2]), "+r"(p[3]), "+r"(p[4]), "+r"(p[5]), "+r"(p[6]), "+r"(p[7]),
+                   "+r"(p[8]), "+r"(p[9]), "+r"(p[10]), "+r"(p[11]), "+r"(p[12]), "+r"(p[13]), "+r"(p[14]), "+r"(p[15])
+                 :
+                 : "memory");
+}
+
 struct Tile128 {
     int m0, hi, n0, e;   // first row, end of its rows, first column, expert
 };
 
-// Tile t of the launch: experts in order, or groups of T128_GROUP_M m-tiles; m fastest.
+// Tile t of the launch: experts in order, or groups of a.group m-tiles; m fastest.
 template <int BN, typename Ctl>
 __device__ __forceinline__ Tile128 tile128(const Tile128Args &a, const Ctl *ctl, int t) {
     Tile128 r;
@@ -124,8 +134,8 @@ __device__ __forceinline__ Tile128 tile128(const Tile128Args &a, const Ctl *ctl,
         r.m0 = lo + (in % mt) * T128_BM;
         r.n0 = in / mt * BN;
     } else {
-        const int per = T128_GROUP_M * a.nt, grp = t / per, first = grp * T128_GROUP_M;
-        const int size = min(a.mt - first, T128_GROUP_M), in = t - grp * per;
+        const int per = a.group * a.nt, grp = t / per, first = grp * a.group;
+        const int size = min(a.mt - first, a.group), in = t - grp * per;
         r.e = 0;
         r.m0 = (first + in % size) * T128_BM;
         r.n0 = in / size * BN;
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 for (int x = 0; x < C::COLS / 16; ++x) {
                     uint32_t p[16];
                     tmem_ld_x16(taddr + b * BN + 16 * x, p);
-                    tmem_ld_wait();
+                    tmem_ld_wait_for(p);
                     if (x == C::COLS / 16 - 1) {   // the partial is in registers
                         tc_fence_before();
                         __syncwarp();
