@@ -40,7 +40,25 @@ namespace {
 
 constexpr int64_t kLim = int64_t(1) << 30;   // 32-bit indices in the kernels keep room for a tile past the end
 
-int launched() { return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA; }
+// Launches with programmatic stream serialization: the kernel's start overlaps the end of
+// the previous one of these kernels on the stream (each waits before it touches memory).
+template <typename Args>
+int launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, const Args &args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
 
 // Shapes and pointers common to both products.  FP8_OK with *empty set: nothing to do.
 int check_product(const void *A, const float *sA, const void *B, const float *sB, const void *C, int64_t M,
@@ -63,10 +81,11 @@ int check_product(const void *A, const float *sA, const void *B, const float *sB
 }
 
 template <int NT, int U, int WARPS, int CTAS>
-int launch_rows(const RowsArgs &a, int64_t groups, cudaStream_t stream) {
+int launch_rows(const RowsArgs &a, int64_t groups, DeviceState *d, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.N + ROWS_N - 1) / ROWS_N), static_cast<unsigned>(groups));
-    bsfp8_block128_rows<NT, U, WARPS, CTAS><<<grid, WARPS * 32, 0, stream>>>(a);
-    return launched();
+    if (static_cast<int64_t>(grid.x) * groups <= static_cast<int64_t>(CTAS) * d->sm_count)
+        return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, true>, grid, WARPS * 32, 0, 1, a, stream);
+    return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, false>, grid, WARPS * 32, 0, 1, a, stream);
 }
 
 RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
@@ -121,24 +140,10 @@ int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cud
     Tile128Args a{};
     const int rc = tile_args(a, r, BN, d);
     if (rc != FP8_OK) return rc;
-    if constexpr (SPLIT) {   // one tile per cluster
-        cudaLaunchConfig_t cfg{};
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(split);
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-        cfg.blockDim = dim3(T128_THREADS);
-        cfg.dynamicSmemBytes = smem128<BN>();
-        cfg.stream = stream;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, bsfp8_block128_tile<BN, true>, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
-    } else {
-        const unsigned grid = static_cast<unsigned>(tiles < d->sm_count ? tiles : d->sm_count);
-        bsfp8_block128_tile<BN, false><<<grid, T128_THREADS, smem128<BN>(), stream>>>(a);
-        return launched();
-    }
+    // split: one tile per cluster; else persistent CTAs
+    const int64_t ctas = SPLIT ? tiles * split : tiles < d->sm_count ? tiles : d->sm_count;
+    return launch(bsfp8_block128_tile<BN, SPLIT>, dim3(static_cast<unsigned>(ctas)), T128_THREADS, smem128<BN>(),
+                  split, a, stream);
 }
 
 int launch_native(const RowsArgs &r, int64_t tiles, DeviceState *d, cudaStream_t stream) {
@@ -146,8 +151,7 @@ int launch_native(const RowsArgs &r, int64_t tiles, DeviceState *d, cudaStream_t
     const int rc = tile_args(a, r, N128_BN, d);
     if (rc != FP8_OK) return rc;
     const unsigned grid = static_cast<unsigned>(tiles < d->sm_count ? tiles : d->sm_count);
-    bsfp8_block128_native<<<grid, T128_THREADS, smem_n128(), stream>>>(a);
-    return launched();
+    return launch(bsfp8_block128_native, dim3(grid), T128_THREADS, smem_n128(), 1, a, stream);
 }
 
 // CTAs that share a tile's K: as many as the GPU still has room for, four K blocks
@@ -160,10 +164,10 @@ int split_of(int64_t tiles, int KB, int sms) {
 
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
-    if (!pinned && a.M <= 8) return launch_rows<1, 2, 8, 3>(a, 1, stream);
+    if (!pinned && a.M <= 8) return launch_rows<1, 2, 8, 3>(a, 1, d, stream);
     const int64_t groups = (a.M + 15) / 16;
     if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
-        return launch_rows<2, 1, 8, 3>(a, groups, stream);
+        return launch_rows<2, 1, 8, 3>(a, groups, d, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
     if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
@@ -178,7 +182,7 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 4 * static_cast<int64_t>(a.E))
-        return launch_rows<1, 2, 4, 8>(a, a.M < a.E ? a.M : a.E, stream);
+        return launch_rows<1, 2, 4, 8>(a, a.M < a.E ? a.M : a.E, d, stream);
     const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
     const int64_t wide = most * ((a.N + 255) / 256), narrow = most * ((a.N + 127) / 128);
     if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
@@ -224,11 +228,10 @@ int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, vo
         const int64_t ctas = (n * a.KB + QTOK_GROUPS - 1) / QTOK_GROUPS;
         const int64_t most = static_cast<int64_t>(d->sm_count) * 64;
         const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-        if (flags & FP8_QUANT_POW2)
-            bsfp8_quantize_tokens<GATED, true><<<grid, QTOK_THREADS, 0, stream>>>(a);
-        else
-            bsfp8_quantize_tokens<GATED, false><<<grid, QTOK_THREADS, 0, stream>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
+        const int rc = launch(flags & FP8_QUANT_POW2 ? bsfp8_quantize_tokens<GATED, true>
+                                                     : bsfp8_quantize_tokens<GATED, false>,
+                              dim3(grid), QTOK_THREADS, 0, 1, a, stream);
+        if (rc != FP8_OK) return rc;
         if (rows) {
             a.rows += n;
         } else {

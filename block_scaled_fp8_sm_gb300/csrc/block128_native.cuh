@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
         tmem_alloc(&ctl->tmem, 512);
         tmem_relinquish();
     }
+    launch_dependents();
+    wait_for_previous();
     if (warp == 2) count_tiles(a, ctl);
     tc_fence_before();
     __syncthreads();

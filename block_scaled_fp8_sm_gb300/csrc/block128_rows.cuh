@@ -17,6 +17,12 @@
 // cover one another's starts and sums (24 rows over 22 of 64 experts of 4096 x 7168:
 // 89 us; eight warps and three CTAs 97; U = 4, two CTAs 110).
 //
+// Every launch may be set up while the previous kernel ends (programmatic dependent
+// launch); NEXT, a launch whose CTAs all fit on the GPU at once (one token: 256), also lets
+// the next one in after its K loop: 1 x 4096 x 7168 in a stream of calls 8.2 -> 6.4 us.  At
+// its start the next launch's CTAs would take its places on the SMs (7.6 us), and launches
+// of several waves lose by it (24 rows over 64 experts 101 -> 115 us).
+//
 // The K order inside a block is permuted alike on both sides: lane t of a
 // quad holds bytes 64 j + 16 t .. + 15 (j = 0, 1), so a load of a warp covers 64
 // contiguous bytes of each of 8 rows.
@@ -40,6 +46,11 @@ struct RowsArgs {
 };
 
 constexpr int ROWS_N = 16;   // rows of B per CTA
+
+// Programmatic dependent launch: the next kernel of the stream may be set up while this
+// one runs, and waits for this one's end (and its memory) before it reads or writes.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                  uint32_t b0, uint32_t b1) {
@@ -91,13 +102,14 @@ __device__ __forceinline__ int busy_expert(const int32_t *offsets, int E, int T,
     return *found;
 }
 
-template <int NT, int U, int WARPS, int CTAS>
+template <int NT, int U, int WARPS, int CTAS, bool NEXT>
 __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const RowsArgs a) {
     __shared__ float red[WARPS][NT][4][32];
     __shared__ int counts[WARPS];
     __shared__ int found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = static_cast<int>(blockIdx.x) * ROWS_N;
+    wait_for_previous();
     int lo = 0, hi = a.M, e = 0;
     if (a.offsets) {
         e = busy_expert(a.offsets, a.E, a.M, static_cast<int>(blockIdx.y), counts, &found, a.status);
@@ -163,6 +175,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const Ro
                     }
                 }
             }
+        }
+        if constexpr (NEXT) {
+            if (m0 + 8 * NT >= hi) launch_dependents();
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)

@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         tmem_alloc(&ctl->tmem, 512);
         tmem_relinquish();
     }
+    launch_dependents();
+    wait_for_previous();
     if (warp == 2) {
         count_tiles(a, ctl);
     }
@@ -330,16 +332,16 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 bool ok = true;
                 for (int t = unit; t < tiles && ok; t += units) {
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        ok = wait128(&ctl->tempty[b], bph, ctl, a) && wait128(&ctl->full[s], ph, ctl, a);
-                        if (!ok) break;
-                        tc_fence_after();
                         const uint64_t ad = sdesc_k_sw128(smem_u32(sm_a + s * C::A_BYTES));
                         const uint64_t bd = sdesc_k_sw128(smem_u32(sm_b + s * C::B_BYTES));
-                        const uint32_t d = tmem + b * BN;
+                        // the operands first: the partial's release is what comes last
+                        ok = wait128(&ctl->full[s], ph, ctl, a) && wait128(&ctl->tempty[b], bph, ctl, a);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f8(d, ad + 2 * i, bd + 2 * i, idesc, i > 0);
-                        mma_commit(&ctl->empty[s]);
+                        for (int i = 0; i < 4; ++i) mma_f8(tmem + b * BN, ad + 2 * i, bd + 2 * i, idesc, i > 0);
                         mma_commit(&ctl->tfull[b]);
+                        mma_commit(&ctl->empty[s]);
                         if (++s == C::STAGES) {
                             s = 0;
                             ph ^= 1u;

@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "block128_rows.cuh"
 #include "quant_kernel.cuh"
 
 namespace bsfp8 {
@@ -115,6 +116,8 @@ __device__ __forceinline__ uint2 codes8_pow2(const uint64_t (&y)[4], float inv) 
 
 template <bool GATED, bool POW2>
 __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_quantize_tokens(const QuantTokensArgs a) {
+    launch_dependents();
+    wait_for_previous();
     const int l = threadIdx.x & 7;
     const uint32_t stride = gridDim.x * QTOK_GROUPS;
     // the whole warp stays in the loop together (shuffles): the bound is the warp's
