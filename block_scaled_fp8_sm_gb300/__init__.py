@@ -176,11 +176,23 @@ def fp8_quantize_blocks(x, q=None, s=None, stream=None):
 # sizes).  A call of a few microseconds is bound by this marshalling: the checks are
 # written out, without helpers or tuples built per tensor.
 
-def _sizes_differ(what, *tensors):
-    for t, size in tensors:
-        if t.element_size() != size:
-            return f"{what}: a tensor of type {t.dtype} where {size}-byte elements are expected"
-    return f"{what}: tensors must be contiguous"
+class _Types:
+    """torch's types, looked up once (torch is imported on first use)."""
+    loaded = None
+
+    def __init__(self):
+        import torch
+        self.codes = frozenset((torch.uint8, torch.float8_e4m3fn))
+        self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
+        _Types.loaded = self
+
+
+def _refused(what, *tensors):
+    """The ValueError for tensors that are not contiguous CUDA tensors of their types."""
+    for name, t, kind in tensors:
+        if not (t.dtype in kind if isinstance(kind, frozenset) else t.dtype is kind):
+            return ValueError(f"{what}: {name} has type {t.dtype}")
+    return ValueError(f"{what}: tensors must be contiguous and on the GPU")
 
 
 def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
@@ -194,10 +206,13 @@ def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
     N, kb = B.shape[0], (K + 127) // 128
     if (B.shape != (N, K) or C.shape != (M, N) or sA.shape != (M, kb) or sB.shape != ((N + 127) // 128, kb)):
         raise ValueError("fp8_gemm_block128: shapes of A, sA, B, sB, C do not match")
-    if not (A.element_size() == B.element_size() == 1 and sA.element_size() == sB.element_size() == 4
-            and C.element_size() == 2 and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous()
-            and sB.is_contiguous() and C.is_contiguous()):
-        raise ValueError(_sizes_differ("fp8_gemm_block128", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2)))
+    d = _Types.loaded or _Types()
+    if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
+            and C.dtype is d.bf16 and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous()
+            and sB.is_contiguous() and C.is_contiguous()
+            and A.is_cuda and sA.is_cuda and B.is_cuda and sB.is_cuda and C.is_cuda):
+        raise _refused("fp8_gemm_block128", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
+                       ("sB", sB, d.f32), ("C", C, d.bf16))
     rc = library().fp8_gemm_block128_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), M, N,
                                         K, FP8_PATH_AUTO if mode is None else mode, _stream(stream))
     if rc:
@@ -217,11 +232,13 @@ def fp8_gemm_experts(A, sA, B, sB, C, offsets, stream=None, mode=None):
     if (B.shape != (E, N, K) or C.shape != (T, N) or sA.shape != (T, kb)
             or sB.shape != (E, (N + 127) // 128, kb) or offsets.shape != (E + 1,)):
         raise ValueError("fp8_gemm_experts: shapes of A, sA, B, sB, C, offsets do not match")
-    if not (A.element_size() == B.element_size() == 1
-            and sA.element_size() == sB.element_size() == offsets.element_size() == 4 and C.element_size() == 2
-            and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous() and sB.is_contiguous()
-            and C.is_contiguous() and offsets.is_contiguous()):
-        raise ValueError(_sizes_differ("fp8_gemm_experts", (A, 1), (sA, 4), (B, 1), (sB, 4), (C, 2), (offsets, 4)))
+    d = _Types.loaded or _Types()
+    if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
+            and C.dtype is d.bf16 and offsets.dtype is d.i32 and A.is_contiguous() and sA.is_contiguous()
+            and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous() and offsets.is_contiguous()
+            and A.is_cuda and sA.is_cuda and B.is_cuda and sB.is_cuda and C.is_cuda and offsets.is_cuda):
+        raise _refused("fp8_gemm_experts", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
+                       ("sB", sB, d.f32), ("C", C, d.bf16), ("offsets", offsets, d.i32))
     rc = library().fp8_gemm_experts_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(),
                                        offsets.data_ptr(), T, N, K, E, FP8_PATH_AUTO if mode is None else mode,
                                        _stream(stream))
@@ -243,11 +260,12 @@ def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
         q, s = _token_operands(M, K, q, s, x.device)
     if q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_quantize_tokens: q must be [M, K] and s [M, ceil(K/128)]")
-    if not (x.element_size() == 2 and q.element_size() == 1 and s.element_size() == 4 and q.is_contiguous()
-            and s.is_contiguous() and (x.stride(1) == 1 or K <= 1)):
-        raise ValueError(_sizes_differ("fp8_quantize_tokens", (x, 2), (q, 1), (s, 4)))
-    if rows is not None and not (rows.element_size() == 4 and rows.dim() == 1 and rows.is_contiguous()):
-        raise ValueError(_sizes_differ("fp8_quantize_tokens: rows (a vector)", (rows, 4)))
+    d = _Types.loaded or _Types()
+    if rows is not None and not (rows.dtype is d.i32 and rows.dim() == 1 and rows.is_contiguous() and rows.is_cuda):
+        raise _refused("fp8_quantize_tokens (rows: a vector)", ("rows", rows, d.i32))
+    if not (x.dtype is d.bf16 and q.dtype in d.codes and s.dtype is d.f32 and q.is_contiguous()
+            and s.is_contiguous() and (x.stride(1) == 1 or K <= 1) and x.is_cuda and q.is_cuda and s.is_cuda):
+        raise _refused("fp8_quantize_tokens", ("x", x, d.bf16), ("q", q, d.codes), ("s", s, d.f32))
     rc = library().fp8_quantize_tokens(x.data_ptr(), x.stride(0) if R > 1 else K, R,
                                        None if rows is None else rows.data_ptr(), q.data_ptr(), s.data_ptr(), M, K,
                                        FP8_QUANT_POW2 if pow2 else 0, _stream(stream))
@@ -265,9 +283,10 @@ def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
         q, s = _token_operands(M, K, q, s, x.device)
     if K2 % 2 or q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_swiglu_quantize_tokens: x is [M, 2K], q [M, K] and s [M, ceil(K/128)]")
-    if not (x.element_size() == 2 and q.element_size() == 1 and s.element_size() == 4 and q.is_contiguous()
-            and s.is_contiguous() and (x.stride(1) == 1 or K2 <= 1)):
-        raise ValueError(_sizes_differ("fp8_swiglu_quantize_tokens", (x, 2), (q, 1), (s, 4)))
+    d = _Types.loaded or _Types()
+    if not (x.dtype is d.bf16 and q.dtype in d.codes and s.dtype is d.f32 and q.is_contiguous()
+            and s.is_contiguous() and (x.stride(1) == 1 or K2 <= 1) and x.is_cuda and q.is_cuda and s.is_cuda):
+        raise _refused("fp8_swiglu_quantize_tokens", ("x", x, d.bf16), ("q", q, d.codes), ("s", s, d.f32))
     rc = library().fp8_swiglu_quantize_tokens(x.data_ptr(), x.stride(0) if M > 1 else K2, q.data_ptr(), s.data_ptr(),
                                               M, K, FP8_QUANT_POW2 if pow2 else 0, _stream(stream))
     if rc:

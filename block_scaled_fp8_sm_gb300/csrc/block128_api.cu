@@ -57,7 +57,19 @@ int launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess) return FP8_OK;
+    (void)cudaGetLastError();   // reported here: not left for a later call
+    return FP8_ERR_CUDA;
+}
+
+// The tensor-map cache may fail to allocate: no exception leaves a C entry point.
+template <typename F>
+int guarded(F body) {
+    try {
+        return body();
+    } catch (...) {
+        return FP8_ERR_CUDA;
+    }
 }
 
 // Shapes and pointers common to both products.  FP8_OK with *empty set: nothing to do.
@@ -262,7 +274,7 @@ int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const fl
     if (K == 0) return zero_fill(C, M * N, stream);
     RowsArgs a = rows_args(A, sA, B, sB, C, M, N, K);
     a.status = d->status;
-    return launch_product(a, mode, d, stream);
+    return guarded([&] { return launch_product(a, mode, d, stream); });
 }
 
 int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
@@ -287,7 +299,7 @@ int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const flo
     a.offsets = offsets;
     a.E = E;
     a.status = d->status;
-    return launch_experts(a, mode, d, stream);
+    return guarded([&] { return launch_experts(a, mode, d, stream); });
 }
 
 int fp8_gemm_experts(const void *A, const float *sA, const void *B, const float *sB, void *C, const int32_t *offsets,

@@ -99,5 +99,12 @@ def test_python_refusals():
         bs.fp8_quantize_tokens(x, rows=z(3, dtype=torch.int64))
     with pytest.raises(ValueError, match="contiguous"):
         bs.fp8_quantize_tokens(z(256, 4, dtype=torch.bfloat16).T)
+    with pytest.raises(ValueError, match="type"):
+        bs.fp8_quantize_tokens(x.to(torch.float16))
+    for call in (lambda: bs.fp8_gemm_block128(A, sA, B, sB, C), lambda: bs.fp8_quantize_tokens(x),
+                 lambda: bs.fp8_gemm_experts(A, sA, B3, sB3, C, z(4, dtype=torch.int32)),
+                 lambda: bs.fp8_swiglu_quantize_tokens(x)):
+        with pytest.raises(ValueError, match="GPU"):   # host tensors
+            call()
     with pytest.raises(ValueError):
         bs.fp8_swiglu_quantize_tokens(z(4, 33, dtype=torch.bfloat16))
