@@ -75,7 +75,8 @@ struct Ctrl128 {
     uint64_t tfull[Cfg128<BN>::BUFS], tempty[Cfg128<BN>::BUFS], drain;
     uint32_t tmem;
     int abort, tiles;
-    int start[T128_MAX_EXPERTS + 1];   // experts: first tile of each
+    int start[T128_MAX_EXPERTS + 1];   // experts: first tile of each,
+    int2 rows[T128_MAX_EXPERTS];       // and its rows
 };
 
 template <int BN>
@@ -127,11 +128,11 @@ __device__ __forceinline__ Tile128 tile128(const Tile128Args &a, const Ctl *ctl,
             if (ctl->start[mid] <= t) e0 = mid;
             else e1 = mid;
         }
-        int lo;
-        expert_rows(a.offsets, e0, a.M, lo, r.hi);
-        const int in = t - ctl->start[e0], mt = (ctl->start[e0 + 1] - ctl->start[e0]) / a.nt;
+        const int2 rows = ctl->rows[e0];
+        const int in = t - ctl->start[e0], mt = (rows.y - rows.x + T128_BM - 1) / T128_BM;
         r.e = e0;
-        r.m0 = lo + (in % mt) * T128_BM;
+        r.hi = rows.y;
+        r.m0 = rows.x + (in % mt) * T128_BM;
         r.n0 = in / mt * BN;
     } else {
         const int per = a.group * a.nt, grp = t / per, first = grp * a.group;
@@ -171,6 +172,40 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr, uint32_t rank) {
         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
         : "r"(addr), "r"(rank));
     return v;
+}
+
+// acc += s * (16 columns of a partial): the load, its wait and the FMAs as one block, so
+// that the compiler keeps this order whatever surrounds it (loads hoisted over the FMAs of
+// the piece before, or two pieces in flight, ran slower: the other warp of the
+// sub-partition fills the wait).
+__device__ __forceinline__ void promote16(float *acc, uint32_t taddr, float s) {
+    asm volatile(
+        "{\n\t.reg .b32 p0, p1, p2, p3, p4, p5, p6, p7, p8, p9, p10, p11, p12, p13, p14, p15;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {p0,p1,p2,p3,p4,p5,p6,p7,p8,p9,p10,p11,p12,p13,p14,p15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "fma.rn.f32 %0, p0, %17, %0;\n\t"
+        "fma.rn.f32 %1, p1, %17, %1;\n\t"
+        "fma.rn.f32 %2, p2, %17, %2;\n\t"
+        "fma.rn.f32 %3, p3, %17, %3;\n\t"
+        "fma.rn.f32 %4, p4, %17, %4;\n\t"
+        "fma.rn.f32 %5, p5, %17, %5;\n\t"
+        "fma.rn.f32 %6, p6, %17, %6;\n\t"
+        "fma.rn.f32 %7, p7, %17, %7;\n\t"
+        "fma.rn.f32 %8, p8, %17, %8;\n\t"
+        "fma.rn.f32 %9, p9, %17, %9;\n\t"
+        "fma.rn.f32 %10, p10, %17, %10;\n\t"
+        "fma.rn.f32 %11, p11, %17, %11;\n\t"
+        "fma.rn.f32 %12, p12, %17, %12;\n\t"
+        "fma.rn.f32 %13, p13, %17, %13;\n\t"
+        "fma.rn.f32 %14, p14, %17, %14;\n\t"
+        "fma.rn.f32 %15, p15, %17, %15;\n\t"
+        "}"
+        : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3]),
+          "+f"(acc[4]), "+f"(acc[5]), "+f"(acc[6]), "+f"(acc[7]),
+          "+f"(acc[8]), "+f"(acc[9]), "+f"(acc[10]), "+f"(acc[11]),
+          "+f"(acc[12]), "+f"(acc[13]), "+f"(acc[14]), "+f"(acc[15])
+        : "r"(taddr), "f"(s)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -225,7 +260,10 @@ __device__ __forceinline__ void count_tiles(const Tile128Args &a, Ctl *ctl) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += v;
         }
-        if (e < a.E) ctl->start[e] = base + sum - n;
+        if (e < a.E) {
+            ctl->start[e] = base + sum - n;
+            ctl->rows[e] = make_int2(lo, hi);
+        }
         base += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
     if (lane == 0) ctl->start[a.E] = ctl->tiles = base;
@@ -368,20 +406,26 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         int b = 0;
         uint32_t bph = 0;
         bool ok = true;
-        for (int t = unit; t < tiles && ok; t += units) {
-            const Tile128 tt = tile128<BN>(a, ctl, t);
+        // a tile's place, its scales' addresses and the first two of them
+        Tile128 tt{};
+        const float *psa = nullptr, *psb = nullptr;
+        float sa = 0.0f, sb = 0.0f;
+        auto begin = [&](int t) {
+            tt = tile128<BN>(a, ctl, t);
             const int m = min(tt.m0 + r, tt.hi - 1);
             const int nb = min((tt.n0 + h * C::COLS) / 128, a.NB - 1);
-            const float *psa = a.sA + static_cast<int64_t>(m) * a.KB;
-            const float *psb = a.sB + (static_cast<int64_t>(tt.e) * a.NB + nb) * a.KB;
-            float acc[C::COLS];
-#pragma unroll
-            for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
-            float sa = 0.0f, sb = 0.0f;
+            psa = a.sA + static_cast<int64_t>(m) * a.KB;
+            psb = a.sB + (static_cast<int64_t>(tt.e) * a.NB + nb) * a.KB;
             if (kb0 < kb1) {
                 sa = __ldg(psa + kb0);
                 sb = __ldg(psb + kb0);
             }
+        };
+        if (unit < tiles) begin(unit);
+        for (int t = unit; t < tiles && ok; t += units) {
+            float acc[C::COLS];
+#pragma unroll
+            for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
             for (int kb = kb0; kb < kb1; ++kb) {
                 const float sc = sa * sb;
                 const int next = min(kb + 1, kb1 - 1);
@@ -390,25 +434,27 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->tfull[b], bph, ctl, a));
                 if (!ok) break;
                 tc_fence_after();
+                constexpr int PIECES = C::COLS / 16;
 #pragma unroll
-                for (int x = 0; x < C::COLS / 16; ++x) {
-                    uint32_t p[16];
-                    tmem_ld_x16(taddr + b * BN + 16 * x, p);
-                    tmem_ld_wait_for(p);
-                    if (x == C::COLS / 16 - 1) {   // the partial is in registers
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->tempty[b]);
-                    }
+                for (int x = 0; x + 1 < PIECES; ++x) promote16(acc + 16 * x, taddr + b * BN + 16 * x, sc);
+                uint32_t p[16];
+                tmem_ld_x16(taddr + b * BN + 16 * (PIECES - 1), p);
+                tmem_ld_wait_for(p);
+                tc_fence_before();   // the partial is in registers
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->tempty[b]);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[16 * x + j] = fmaf(__uint_as_float(p[j]), sc, acc[16 * x + j]);
-                }
+                for (int j = 0; j < 16; ++j)
+                    acc[C::COLS - 16 + j] = fmaf(__uint_as_float(p[j]), sc, acc[C::COLS - 16 + j]);
                 if (++b == C::BUFS) {
                     b = 0;
                     bph ^= 1u;
                 }
             }
             if (!ok) break;
+            const Tile128 cur = tt;
+            // the next tile's first scales are on their way while this one is stored
+            if (t + units < tiles) begin(t + units);
             if constexpr (SPLIT) {
                 // the partial sums go to the operand ring's memory (nothing is in
                 // flight there any more: the last partial came after the last load),
@@ -425,7 +471,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = bf16_pair(acc[32 * x + 2 * j], acc[32 * x + 2 * j + 1]);
-                    store_rows32(mine, a, tt, q, tt.n0 + h * C::COLS + 32 * x, w);
+                    store_rows32(mine, a, cur, q, cur.n0 + h * C::COLS + 32 * x, w);
                 }
             }
         }
