@@ -15,7 +15,8 @@
 // 4-11 read the sums once per tile, round them to bf16 and release the accumulator
 // before they store.  Tensor memory: sums in columns 0-255, scales from column 256.
 //
-// 8192 x 28672 x 8192: 1217 us against 1410 us by promotion (same call).
+// 8192 x 28672 x 8192: 1217 us (3160 TFLOP/s, 82 % of twice the measured bf16 rate, under
+// the power cap) against 1406 us by promotion.
 #pragma once
 #include "block128_tile.cuh"
 

@@ -15,6 +15,17 @@
 // the tensor-memory lanes (rows) 32 (w mod 4) .., columns of half (w - 4) / 4.  The
 // partials are double- (BN = 256) or quadruple-buffered (BN = 128).
 //
+// What bounds it: a partial's round trip.  The four MMAs of a block keep the tensor pipe
+// busy ~505 cycles, the epilogue needs ~660 for its eight load-and-FMA pieces and the
+// hand-over, and with two 256-column partials the sum of both and of the two signals is
+// paid every second block: ~870 cycles a block, the tensor pipe 55-65 % busy (4096^3 61 us,
+// 2250 TFLOP/s; 8192 x 28672 x 8192 1406 us, 2740, where power holds the clock near 1.8
+// GHz).  Measured and slower: more, narrower partials (128 columns 72 us: an N = 128 MMA
+// costs as much as N = 256), 192 columns with twelve epilogue warps (71), sixteen warps
+// (78), packed FMAs (67: the loaded values have to be moved into pairs), two pieces in
+// flight (61-70), scales staged in shared memory by the idle warps (73).  The role threads
+// are chosen by elect.sync: with lane == 0 the MMA thread's own loop took 20 % longer.
+//
 // Without SPLIT a CTA is persistent over tiles; with SPLIT a cluster of CTAs shares
 // one tile, each taking a range of K blocks: the partial sums meet in the CTAs' own
 // shared memory and are added in rank order over distributed shared memory, so a
@@ -38,9 +49,8 @@ constexpr int T128_MAX_EXPERTS = 1024;
 constexpr int T128_MAX_SPLIT = 4;   // CTAs of a cluster
 // Registers per thread after the split: the launch holds 384 x 168 = 64512; the role
 // warpgroup keeps 80, the two epilogue warpgroups take 208 (128 x 80 + 256 x 208 =
-// 63488): a thread holds 128 sums and 16 values of a partial.  At 168 the K loop spilled
-// and 8192 x 28672 x 8192 took 2423 us, now 1445 us.  Scalar FMAs: packed pairs
-// (fma.rn.f32x2) need the partial's values moved into aligned pairs first (1500 us).
+// 63488): a thread holds 128 sums and 16 values of a partial.  At 168 the K loop spilled:
+// 4096^3 109 us, with the split 70 us.
 constexpr int T128_ROLE_REGS = 80;
 constexpr int T128_EPI_REGS = 208;
 

@@ -10,9 +10,10 @@
 // of the piece: every load of a warp is four runs of 128 bytes): the maximum takes
 // three shuffles for sixteen values.  The row of a piece comes from a multiplication
 // by the reciprocal of the pieces per row.  Loads in flight come from resident warps (64
-// of them an SM, 48 where the arithmetic needs 40 registers) and not from pieces loaded ahead: 16384 x 7168 gathered 39 us,
-// plain 54.6 (53.3 at the measured copy bandwidth), gated 16001 x 4096 61.6; two pieces
-// ahead with fewer warps 41 / 57 / 65, four 43 / 56 / 82.
+// of them an SM, 48 where the arithmetic needs 40 registers), not from pieces loaded ahead:
+// 16384 x 7168 gathered from 4096 tokens 38 us (180 MB at the copy bandwidth 27; L2 serves
+// the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 60 us (49: integer and
+// conversion work); two pieces ahead with half the warps 41 / 57 / 65.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
