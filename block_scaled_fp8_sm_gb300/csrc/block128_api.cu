@@ -132,7 +132,6 @@ int tile_args(Tile128Args &a, const RowsArgs &r, int BN, DeviceState *d) {
     a.withhold = withheld_stage();
     a.M = r.M;
     a.N = r.N;
-    a.K = r.K;
     a.KB = r.KB;
     a.NB = (r.N + 127) / 128;
     a.E = r.E;
@@ -208,7 +207,7 @@ template <bool GATED>
 int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, void *q, float *s, int64_t M,
              int64_t K, int flags, cudaStream_t stream) {
     const int64_t width = GATED ? 2 * K : K;
-    if (M < 0 || K < 0 || x_rows < 0 || M >= kLim || width >= kLim || x_rows >= kLim) return FP8_ERR_SHAPE;
+    if (M < 0 || K < 0 || x_rows < 0 || M >= kLim || width >= kLim || x_rows >= kLim || ldx >= 2 * kLim) return FP8_ERR_SHAPE;
     if (K % 16 != 0 || ldx < width || ldx % 8 != 0) return FP8_ERR_SHAPE;
     if (flags & ~FP8_QUANT_POW2) return FP8_ERR_MODE;
     if (M == 0 || K == 0) return FP8_OK;
@@ -223,10 +222,10 @@ int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, vo
     a.rows = rows;
     a.q = static_cast<uint8_t *>(q);
     a.s = s;
-    a.ldx = ldx;
-    a.x_rows = x_rows;
-    a.K = static_cast<int>(K);
-    a.KB = static_cast<int>((K + 127) / 128);
+    a.ldx = static_cast<uint32_t>(ldx);
+    a.x_rows = static_cast<uint32_t>(x_rows);
+    a.K = static_cast<uint32_t>(K);
+    a.KB = static_cast<uint32_t>((K + 127) / 128);
     // p / KB for p < 2^31: multiplier ceil(2^(31 + l) / KB) with l = ceil(log2 KB)
     // (Granlund and Montgomery, PLDI 1994), below 2^32
     int l = 0;
@@ -248,7 +247,7 @@ int quantize(const void *x, int64_t ldx, int64_t x_rows, const int32_t *rows, vo
             a.rows += n;
         } else {
             a.x += n * ldx;
-            a.x_rows -= n;
+            a.x_rows -= static_cast<uint32_t>(n);
         }
         a.q += n * K;
         a.s += n * a.KB;

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
                 }
             }
         }
-        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, 2u);   // STATUS_SCALE
+        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, STATUS_SCALE);
     } else {
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::COLS;

@@ -31,6 +31,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "status.h"
 
 namespace bsfp8 {
 
@@ -85,7 +86,7 @@ __device__ __forceinline__ int busy_expert(const int32_t *offsets, int E, int T,
         if (e < E) {
             expert_rows(offsets, e, T, lo, hi);
             if (last && blockIdx.x == 0 && (lo != __ldg(offsets + e) || hi != __ldg(offsets + e + 1) || hi < lo))
-                atomicOr(status, 4u);   // STATUS_RECORD
+                atomicOr(status, STATUS_RECORD);
         }
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, hi > lo);
         if (lane == 0) counts[warp] = __popc(mask);

@@ -64,7 +64,7 @@ struct Tile128Args {
     const int32_t *offsets;   // [E + 1], or null: one product
     uint32_t *status;
     long long wait_limit;
-    int M, N, K, KB, NB, E, mt, nt;
+    int M, N, KB, NB, E, mt, nt;
     int group;                // m-tiles whose A stays in L2 while B passes once
     int withhold;             // test hook: CTA 0 never loads this stage (-1: off)
 };
@@ -106,7 +106,7 @@ __device__ __forceinline__ bool wait128(uint64_t *bar, uint32_t parity, Ctl *ctl
             if (*reinterpret_cast<volatile int *>(&ctl->abort)) return false;
             if (clock64() - t0 > a.wait_limit) {
                 *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
-                atomicOr(a.status, 1u);   // STATUS_TIMEOUT
+                atomicOr(a.status, STATUS_TIMEOUT);
                 return false;
             }
         }
@@ -261,7 +261,7 @@ __device__ __forceinline__ void count_tiles(const Tile128Args &a, Ctl *ctl) {
         if (e < a.E) {
             expert_rows(a.offsets, e, a.M, lo, hi);
             if (blockIdx.x == 0 && (lo != __ldg(a.offsets + e) || hi != __ldg(a.offsets + e + 1) || hi < lo))
-                atomicOr(a.status, 4u);   // STATUS_RECORD
+                atomicOr(a.status, STATUS_RECORD);
         }
         const int n = hi > lo ? (hi - lo + T128_BM - 1) / T128_BM * a.nt : 0;
         int sum = n;

@@ -83,6 +83,7 @@
 
 #include "ptx.cuh"
 #include "quant_kernel.cuh"
+#include "status.h"
 
 namespace bsfp8 {
 
@@ -96,7 +97,6 @@ constexpr int MAX_GROUPS = 64;
 constexpr int GROUP_M = 8;         // tile-order swizzle width (m-tiles) for L2 reuse
 constexpr int TILE_N = 256;        // the BN every launch uses
 
-enum : uint32_t { STATUS_TIMEOUT = 1u, STATUS_SCALE = 2u, STATUS_RECORD = 4u };
 enum : int { PATH_AUTO = 0, PATH_NATIVE = 1, PATH_PROMOTE = 2 };
 // Scale layouts (a kernel template parameter, so each layout compiles its own
 // kernel and the block-scaled kernels carry no code for the others):

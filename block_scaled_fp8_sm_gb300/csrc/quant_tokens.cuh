@@ -11,8 +11,8 @@
 // three shuffles for sixteen values.  The row of a piece comes from a multiplication
 // by the reciprocal of the pieces per row.  Loads in flight come from resident warps (64
 // of them an SM, 48 where the arithmetic needs 40 registers), not from pieces loaded ahead:
-// 16384 x 7168 gathered from 4096 tokens 38 us (180 MB at the copy bandwidth 27; L2 serves
-// the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 60 us (49: integer and
+// 16384 x 7168 gathered from 4096 tokens 36.6 us (180 MB at the copy bandwidth 27; L2 serves
+// the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 58.5 us (49: integer and
 // conversion work); two pieces ahead with half the warps 41 / 57 / 65.
 #pragma once
 #include <cuda_bf16.h>
@@ -31,10 +31,10 @@ struct QuantTokensArgs {
     const int32_t *rows;      // [M] source rows, or null
     uint8_t *q;               // [M, K]
     float *s;                 // [M, KB]
-    int64_t ldx, x_rows;
+    uint32_t ldx, x_rows;     // (32-bit factors: one wide multiplication per address)
     uint32_t pieces;          // M * KB < 2^31
     uint32_t mul, shift;      // piece / KB = piece * mul >> shift, exact for pieces < 2^31
-    int K, KB;
+    uint32_t K, KB;
 };
 
 // s rounded up to a power of two, at least 2^-126 (so that 1/s is exact).
@@ -47,18 +47,16 @@ __device__ __forceinline__ uint64_t f32x2_of(float lo, float hi) {
 }
 
 // silu(g) u on two values.  exp(-|g|) = 2^t, t = -|g| log2(e): the product's rounding
-// error t_lo comes from an fma (Dekker's error-free product) and enters as
-// 2^t (1 + t_lo ln 2); the sigmoid is r = 1 / (1 + e), or e r for negative g, so no
-// exponential overflows and small results keep their relative precision.
+// error comes from an fma (Dekker's error-free product) and enters as 2^t (1 + t_lo ln 2);
+// the sigmoid is r = 1 / (1 + e), or e r for negative g, so no exponential overflows and
+// small results keep their relative precision.
 __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
     constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
     uint32_t g0, g1;
     f32x2_unpack(g, g0, g1);
-    const uint64_t a = f32x2_pack(g0 | 0x80000000u, g1 | 0x80000000u);   // -|g|
-    const uint64_t l2 = f32x2_of(kL, kL);
-    const uint64_t t = mul_f32x2_rn(a, l2);
-    const uint64_t neg_t = t ^ 0x8000000080000000ull;
-    uint64_t lo = fma_f32x2_rn(a, l2, neg_t);
+    const uint64_t a = f32x2_pack(g0 & 0x7FFFFFFFu, g1 & 0x7FFFFFFFu);   // |g|
+    const uint64_t t = mul_f32x2_rn(a, f32x2_of(-kL, -kL));
+    uint64_t lo = fma_f32x2_rn(a, f32x2_of(kL, kL), t);   // |g| log2(e) + t = -t_lo
     lo = fma_f32x2_rn(a, f32x2_of(kLlo, kLlo), lo);
     uint32_t t0, t1;
     f32x2_unpack(t, t0, t1);
@@ -66,7 +64,7 @@ __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
     asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(__uint_as_float(t0)));
     asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(__uint_as_float(t1)));
     uint64_t e = f32x2_of(e0, e1);
-    e = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(kLn2, kLn2)), e, e);
+    e = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(-kLn2, -kLn2)), e, e);
     uint32_t b0, b1;
     f32x2_unpack(e, b0, b1);
     float r0, r1;
@@ -119,7 +117,7 @@ template <bool GATED, bool POW2>
 __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_quantize_tokens(const QuantTokensArgs a) {
     launch_dependents();
     wait_for_previous();
-    const int l = threadIdx.x & 7;
+    const uint32_t l = threadIdx.x & 7u;
     const uint32_t stride = gridDim.x * QTOK_GROUPS;
     // the whole warp stays in the loop together (shuffles): the bound is the warp's
     const uint32_t first = blockIdx.x * QTOK_GROUPS + (threadIdx.x >> 5) * 4, mine = (threadIdx.x >> 3) & 3;
@@ -128,14 +126,15 @@ __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_qu
         const uint32_t p = base + mine;
         const bool in = p < a.pieces;
         const uint32_t row = static_cast<uint32_t>(static_cast<uint64_t>(p) * a.mul >> a.shift);
-        const int kb = in ? static_cast<int>(p - row * a.KB) : -1;
-        int64_t src = row;
-        if (a.rows && in) src = __ldg(a.rows + row);
-        const bool ok = in && src >= 0 && src < a.x_rows;
-        const __nv_bfloat16 *px = a.x + src * a.ldx + kb * 128 + 8 * l;
+        const uint32_t kb = p - row * a.KB;
+        const uint32_t col = kb * 128u + 8u * l;   // and col + 64
+        uint32_t src = row;
+        if (a.rows && in) src = static_cast<uint32_t>(__ldg(a.rows + row));   // a negative index is a large one
+        const bool ok = in && src < a.x_rows;
+        const __nv_bfloat16 *px = a.x + (static_cast<uint64_t>(src) * a.ldx + col);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const bool there = ok && kb * 128 + 64 * j + 8 * l < a.K;
+            const bool there = ok && col + 64u * j < a.K;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
             v[j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + 64 * j)) : zero;
             if constexpr (GATED) up[j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + a.K + 64 * j)) : zero;
@@ -205,13 +204,13 @@ __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_qu
                 for (int j = 0; j < 2; ++j) codes[j] = codes8<false>(w[j], s, 0.0f);
             }
         }
+        if (in) {
+            uint8_t *pq = a.q + (static_cast<uint64_t>(row) * a.K + col);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int col = kb * 128 + 64 * j + 8 * l;
-            if (kb >= 0 && col < a.K)
-                *reinterpret_cast<uint2 *>(a.q + static_cast<int64_t>(row) * a.K + col) = codes[j];
+            for (int j = 0; j < 2; ++j)
+                if (col + 64u * j < a.K) *reinterpret_cast<uint2 *>(pq + 64 * j) = codes[j];
+            if (l == 0) a.s[p] = s;
         }
-        if (kb >= 0 && l == 0) a.s[static_cast<int64_t>(row) * a.KB + kb] = s;
     }
 }
 

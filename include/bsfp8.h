@@ -368,7 +368,7 @@ int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const flo
  *    without rows (then x_rows >= M).  An index outside [0, x_rows) gives
  *    a row of zeros with scales 1 (a padding slot).
  * q: E4M3 [M, K] (16-byte aligned), s: fp32 [M, KB]; both fully overwritten.
- * K a multiple of 16; M, x_rows < 2^30, K < 2^29.  M = 0 or K = 0: nothing is
+ * K a multiple of 16; M, x_rows < 2^30, K < 2^29, ldx < 2^31.  M = 0 or K = 0: nothing is
  * enqueued.  NaN or infinite values give undefined codes in their own piece.
  * Returns FP8_OK or FP8_ERR_SHAPE / FP8_ERR_NULL / FP8_ERR_ALIGN /
  * FP8_ERR_MODE (flags) / FP8_ERR_CUDA. */
