@@ -254,7 +254,7 @@ __device__ __forceinline__ void count_tiles(const Tile128Args &a, Ctl *ctl) {
         if (lane == 0) ctl->tiles = a.mt * a.nt;
         return;
     }
-    int base = 0;
+    int base = 0, top = 0;   // tiles so far; the rows below `top` have an expert
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
         int lo = 0, hi = 0;
@@ -263,6 +263,17 @@ __device__ __forceinline__ void count_tiles(const Tile128Args &a, Ctl *ctl) {
             if (blockIdx.x == 0 && (lo != __ldg(a.offsets + e) || hi != __ldg(a.offsets + e + 1) || hi < lo))
                 atomicOr(a.status, STATUS_RECORD);
         }
+        // ranges that overlap (a bad table) are cut, so that there are never more tiles
+        // than a table of ascending rows can have
+        int most = hi;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, most, o);
+            if (lane >= o) most = max(most, v);
+        }
+        const int before = __shfl_up_sync(0xFFFFFFFFu, most, 1);
+        lo = max(lo, lane > 0 ? max(before, top) : top);
+        top = max(top, __shfl_sync(0xFFFFFFFFu, most, 31));
         const int n = hi > lo ? (hi - lo + T128_BM - 1) / T128_BM * a.nt : 0;
         int sum = n;
 #pragma unroll

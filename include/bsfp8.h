@@ -325,8 +325,8 @@ int64_t fp8_grouped_workspace_bytes(int32_t G);
  * acc = fma(sA * sB, sum, acc) in fp32, K ascending.  AUTO splits K between
  * CTAs where the tiles alone would leave the GPU idle (few rows), and adds the
  * parts in a fixed order: a call repeats bit for bit, but a row's last bits may
- * differ between calls of different M.  PROMOTE never splits and uses one
- * tile shape, so each row's bits are the same for every M.
+ * differ between calls of different M.  PROMOTE never splits K, so
+ * each row's bits are the same for every M.
  * FP8_PATH_NATIVE promises power-of-two scales (FP8_QUANT_POW2 makes them). */
 
 /* Returns FP8_OK or FP8_ERR_SHAPE / FP8_ERR_NULL / FP8_ERR_ALIGN / FP8_ERR_CUDA
@@ -345,7 +345,8 @@ int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const fl
  * An expert may have any number of rows, none included; its weights are then
  * not read.  Rows of C outside [offsets[0], offsets[E]) are not written.  A
  * table that decreases or leaves [0, T] is clamped into [0, T], never
- * followed out of bounds, and reported as FP8_ERR_RECORD by fp8_status_query.
+ * followed out of bounds, and reported as FP8_ERR_RECORD by fp8_status_query;
+ * which rows of C are then written, and from which expert, is undefined.
  * E <= FP8_MAX_EXPERTS and E * N < 2^31; T == 0, N == 0 or E == 0: nothing is enqueued; K == 0
  * gives FP8_ERR_SHAPE.  Returns as fp8_gemm_block128(_ex). */
 #define FP8_MAX_EXPERTS 1024

@@ -154,6 +154,20 @@ def test_rows_do_not_depend_on_the_batch_when_pinned(bs):
         assert torch.equal(C.view(torch.int16), full[:m].view(torch.int16)), m
 
 
+def test_rows_do_not_depend_on_the_tile_width_when_pinned(bs):
+    """Enough rows for the 256-column tiles against few rows (128 columns)."""
+    M, N, K = 6000, 1032, 1168
+    p = Product(M, N, K, seed=15)
+    A, sA, B, sB = p.on(DEV)
+    full = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    bs.fp8_gemm_block128(A, sA, B, sB, full, mode=bs.FP8_PATH_PROMOTE)
+    for a, m in ((0, 100), (3000, 1), (5800, 200)):
+        C = torch.empty(m, N, dtype=torch.bfloat16, device=DEV)
+        bs.fp8_gemm_block128(A[a:a + m], sA[a:a + m], B, sB, C, mode=bs.FP8_PATH_PROMOTE)
+        torch.cuda.synchronize()
+        assert torch.equal(C.view(torch.int16), full[a:a + m].view(torch.int16)), (a, m)
+
+
 @pytest.mark.parametrize("M", [1, 20, 100, 600])
 def test_a_call_repeats_bit_for_bit(bs, M):
     p = Product(M, 520, 2064, seed=12)
@@ -244,6 +258,21 @@ def test_experts_bad_table_is_clamped_and_reported(bs, T):
         torch.cuda.synchronize()
         assert bs.fp8_status_query() == bs._abi.FP8_ERR_RECORD, off
         assert bs.fp8_status_query() == 0
+
+
+def test_experts_overlapping_table_ends(bs):
+    """Every expert claims all rows: clamped to disjoint ranges (tiles and split tiles),
+    reported, nothing written outside of C."""
+    for T, N, mode in ((900, 264, None), (40, 136, None), (3000, 1032, 1)):
+        E = 6
+        p = Product(T, N, 272, seed=10, E=E, pow2=True)
+        whole, C = _guarded(T, N)
+        bs.fp8_gemm_experts(*p.on(DEV), C, torch.tensor([0, T, 0, T, 0, T, 0], dtype=torch.int32, device=DEV), mode=mode)
+        torch.cuda.synchronize()
+        assert bs.fp8_status_query() == bs._abi.FP8_ERR_RECORD
+        assert torch.all(whole[0] == -7.0) and torch.all(whole[-1] == -7.0)
+        Cr, Tm = product(p.A, p.sA, p.B[0], p.sB[0])
+        check(bf16_to_f64(C), Cr, Tm, f"experts overlapping {T}")
 
 
 def test_experts_graph_follows_the_table(bs):
