@@ -176,15 +176,20 @@ def fp8_quantize_blocks(x, q=None, s=None, stream=None):
 # sizes).  A call of a few microseconds is bound by this marshalling: the checks are
 # written out, without helpers or tuples built per tensor.
 
-class _Types:
-    """torch's types, looked up once (torch is imported on first use)."""
+class _Calls:
+    """The library's functions and torch's types, looked up once (on first use)."""
     loaded = None
 
     def __init__(self):
         import torch
         self.codes = frozenset((torch.uint8, torch.float8_e4m3fn))
         self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
-        _Types.loaded = self
+        # the current stream of a device; the first call initialises CUDA
+        self.stream = torch._C._cuda_getCurrentRawStream
+        lib = library()
+        self.block128, self.experts = lib.fp8_gemm_block128_ex, lib.fp8_gemm_experts_ex
+        self.quantize, self.swiglu = lib.fp8_quantize_tokens, lib.fp8_swiglu_quantize_tokens
+        _Calls.loaded = self
 
 
 def _refused(what, *tensors):
@@ -206,15 +211,16 @@ def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
     N, kb = B.shape[0], (K + 127) // 128
     if (B.shape != (N, K) or C.shape != (M, N) or sA.shape != (M, kb) or sB.shape != ((N + 127) // 128, kb)):
         raise ValueError("fp8_gemm_block128: shapes of A, sA, B, sB, C do not match")
-    d = _Types.loaded or _Types()
+    d = _Calls.loaded or _Calls()
     if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
             and C.dtype is d.bf16 and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous()
             and sB.is_contiguous() and C.is_contiguous()
             and A.is_cuda and sA.is_cuda and B.is_cuda and sB.is_cuda and C.is_cuda):
         raise _refused("fp8_gemm_block128", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
                        ("sB", sB, d.f32), ("C", C, d.bf16))
-    rc = library().fp8_gemm_block128_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), M, N,
-                                        K, FP8_PATH_AUTO if mode is None else mode, _stream(stream))
+    rc = d.block128(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), M, N, K,
+                    FP8_PATH_AUTO if mode is None else mode,
+                    d.stream(A.get_device()) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_gemm_block128")
     return C
@@ -232,16 +238,16 @@ def fp8_gemm_experts(A, sA, B, sB, C, offsets, stream=None, mode=None):
     if (B.shape != (E, N, K) or C.shape != (T, N) or sA.shape != (T, kb)
             or sB.shape != (E, (N + 127) // 128, kb) or offsets.shape != (E + 1,)):
         raise ValueError("fp8_gemm_experts: shapes of A, sA, B, sB, C, offsets do not match")
-    d = _Types.loaded or _Types()
+    d = _Calls.loaded or _Calls()
     if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
             and C.dtype is d.bf16 and offsets.dtype is d.i32 and A.is_contiguous() and sA.is_contiguous()
             and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous() and offsets.is_contiguous()
             and A.is_cuda and sA.is_cuda and B.is_cuda and sB.is_cuda and C.is_cuda and offsets.is_cuda):
         raise _refused("fp8_gemm_experts", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
                        ("sB", sB, d.f32), ("C", C, d.bf16), ("offsets", offsets, d.i32))
-    rc = library().fp8_gemm_experts_ex(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(),
-                                       offsets.data_ptr(), T, N, K, E, FP8_PATH_AUTO if mode is None else mode,
-                                       _stream(stream))
+    rc = d.experts(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), offsets.data_ptr(), T, N, K,
+                   E, FP8_PATH_AUTO if mode is None else mode,
+                   d.stream(A.get_device()) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_gemm_experts")
     return C
@@ -260,15 +266,15 @@ def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
         q, s = _token_operands(M, K, q, s, x.device)
     if q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_quantize_tokens: q must be [M, K] and s [M, ceil(K/128)]")
-    d = _Types.loaded or _Types()
+    d = _Calls.loaded or _Calls()
     if rows is not None and not (rows.dtype is d.i32 and rows.dim() == 1 and rows.is_contiguous() and rows.is_cuda):
         raise _refused("fp8_quantize_tokens (rows: a vector)", ("rows", rows, d.i32))
     if not (x.dtype is d.bf16 and q.dtype in d.codes and s.dtype is d.f32 and q.is_contiguous()
             and s.is_contiguous() and (x.stride(1) == 1 or K <= 1) and x.is_cuda and q.is_cuda and s.is_cuda):
         raise _refused("fp8_quantize_tokens", ("x", x, d.bf16), ("q", q, d.codes), ("s", s, d.f32))
-    rc = library().fp8_quantize_tokens(x.data_ptr(), x.stride(0) if R > 1 else K, R,
-                                       None if rows is None else rows.data_ptr(), q.data_ptr(), s.data_ptr(), M, K,
-                                       FP8_QUANT_POW2 if pow2 else 0, _stream(stream))
+    rc = d.quantize(x.data_ptr(), x.stride(0) if R > 1 else K, R, None if rows is None else rows.data_ptr(),
+                    q.data_ptr(), s.data_ptr(), M, K, FP8_QUANT_POW2 if pow2 else 0,
+                    d.stream(x.get_device()) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_quantize_tokens")
     return q, s
@@ -283,12 +289,13 @@ def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
         q, s = _token_operands(M, K, q, s, x.device)
     if K2 % 2 or q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_swiglu_quantize_tokens: x is [M, 2K], q [M, K] and s [M, ceil(K/128)]")
-    d = _Types.loaded or _Types()
+    d = _Calls.loaded or _Calls()
     if not (x.dtype is d.bf16 and q.dtype in d.codes and s.dtype is d.f32 and q.is_contiguous()
             and s.is_contiguous() and (x.stride(1) == 1 or K2 <= 1) and x.is_cuda and q.is_cuda and s.is_cuda):
         raise _refused("fp8_swiglu_quantize_tokens", ("x", x, d.bf16), ("q", q, d.codes), ("s", s, d.f32))
-    rc = library().fp8_swiglu_quantize_tokens(x.data_ptr(), x.stride(0) if M > 1 else K2, q.data_ptr(), s.data_ptr(),
-                                              M, K, FP8_QUANT_POW2 if pow2 else 0, _stream(stream))
+    rc = d.swiglu(x.data_ptr(), x.stride(0) if M > 1 else K2, q.data_ptr(), s.data_ptr(), M, K,
+                  FP8_QUANT_POW2 if pow2 else 0,
+                  d.stream(x.get_device()) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_swiglu_quantize_tokens")
     return q, s

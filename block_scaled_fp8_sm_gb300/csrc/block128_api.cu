@@ -173,9 +173,21 @@ int split_of(int64_t tiles, int KB, int sms) {
     return split;
 }
 
+// The form of one product.
+//
+// Rows: up to 8 rows always (1 x 4096 x 7168 6.4 us against 9.2 by tiles, 1 x 28672 x 8192
+// 37 against 47).  Up to 64 rows where B is small: each group of 16 rows costs the rows form
+// about 2.3 us + 0.24 us per MB of B, a launch of tiles 5.6 us + 0.14 us per MB in all
+// (16 x 4096 x 7168 9.3 / 9.2 us; 32 x 2048 x 4096 6.6 / 7.7; 64 x 1024 x 2048 4.3 / 7.0; 64
+// x 8192 x 512 9.8 / 4.6).
+//
+// Tiles of 128 x 256 once they fill the SMs (4096^3 61 us; 72 with 128 columns), else of
+// 128 x 128 with K split over clusters (37 x 4104 x 7184 10 us; 19 unsplit).
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
-    if (!pinned && a.M <= 8) return launch_rows<1, 2, 8, 3>(a, 1, d, stream);
+    if (!pinned && a.M <= 8)
+        return (a.N + ROWS_N - 1) / ROWS_N <= 2 * d->sm_count ? launch_rows<1, 4, 8, 2>(a, 1, d, stream)
+                                                              : launch_rows<1, 4, 4, 4>(a, 1, d, stream);
     const int64_t groups = (a.M + 15) / 16;
     if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
         return launch_rows<2, 1, 8, 3>(a, groups, d, stream);
@@ -189,11 +201,14 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
 }
 
 // Experts: the row counts are on the device, so the rule goes by what is possible: at
-// most min(E, T) + T / 128 row tiles.
+// most min(E, T) + T / 128 row tiles.  Rows up to four on average (rows / tiles: 64 rows
+// over 16 experts of 4096 x 7168 70 / 73 us, 96 rows 80 / 73; 32 over 8 of 1024 x 2048 4.9 /
+// 7.5; 256 over 64 of 4096 x 2048 86 / 83, 384 97 / 84).  256-column tiles where they can
+// fill the SMs (16 experts, 532 rows of 4096 x 7168: 77 us, 87 with 128 columns).
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 4 * static_cast<int64_t>(a.E))
-        return launch_rows<1, 2, 4, 8>(a, a.M < a.E ? a.M : a.E, d, stream);
+        return launch_rows<1, 2, 4, 6>(a, a.M < a.E ? a.M : a.E, d, stream);
     const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
     const int64_t wide = most * ((a.N + 255) / 256), narrow = most * ((a.N + 127) / 128);
     if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);

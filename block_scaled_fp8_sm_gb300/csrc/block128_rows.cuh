@@ -11,17 +11,20 @@
 // fp32, then acc += (sA sB) * sum in fp32; the warps' sums are added in
 // warp order.  A row's bits do not depend on the other rows.
 //
-// One product has few CTAs (256 for 4096 columns): eight warps each, U = 2 blocks loaded
-// ahead, three CTAs on an SM (1 x 4096 x 7168: 6.1 us; U = 4, two CTAs 6.3; four warps,
-// eight CTAs 8.2).  Experts have many: four warps, eight CTAs on an SM, whose loads
-// cover one another's starts and sums (24 rows over 22 of 64 experts of 4096 x 7168:
-// 89 us; eight warps and three CTAs 97; U = 4, two CTAs 110).
+// What bounds a launch is how many bytes of B are on their way.  Up to two CTAs for each
+// SM (4096 columns: 256): eight warps, U = 4 blocks loaded ahead, two CTAs on an SM (1 x
+// 4096 x 7168, weights not in L2: 8.3 us; U = 2 and three CTAs 9.2, four warps 9.4; in L2
+// 6.4).  More CTAs: four warps, U = 4, four CTAs on an SM (8 x 16384 x 8192 25.0 us, 5.4
+// TB/s; the former 28.5, U = 2 and eight warps 26.8).  Experts, where each CTA first finds
+// its expert: four warps, U = 2, six CTAs, whose loads cover one another's starts (24 rows
+// over 64 experts of 4096 x 7168: 85.7 us, 6.5 TB/s; U = 4 and four CTAs 90; eight CTAs of
+// 64 registers 89).
 //
 // Every launch may be set up while the previous kernel ends (programmatic dependent
 // launch); NEXT, a launch whose CTAs all fit on the GPU at once (one token: 256), also lets
 // the next one in after its K loop: 1 x 4096 x 7168 in a stream of calls 8.2 -> 6.4 us.  At
 // its start the next launch's CTAs would take its places on the SMs (7.6 us), and launches
-// of several waves lose by it (24 rows over 64 experts 101 -> 115 us).
+// of several waves lose by it (24 rows over 64 experts 89 -> 115 us).
 //
 // The K order inside a block is permuted alike on both sides: lane t of a
 // quad holds bytes 64 j + 16 t .. + 15 (j = 0, 1), so a load of a warp covers 64
