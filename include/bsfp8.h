@@ -327,7 +327,12 @@ int64_t fp8_grouped_workspace_bytes(int32_t G);
  * parts in a fixed order: a call repeats bit for bit, but a row's last bits may
  * differ between calls of different M.  PROMOTE never splits K, so
  * each row's bits are the same for every M.
- * FP8_PATH_NATIVE promises power-of-two scales (FP8_QUANT_POW2 makes them). */
+ * FP8_PATH_NATIVE promises positive normal power-of-two scales (FP8_QUANT_POW2
+ * makes them): where there are enough tiles for it, the block-scaled
+ * tensor-core path applies them inside the MMA; a scale that is not one is
+ * then reported as FP8_ERR_SCALE by fp8_status_query and the results it takes
+ * part in are undefined.  Fewer rows take AUTO's forms, which multiply by any
+ * scale. */
 
 /* Returns FP8_OK or FP8_ERR_SHAPE / FP8_ERR_NULL / FP8_ERR_ALIGN / FP8_ERR_CUDA
  * (and FP8_ERR_MODE for an unknown mode).  M == 0 or N == 0: nothing is
