@@ -190,7 +190,8 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
                                                               : launch_rows<1, 4, 4, 4>(a, 1, d, stream);
     const int64_t groups = (a.M + 15) / 16;
     if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
-        return launch_rows<2, 1, 8, 3>(a, groups, d, stream);
+        return (a.N + ROWS_N - 1) / ROWS_N * groups <= 2 * d->sm_count ? launch_rows<2, 1, 8, 2>(a, groups, d, stream)
+                                                                       : launch_rows<2, 2, 4, 4>(a, groups, d, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
     if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
