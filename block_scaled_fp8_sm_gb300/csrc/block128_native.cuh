@@ -189,11 +189,11 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
                 for (int r = 0; r < 3; ++r) {
                     float v[4];
                     if (vec) {
-                        const float4 x = __ldg(reinterpret_cast<const float4 *>(row[r] + kb));
+                        const float4 x = *reinterpret_cast<const float4 *>(row[r] + kb);
                         v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = __ldg(row[r] + min(kb + j, a.KB - 1));
+                        for (int j = 0; j < 4; ++j) v[j] = row[r][min(kb + j, a.KB - 1)];
                     }
                     word[r] = 0u;
 #pragma unroll

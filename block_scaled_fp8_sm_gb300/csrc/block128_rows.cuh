@@ -54,6 +54,11 @@ constexpr int ROWS_N = 16;   // rows of B per CTA
 
 // Programmatic dependent launch: the next kernel of the stream may be set up while this
 // one runs, and waits for this one's end (and its memory) before it reads or writes.
+//
+// So a kernel is live while the one before it still writes, and whatever that one may have
+// written (a quantizer's codes and scales, a product's rows, any operand) is not read-only
+// for the kernel's life: the kernels launched this way read global memory with ordinary
+// loads, which the wait orders, and never through the non-coherent path.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -64,15 +69,15 @@ __device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg16_if(const uint8_t *p, bool ok) {
-    return ok ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ uint4 load16_if(const uint8_t *p, bool ok) {
+    return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Rows of expert e: offsets clamped to [0, T]; a table that decreases or leaves
 // [0, T] gives clamped ranges.
 __device__ __forceinline__ void expert_rows(const int32_t *offsets, int e, int T, int &lo, int &hi) {
-    lo = min(max(__ldg(offsets + e), 0), T);
-    hi = min(max(__ldg(offsets + e + 1), 0), T);
+    lo = min(max(offsets[e], 0), T);
+    hi = min(max(offsets[e + 1], 0), T);
 }
 
 // The `slot`-th expert that has rows (-1: there are fewer), found by the whole
@@ -89,7 +94,7 @@ __device__ __forceinline__ int busy_expert(const int32_t *offsets, int E, int T,
         int lo = 0, hi = 0;
         if (e < E) {
             expert_rows(offsets, e, T, lo, hi);
-            if (last && blockIdx.x == 0 && (lo != __ldg(offsets + e) || hi != __ldg(offsets + e + 1) || hi < lo))
+            if (last && blockIdx.x == 0 && (lo != offsets[e] || hi != offsets[e + 1] || hi < lo))
                 atomicOr(status, STATUS_RECORD);
         }
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, hi > lo);
@@ -143,8 +148,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const Ro
                 for (int j = 0; j < 2; ++j) {
                     const int k = (kb0 + u * WARPS) * 128 + 64 * j;   // sizes are below 2^30: no overflow
                     const bool in = k + 16 * t < a.K;
-                    w0[u][j] = ldg16_if(B0 + k, in);
-                    w1[u][j] = ldg16_if(B1 + k, in && ok1);
+                    w0[u][j] = load16_if(B0 + k, in);
+                    w1[u][j] = load16_if(B1 + k, in && ok1);
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -154,13 +159,13 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const Ro
                     for (int j = 0; j < 2; ++j) {
                         const int k = (kb0 + u * WARPS) * 128 + 64 * j + 16 * t;
                         const int m = m0 + 8 * n + g;
-                        x[u][n][j] = ldg16_if(a.A + static_cast<int64_t>(m) * a.K + k, m < hi && k < a.K);
+                        x[u][n][j] = load16_if(a.A + static_cast<int64_t>(m) * a.K + k, m < hi && k < a.K);
                     }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int kb = kb0 + u * WARPS;
                 if (kb < a.KB) {
-                    const float sb = __ldg(sB + kb);
+                    const float sb = sB[kb];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -171,8 +176,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const Ro
                         }
                         const int m = m0 + 8 * n + 2 * t;
                         const float *s = a.sA + static_cast<int64_t>(m) * a.KB + kb;
-                        const float s0 = m < hi ? __ldg(s) * sb : 0.0f;
-                        const float s1 = m + 1 < hi ? __ldg(s + a.KB) * sb : 0.0f;
+                        const float s0 = m < hi ? s[0] * sb : 0.0f;
+                        const float s1 = m + 1 < hi ? s[a.KB] * sb : 0.0f;
                         acc[n][0] = fmaf(s0, p[0], acc[n][0]);
                         acc[n][1] = fmaf(s1, p[1], acc[n][1]);
                         acc[n][2] = fmaf(s0, p[2], acc[n][2]);

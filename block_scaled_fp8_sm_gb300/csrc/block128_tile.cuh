@@ -260,7 +260,7 @@ __device__ __forceinline__ void count_tiles(const Tile128Args &a, Ctl *ctl) {
         int lo = 0, hi = 0;
         if (e < a.E) {
             expert_rows(a.offsets, e, a.M, lo, hi);
-            if (blockIdx.x == 0 && (lo != __ldg(a.offsets + e) || hi != __ldg(a.offsets + e + 1) || hi < lo))
+            if (blockIdx.x == 0 && (lo != a.offsets[e] || hi != a.offsets[e + 1] || hi < lo))
                 atomicOr(a.status, STATUS_RECORD);
         }
         // ranges that overlap (a bad table) are cut, so that there are never more tiles
@@ -438,8 +438,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             psa = a.sA + static_cast<int64_t>(m) * a.KB;
             psb = a.sB + (static_cast<int64_t>(tt.e) * a.NB + nb) * a.KB;
             if (kb0 < kb1) {
-                sa = __ldg(psa + kb0);
-                sb = __ldg(psb + kb0);
+                sa = psa[kb0];
+                sb = psb[kb0];
             }
         };
         if (unit < tiles) begin(unit);
@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             for (int kb = kb0; kb < kb1; ++kb) {
                 const float sc = sa * sb;
                 const int next = min(kb + 1, kb1 - 1);
-                sa = __ldg(psa + next);
-                sb = __ldg(psb + next);
+                sa = psa[next];
+                sb = psb[next];
                 ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->tfull[b], bph, ctl, a));
                 if (!ok) break;
                 tc_fence_after();

@@ -129,15 +129,15 @@ __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_qu
         const uint32_t kb = p - row * a.KB;
         const uint32_t col = kb * 128u + 8u * l;   // and col + 64
         uint32_t src = row;
-        if (a.rows && in) src = static_cast<uint32_t>(__ldg(a.rows + row));   // a negative index is a large one
+        if (a.rows && in) src = static_cast<uint32_t>(a.rows[row]);   // a negative index is a large one
         const bool ok = in && src < a.x_rows;
         const __nv_bfloat16 *px = a.x + (static_cast<uint64_t>(src) * a.ldx + col);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const bool there = ok && col + 64u * j < a.K;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            v[j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + 64 * j)) : zero;
-            if constexpr (GATED) up[j] = there ? __ldg(reinterpret_cast<const uint4 *>(px + a.K + 64 * j)) : zero;
+            v[j] = there ? *reinterpret_cast<const uint4 *>(px + 64 * j) : zero;
+            if constexpr (GATED) up[j] = there ? *reinterpret_cast<const uint4 *>(px + a.K + 64 * j) : zero;
         }
         uint32_t w[2][4];
         uint64_t y[2][4];
