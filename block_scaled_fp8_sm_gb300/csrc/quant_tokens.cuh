@@ -54,7 +54,8 @@ __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
     constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
     uint32_t g0, g1;
     f32x2_unpack(g, g0, g1);
-    const uint64_t a = f32x2_pack(g0 & 0x7FFFFFFFu, g1 & 0x7FFFFFFFu);   // |g|
+    // |g|, at most 256: exp(-256) is zero in fp32, and the product below stays finite
+    const uint64_t a = f32x2_of(fminf(fabsf(__uint_as_float(g0)), 256.0f), fminf(fabsf(__uint_as_float(g1)), 256.0f));
     const uint64_t t = mul_f32x2_rn(a, f32x2_of(-kL, -kL));
     uint64_t lo = fma_f32x2_rn(a, f32x2_of(kL, kL), t);   // |g| log2(e) + t = -t_lo
     lo = fma_f32x2_rn(a, f32x2_of(kLlo, kLlo), lo);

@@ -1,0 +1,76 @@
+"""The gated quantizer over the whole range of bf16 gates and ups, against silu(gate) up in
+64 bits.
+
+Error of the kernel's y: the sigmoid's exponential is the square of one taken at half the
+argument (2 ulp of 2^-23, twice: 2^-21; its correction and the square, three roundings of
+2^-24), 1 + e and the reciprocal (2^-24 and 2^-23), the products (four of 2^-24): together
+2^-21 + 2^-23 + 8 * 2^-24 = 1.125 * 2^-20.  The quotient by the scale adds an ulp, 2^-23:
+1.25 * 2^-20.  A code may be half a step and that much of the value off; a scale that much of
+itself, or, rounded up to a power of two, one power where the unrounded one is that near."""
+import numpy as np
+import pytest
+import torch
+
+from tests._block128 import TABLE, blocks, quantized
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TOL = 1.25 * 2.0 ** -20
+MAX = float(torch.finfo(torch.bfloat16).max)
+
+
+@pytest.fixture(scope="module")
+def bs():
+    import block_scaled_fp8_sm_gb300 as mod
+    from block_scaled_fp8_sm_gb300 import build
+    build.build()
+    mod.library()
+    return mod
+
+
+def _silu_mul(gate, up):
+    g, u = gate.double().numpy(), up.double().numpy()
+    with np.errstate(over="ignore"):
+        return g / (1 + np.exp(-g)) * u
+
+
+def _check(q, s, y, pow2, what):
+    """Pieces of finite y; one below 2^-100 counts as all zero by definition."""
+    y = y.copy()
+    for b in range(blocks(y.shape[1])):
+        piece = y[:, b * 128:(b + 1) * 128]
+        piece[np.abs(piece).max(axis=1) < 2.0 ** -100] = 0.0
+    got, got_s = TABLE[q.cpu().numpy()], s.cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(got)), f"{what}: NaN codes"
+    _, ws = quantized(y, False)
+    if pow2:
+        near = [quantized(y * (1 + d), True)[1] for d in (-TOL, 0.0, TOL)]
+        assert np.all((got_s == near[0]) | (got_s == near[1]) | (got_s == near[2])), what
+    else:
+        assert np.all(np.abs(got_s - ws) <= TOL * ws), what
+    v = y / np.repeat(got_s, 128, 1)[:, :y.shape[1]]
+    _, e = np.frexp(np.maximum(np.abs(v), 2.0 ** -6))
+    step = np.ldexp(1.0, e - 4)
+    off = np.abs(got - np.clip(v, -448, 448)) - (step / 2 + TOL * np.abs(v))
+    assert np.all(off <= 0), f"{what}: {int((off > 0).sum())} codes, first at {np.argwhere(off > 0)[0]}"
+
+
+def _run(bs, gate, up, pow2, what):
+    x = torch.cat([gate, up], dim=1).to(torch.bfloat16)
+    K = gate.shape[1]
+    q, s = bs.fp8_swiglu_quantize_tokens(x.to(DEV), pow2=pow2)
+    torch.cuda.synchronize()
+    _check(q, s, _silu_mul(x[:, :K], x[:, K:]), pow2, what)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("up", [1.0, 1e-3, -1e-30, 0.0])
+def test_largest_gates(bs, up, pow2):
+    """|gate| log2(e) passes the largest fp32 number from 2.36e38 on."""
+    big = torch.tensor([2.3e38, 2.4e38, 3e38, MAX, -2.3e38, -2.4e38, -3e38, -MAX])
+    g = torch.Generator().manual_seed(1)
+    gate = torch.randn(9, 272, generator=g)
+    gate[:8, 5], gate[:8, 140] = big, big.flip(0)
+    gate[8] = -MAX                        # nothing but zeros
+    u = torch.randn(9, 272, generator=g).sign() * up
+    _run(bs, gate, u, pow2, f"largest gates, up {up}")
