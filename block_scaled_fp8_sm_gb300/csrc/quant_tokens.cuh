@@ -12,7 +12,7 @@
 // by the reciprocal of the pieces per row.  Loads in flight come from resident warps (64
 // of them an SM, 48 where the arithmetic needs 40 registers), not from pieces loaded ahead:
 // 16384 x 7168 gathered from 4096 tokens 36.6 us (180 MB at the copy bandwidth 27; L2 serves
-// the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 58.5 us (49: integer and
+// the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 60.6 us (49: integer and
 // conversion work); two pieces ahead with half the warps 41 / 57 / 65.
 #pragma once
 #include <cuda_bf16.h>
@@ -46,35 +46,39 @@ __device__ __forceinline__ uint64_t f32x2_of(float lo, float hi) {
     return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi));
 }
 
-// silu(g) u on two values.  exp(-|g|) = 2^t, t = -|g| log2(e): the product's rounding
-// error comes from an fma (Dekker's error-free product) and enters as 2^t (1 + t_lo ln 2);
-// the sigmoid is r = 1 / (1 + e), or e r for negative g, so no exponential overflows and
-// small results keep their relative precision.
+// silu(g) u on two values.  n = exp(-|g| / 2) = 2^t, t = -|g| log2(e) / 2: the product's
+// rounding error comes from an fma (Dekker's error-free product) and enters as 2^t (1 +
+// t_lo ln 2).  With r = 1 / (1 + n^2) and m = n for negative g, else 1, the sigmoid is m^2 r,
+// and the result (g m) (u m r): neither half leaves fp32's normal range where the result is
+// in it (at least 2^-100), since |g| m < 1 for negative g and, with the half of the
+// exponential, u m r is no smaller than the result; exp(g) itself is subnormal from g = -87
+// on, and g, u or g u may be out of range where the result is not.
 __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
-    constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
+    constexpr float kL = 0x1.715476p-1f, kLlo = 0x1.4ae0cp-27f, kLn2 = 0x1.62e43p-1f;   // log2(e) / 2 = kL + kLlo
     uint32_t g0, g1;
     f32x2_unpack(g, g0, g1);
-    // |g|, at most 256: exp(-256) is zero in fp32, and the product below stays finite
+    // |g|, at most 256: exp(-128) is zero in fp32, and the product below stays finite
     const uint64_t a = f32x2_of(fminf(fabsf(__uint_as_float(g0)), 256.0f), fminf(fabsf(__uint_as_float(g1)), 256.0f));
     const uint64_t t = mul_f32x2_rn(a, f32x2_of(-kL, -kL));
-    uint64_t lo = fma_f32x2_rn(a, f32x2_of(kL, kL), t);   // |g| log2(e) + t = -t_lo
+    uint64_t lo = fma_f32x2_rn(a, f32x2_of(kL, kL), t);   // |g| log2(e) / 2 + t = -t_lo
     lo = fma_f32x2_rn(a, f32x2_of(kLlo, kLlo), lo);
     uint32_t t0, t1;
     f32x2_unpack(t, t0, t1);
-    float e0, e1;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e0) : "f"(__uint_as_float(t0)));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e1) : "f"(__uint_as_float(t1)));
-    uint64_t e = f32x2_of(e0, e1);
-    e = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(-kLn2, -kLn2)), e, e);
-    uint32_t b0, b1;
-    f32x2_unpack(e, b0, b1);
+    float n0, n1;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(n0) : "f"(__uint_as_float(t0)));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(n1) : "f"(__uint_as_float(t1)));
+    uint64_t n = f32x2_of(n0, n1);
+    n = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(-kLn2, -kLn2)), n, n);
+    uint32_t e0, e1, m0, m1;
+    f32x2_unpack(mul_f32x2_rn(n, n), e0, e1);
     float r0, r1;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(1.0f + __uint_as_float(b0)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(1.0f + __uint_as_float(b1)));
-    const uint32_t n0 = static_cast<int32_t>(g0) < 0 ? b0 : 0x3F800000u;   // e for negative g, else 1
-    const uint32_t n1 = static_cast<int32_t>(g1) < 0 ? b1 : 0x3F800000u;
-    const uint64_t sig = mul_f32x2_rn(f32x2_pack(n0, n1), f32x2_of(r0, r1));
-    return mul_f32x2_rn(mul_f32x2_rn(g, sig), u);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(1.0f + __uint_as_float(e0)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(1.0f + __uint_as_float(e1)));
+    f32x2_unpack(n, m0, m1);
+    m0 = static_cast<int32_t>(g0) < 0 ? m0 : 0x3F800000u;
+    m1 = static_cast<int32_t>(g1) < 0 ? m1 : 0x3F800000u;
+    const uint64_t m = f32x2_pack(m0, m1);
+    return mul_f32x2_rn(mul_f32x2_rn(g, m), mul_f32x2_rn(u, mul_f32x2_rn(m, f32x2_of(r0, r1))));
 }
 
 // The E4M3 codes of eight values, in order.

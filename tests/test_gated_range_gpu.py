@@ -74,3 +74,26 @@ def test_largest_gates(bs, up, pow2):
     gate[8] = -MAX                        # nothing but zeros
     u = torch.randn(9, 272, generator=g).sign() * up
     _run(bs, gate, u, pow2, f"largest gates, up {up}")
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_small_sigmoids_keep_their_precision(bs, pow2):
+    """Gates below -87, whose exponential fp32 cannot hold in full, with ups that bring the
+    result back into range; every piece has values of one magnitude."""
+    g = torch.Generator().manual_seed(2)
+    base = torch.linspace(-172, -84, 64)[:, None]
+    gate = base + torch.randn(64, 384, generator=g) * 0.3
+    up = torch.randn(64, 384, generator=g).clamp(-3, 3) * torch.logspace(24, 38, 64).flip(0)[:, None]
+    _run(bs, gate, up, pow2, "small sigmoids")
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_factors_at_the_ends_of_the_range(bs, pow2):
+    """Subnormal gates with large ups and the other way round, and products next to the
+    largest fp32 number."""
+    g = torch.Generator().manual_seed(3)
+    n = lambda: torch.randn(4, 256, generator=g)   # noqa: E731
+    small, large = torch.tensor([2.0 ** -133, 2.0 ** -130, 2.0 ** -127, 2.0 ** -126])[:, None], 1e30
+    _run(bs, n() * small, n() * large, pow2, "subnormal gates")
+    _run(bs, n().abs() * large, n() * small, pow2, "subnormal ups")
+    _run(bs, 0.5 + n().abs() / 8, n().sign() * MAX, pow2, "largest ups")   # silu(1.4) < 1
