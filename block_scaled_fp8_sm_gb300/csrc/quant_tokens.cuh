@@ -190,7 +190,10 @@ __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_qu
                 codes[0] = codes[1] = make_uint2(0u, 0u);
             } else {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) codes[j] = POW2 ? codes8_pow2(y[j], f) : codes8_f32(y[j], s, f);
+                for (int j = 0; j < 2; ++j)
+                    // an infinite scale (y past the largest fp32 number): f is zero, and a finite factor
+                    // in the remainder leaves 0 for finite y and NaN for infinite ones
+                    codes[j] = POW2 ? codes8_pow2(y[j], f) : codes8_f32(y[j], fminf(s, 3.40282347e38f), f);
             }
         } else if constexpr (POW2) {
             s = pow2_up(block_scale(amax));

@@ -385,7 +385,10 @@ int fp8_quantize_tokens(const void *x, int64_t ldx, int64_t x_rows, const int32_
 /* The same of the gated activation between an expert's two products:
  * y = silu(gate) * up = gate / (1 + exp(-gate)) * up, in fp32, with gate in
  * columns [0, K) and up in columns [K, 2K) of x (M rows, ldx >= 2K).  A piece
- * whose largest |y| is below 2^-100 counts as all zero. */
+ * whose largest |y| is below 2^-100 counts as all zero: its scale is 1 and its
+ * codes are 0.  Where finite gate and up give a y past the largest fp32 number,
+ * the piece's scale is infinite, that y's code NaN and the codes of the piece's
+ * finite values 0. */
 int fp8_swiglu_quantize_tokens(const void *x, int64_t ldx, void *q, float *s, int64_t M, int64_t K, int flags,
                                cudaStream_t stream);
 

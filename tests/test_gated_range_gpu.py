@@ -97,3 +97,28 @@ def test_factors_at_the_ends_of_the_range(bs, pow2):
     _run(bs, n() * small, n() * large, pow2, "subnormal gates")
     _run(bs, n().abs() * large, n() * small, pow2, "subnormal ups")
     _run(bs, 0.5 + n().abs() / 8, n().sign() * MAX, pow2, "largest ups")   # silu(1.4) < 1
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_products_past_the_largest_number(bs, pow2):
+    """Finite gates and ups whose product fp32 cannot hold: as the quotient by an infinite
+    scale gives, NaN for these values and zero for the rest of their piece."""
+    g = torch.Generator().manual_seed(4)
+    gate, up = torch.randn(6, 400, generator=g), torch.randn(6, 400, generator=g)
+    gate[1, 130], up[1, 130] = 1e30, -1e30
+    gate[4, 399], up[4, 399] = 3.0, MAX
+    x = torch.cat([gate, up], dim=1).to(torch.bfloat16)
+    q, s = bs.fp8_swiglu_quantize_tokens(x.to(DEV), pow2=pow2)
+    torch.cuda.synchronize()
+    got, got_s = TABLE[q.cpu().numpy()], s.cpu().numpy()
+    want = np.zeros((6, 400))
+    want[1, 130] = want[4, 399] = np.nan
+    for row, piece in ((1, slice(128, 256)), (4, slice(384, 400))):
+        assert got_s[row, piece.start // 128] == np.inf
+        assert np.array_equal(got[row, piece], want[row, piece], equal_nan=True), (row, got[row, piece])
+    assert int(np.isinf(got_s).sum()) == 2
+    y = _silu_mul(x[:, :400], x[:, 400:])
+    for b in range(4):
+        keep = ~np.isinf(got_s[:, b])
+        cols = slice(b * 128, min(400, b * 128 + 128))
+        _check(q[keep][:, cols], s[keep][:, b:b + 1], y[keep, cols], pow2, f"beside infinite values, piece {b}")
