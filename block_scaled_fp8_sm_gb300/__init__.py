@@ -173,7 +173,7 @@ def fp8_quantize_blocks(x, q=None, s=None, stream=None):
 
 
 # The 128-granular calls check what the C entry points cannot see (they get addresses and
-# sizes).  A call of a few microseconds is bound by this marshalling: the checks are
+# sizes): types, layouts, and that every tensor is on the current device.  A call of a few microseconds is bound by this marshalling: the checks are
 # written out, without helpers or tuples built per tensor.
 
 class _Calls:
@@ -184,8 +184,8 @@ class _Calls:
         import torch
         self.codes = frozenset((torch.uint8, torch.float8_e4m3fn))
         self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
-        # the current stream of a device; the first call initialises CUDA
-        self.stream = torch._C._cuda_getCurrentRawStream
+        # the current device, and the current stream of a device
+        self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         lib = library()
         self.block128, self.experts = lib.fp8_gemm_block128_ex, lib.fp8_gemm_experts_ex
         self.quantize, self.swiglu = lib.fp8_quantize_tokens, lib.fp8_swiglu_quantize_tokens
@@ -193,10 +193,17 @@ class _Calls:
 
 
 def _refused(what, *tensors):
-    """The ValueError for tensors that are not contiguous CUDA tensors of their types."""
+    """The ValueError for tensors that are not contiguous CUDA tensors of their types on
+    the current device (the library launches there)."""
     for name, t, kind in tensors:
         if not (t.dtype in kind if isinstance(kind, frozenset) else t.dtype is kind):
             return ValueError(f"{what}: {name} has type {t.dtype}")
+    devices = [t.get_device() for _, t, _ in tensors]
+    if min(devices) >= 0:
+        where = ", ".join(f"{name} on {d}" for (name, _, _), d in zip(tensors, devices))
+        current = _Calls.loaded.device()
+        if any(d != current for d in devices):
+            return ValueError(f"{what}: tensors must be on the current device {current} ({where})")
     return ValueError(f"{what}: tensors must be contiguous and on the GPU")
 
 
@@ -212,15 +219,17 @@ def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
     if (B.shape != (N, K) or C.shape != (M, N) or sA.shape != (M, kb) or sB.shape != ((N + 127) // 128, kb)):
         raise ValueError("fp8_gemm_block128: shapes of A, sA, B, sB, C do not match")
     d = _Calls.loaded or _Calls()
+    dev = A.get_device()   # -1: a host tensor
     if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
             and C.dtype is d.bf16 and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous()
             and sB.is_contiguous() and C.is_contiguous()
-            and A.is_cuda and sA.is_cuda and B.is_cuda and sB.is_cuda and C.is_cuda):
+            and dev >= 0 and sA.get_device() == dev and B.get_device() == dev and sB.get_device() == dev
+            and C.get_device() == dev and d.device() == dev):
         raise _refused("fp8_gemm_block128", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
                        ("sB", sB, d.f32), ("C", C, d.bf16))
     rc = d.block128(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), M, N, K,
                     FP8_PATH_AUTO if mode is None else mode,
-                    d.stream(A.get_device()) if stream is None else _stream(stream))
+                    d.stream(dev) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_gemm_block128")
     return C
@@ -239,15 +248,17 @@ def fp8_gemm_experts(A, sA, B, sB, C, offsets, stream=None, mode=None):
             or sB.shape != (E, (N + 127) // 128, kb) or offsets.shape != (E + 1,)):
         raise ValueError("fp8_gemm_experts: shapes of A, sA, B, sB, C, offsets do not match")
     d = _Calls.loaded or _Calls()
+    dev = A.get_device()
     if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
             and C.dtype is d.bf16 and offsets.dtype is d.i32 and A.is_contiguous() and sA.is_contiguous()
             and B.is_contiguous() and sB.is_contiguous() and C.is_contiguous() and offsets.is_contiguous()
-            and A.is_cuda and sA.is_cuda and B.is_cuda and sB.is_cuda and C.is_cuda and offsets.is_cuda):
+            and dev >= 0 and sA.get_device() == dev and B.get_device() == dev and sB.get_device() == dev
+            and C.get_device() == dev and offsets.get_device() == dev and d.device() == dev):
         raise _refused("fp8_gemm_experts", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
                        ("sB", sB, d.f32), ("C", C, d.bf16), ("offsets", offsets, d.i32))
     rc = d.experts(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(), C.data_ptr(), offsets.data_ptr(), T, N, K,
                    E, FP8_PATH_AUTO if mode is None else mode,
-                   d.stream(A.get_device()) if stream is None else _stream(stream))
+                   d.stream(dev) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_gemm_experts")
     return C
@@ -267,14 +278,17 @@ def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
     if q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_quantize_tokens: q must be [M, K] and s [M, ceil(K/128)]")
     d = _Calls.loaded or _Calls()
-    if rows is not None and not (rows.dtype is d.i32 and rows.dim() == 1 and rows.is_contiguous() and rows.is_cuda):
-        raise _refused("fp8_quantize_tokens (rows: a vector)", ("rows", rows, d.i32))
+    dev = x.get_device()
+    if rows is not None and not (rows.dtype is d.i32 and rows.dim() == 1 and rows.is_contiguous()
+                                 and rows.get_device() == dev):
+        raise _refused("fp8_quantize_tokens (rows: a vector)", ("rows", rows, d.i32), ("x", x, d.bf16))
     if not (x.dtype is d.bf16 and q.dtype in d.codes and s.dtype is d.f32 and q.is_contiguous()
-            and s.is_contiguous() and (x.stride(1) == 1 or K <= 1) and x.is_cuda and q.is_cuda and s.is_cuda):
+            and s.is_contiguous() and (x.stride(1) == 1 or K <= 1)
+            and dev >= 0 and q.get_device() == dev and s.get_device() == dev and d.device() == dev):
         raise _refused("fp8_quantize_tokens", ("x", x, d.bf16), ("q", q, d.codes), ("s", s, d.f32))
     rc = d.quantize(x.data_ptr(), x.stride(0) if R > 1 else K, R, None if rows is None else rows.data_ptr(),
                     q.data_ptr(), s.data_ptr(), M, K, FP8_QUANT_POW2 if pow2 else 0,
-                    d.stream(x.get_device()) if stream is None else _stream(stream))
+                    d.stream(dev) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_quantize_tokens")
     return q, s
@@ -290,12 +304,14 @@ def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
     if K2 % 2 or q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_swiglu_quantize_tokens: x is [M, 2K], q [M, K] and s [M, ceil(K/128)]")
     d = _Calls.loaded or _Calls()
+    dev = x.get_device()
     if not (x.dtype is d.bf16 and q.dtype in d.codes and s.dtype is d.f32 and q.is_contiguous()
-            and s.is_contiguous() and (x.stride(1) == 1 or K2 <= 1) and x.is_cuda and q.is_cuda and s.is_cuda):
+            and s.is_contiguous() and (x.stride(1) == 1 or K2 <= 1)
+            and dev >= 0 and q.get_device() == dev and s.get_device() == dev and d.device() == dev):
         raise _refused("fp8_swiglu_quantize_tokens", ("x", x, d.bf16), ("q", q, d.codes), ("s", s, d.f32))
     rc = d.swiglu(x.data_ptr(), x.stride(0) if M > 1 else K2, q.data_ptr(), s.data_ptr(), M, K,
                   FP8_QUANT_POW2 if pow2 else 0,
-                  d.stream(x.get_device()) if stream is None else _stream(stream))
+                  d.stream(dev) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_swiglu_quantize_tokens")
     return q, s
