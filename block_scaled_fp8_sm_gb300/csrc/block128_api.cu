@@ -72,17 +72,15 @@ int guarded(F body) {
     }
 }
 
-// Shapes and pointers common to both products.  FP8_OK with *empty set: nothing to do.
-int check_product(const void *A, const float *sA, const void *B, const float *sB, const void *C, int64_t M,
-                  int64_t N, int64_t K, int mode, bool *empty) {
-    *empty = false;
+// Mode and sizes of both products.
+int check_sizes(int64_t M, int64_t N, int64_t K, int mode) {
     if (mode != FP8_PATH_AUTO && mode != FP8_PATH_NATIVE && mode != FP8_PATH_PROMOTE) return FP8_ERR_MODE;
     if (M < 0 || N < 0 || K < 0 || M >= kLim || N >= kLim || K >= kLim) return FP8_ERR_SHAPE;
-    if (N % 8 != 0 || K % 16 != 0) return FP8_ERR_SHAPE;
-    if (M == 0 || N == 0) {
-        *empty = true;
-        return FP8_OK;
-    }
+    return N % 8 != 0 || K % 16 != 0 ? FP8_ERR_SHAPE : FP8_OK;
+}
+
+// Their pointers, once there is something to compute.
+int check_operands(const void *A, const float *sA, const void *B, const float *sB, const void *C, int64_t K) {
     if (!C) return FP8_ERR_NULL;
     if (!aligned(C, 16)) return FP8_ERR_ALIGN;
     if (K > 0) {
@@ -280,9 +278,10 @@ extern "C" {
 
 int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M,
                          int64_t N, int64_t K, int mode, cudaStream_t stream) {
-    bool empty;
-    int rc = check_product(A, sA, B, sB, C, M, N, K, mode, &empty);
-    if (rc != FP8_OK || empty) return rc;
+    int rc = check_sizes(M, N, K, mode);
+    if (rc != FP8_OK || M == 0 || N == 0) return rc;
+    rc = check_operands(A, sA, B, sB, C, K);
+    if (rc != FP8_OK) return rc;
     DeviceState *d = nullptr;
     rc = device_setup(&d);
     if (rc != FP8_OK) return rc;
@@ -300,10 +299,11 @@ int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float
 int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const float *sB, void *C,
                         const int32_t *offsets, int64_t T, int64_t N, int64_t K, int32_t E, int mode,
                         cudaStream_t stream) {
-    bool empty;
     if (E < 0 || E > FP8_MAX_EXPERTS || (N > 0 && N < kLim && E * N >= 2 * kLim)) return FP8_ERR_SHAPE;
-    int rc = check_product(A, sA, B, sB, C, T, N, K, mode, &empty);
-    if (rc != FP8_OK || empty || E == 0) return rc;
+    int rc = check_sizes(T, N, K, mode);
+    if (rc != FP8_OK || T == 0 || N == 0 || E == 0) return rc;   // without experts the weights are no memory at all
+    rc = check_operands(A, sA, B, sB, C, K);
+    if (rc != FP8_OK) return rc;
     if (!offsets) return FP8_ERR_NULL;
     if (!aligned(offsets, 4)) return FP8_ERR_ALIGN;
     if (K == 0) return FP8_ERR_SHAPE;   // which rows belong to an expert is known on the device only
