@@ -8,6 +8,7 @@ kernels; there is no CPU or library fallback, and a non-zero status raises
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import _abi
@@ -49,6 +50,15 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _outputs_on(stream, device):
+    """The context in which a call's outputs are allocated: on the stream that writes them,
+    so that the allocator gives no memory that another stream's queued work still uses."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 
 def _ptr(t):
@@ -160,13 +170,15 @@ def fp8_quantize_blocks(x, q=None, s=None, stream=None):
     """Block quantization of bf16 activations x [M, K] (CUDA tensor) into E4M3
     codes q [M, K] (uint8) and fp32 scales s [ceil(M/32), K/32]: the A and sA
     operands of fp8_gemm_blockscaled.  Returns (q, s); allocates them when not
-    given."""
-    import torch
+    given (on ``stream``)."""
     M, K = x.shape
-    if q is None:
-        q = torch.empty(M, K, dtype=torch.uint8, device=x.device)
-    if s is None:
-        s = torch.empty((M + 31) // 32, K // 32, dtype=torch.float32, device=x.device)
+    if q is None or s is None:
+        import torch
+        with _outputs_on(stream, x.device):
+            if q is None:
+                q = torch.empty(M, K, dtype=torch.uint8, device=x.device)
+            if s is None:
+                s = torch.empty((M + 31) // 32, K // 32, dtype=torch.float32, device=x.device)
     _check(library().fp8_quantize_blocks(_ptr(x), _ptr(q), _ptr(s), M, K, _stream(stream)),
            "fp8_quantize_blocks")
     return q, s
@@ -270,11 +282,11 @@ def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
     sA operands of fp8_gemm_block128 and fp8_gemm_experts.  rows: None (M = R)
     or an int32 CUDA tensor [M] of rows of x to take (outside of [0, R): a row of
     zeros).  pow2: scales rounded up to powers of two.  Returns (q, s);
-    allocates them when not given."""
+    allocates them when not given (on ``stream``)."""
     R, K = x.shape
     M = R if rows is None else rows.shape[0]
     if q is None or s is None:
-        q, s = _token_operands(M, K, q, s, x.device)
+        q, s = _token_operands(M, K, q, s, x.device, stream)
     if q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_quantize_tokens: q must be [M, K] and s [M, ceil(K/128)]")
     d = _Calls.loaded or _Calls()
@@ -300,7 +312,7 @@ def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
     M, K2 = x.shape
     K = K2 // 2
     if q is None or s is None:
-        q, s = _token_operands(M, K, q, s, x.device)
+        q, s = _token_operands(M, K, q, s, x.device, stream)
     if K2 % 2 or q.shape != (M, K) or s.shape != (M, (K + 127) // 128):
         raise ValueError("fp8_swiglu_quantize_tokens: x is [M, 2K], q [M, K] and s [M, ceil(K/128)]")
     d = _Calls.loaded or _Calls()
@@ -317,10 +329,11 @@ def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
     return q, s
 
 
-def _token_operands(M, K, q, s, device):
+def _token_operands(M, K, q, s, device, stream):
     import torch
-    q = torch.empty(M, K, dtype=torch.uint8, device=device) if q is None else q
-    s = torch.empty(M, (K + 127) // 128, dtype=torch.float32, device=device) if s is None else s
+    with _outputs_on(stream, device):
+        q = torch.empty(M, K, dtype=torch.uint8, device=device) if q is None else q
+        s = torch.empty(M, (K + 127) // 128, dtype=torch.float32, device=device) if s is None else s
     return q, s
 
 
