@@ -90,12 +90,14 @@ int check_operands(const void *A, const float *sA, const void *B, const float *s
     return FP8_OK;
 }
 
-template <int NT, int U, int WARPS, int CTAS>
+// ONE_WAVE: the caller knows that all CTAs fit on the GPU at once.
+template <int NT, int U, int WARPS, int CTAS, bool ONE_WAVE = false>
 int launch_rows(const RowsArgs &a, int64_t groups, DeviceState *d, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.N + ROWS_N - 1) / ROWS_N), static_cast<unsigned>(groups));
-    if (static_cast<int64_t>(grid.x) * groups <= static_cast<int64_t>(CTAS) * d->sm_count)
+    if (ONE_WAVE || static_cast<int64_t>(grid.x) * groups <= static_cast<int64_t>(CTAS) * d->sm_count)
         return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, true>, grid, WARPS * 32, 0, 1, a, stream);
-    return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, false>, grid, WARPS * 32, 0, 1, a, stream);
+    if constexpr (!ONE_WAVE)
+        return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, false>, grid, WARPS * 32, 0, 1, a, stream);
 }
 
 RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
@@ -184,11 +186,11 @@ int split_of(int64_t tiles, int KB, int sms) {
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 8)
-        return (a.N + ROWS_N - 1) / ROWS_N <= 2 * d->sm_count ? launch_rows<1, 4, 8, 2>(a, 1, d, stream)
+        return (a.N + ROWS_N - 1) / ROWS_N <= 2 * d->sm_count ? launch_rows<1, 4, 8, 2, true>(a, 1, d, stream)
                                                               : launch_rows<1, 4, 4, 4>(a, 1, d, stream);
     const int64_t groups = (a.M + 15) / 16;
     if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
-        return (a.N + ROWS_N - 1) / ROWS_N * groups <= 2 * d->sm_count ? launch_rows<2, 1, 8, 2>(a, groups, d, stream)
+        return (a.N + ROWS_N - 1) / ROWS_N * groups <= 2 * d->sm_count ? launch_rows<2, 1, 8, 2, true>(a, groups, d, stream)
                                                                        : launch_rows<2, 2, 4, 4>(a, groups, d, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);

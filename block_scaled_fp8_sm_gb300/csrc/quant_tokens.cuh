@@ -19,7 +19,7 @@
 #include <cstdint>
 
 #include "block128_rows.cuh"
-#include "quant_kernel.cuh"
+#include "quant_math.cuh"
 
 namespace bsfp8 {
 
