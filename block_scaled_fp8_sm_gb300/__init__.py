@@ -308,7 +308,10 @@ def fp8_quantize_tokens(x, q=None, s=None, rows=None, pow2=False, stream=None):
 
 def fp8_swiglu_quantize_tokens(x, q=None, s=None, pow2=False, stream=None):
     """fp8_quantize_tokens of silu(gate) * up, with gate = x[:, :K] and
-    up = x[:, K:] of bf16 x [M, 2K] (rows may be strided)."""
+    up = x[:, K:] of bf16 x [M, 2K] (rows may be strided).  128 values whose
+    largest magnitude is below 2^-100 count as zeros (codes 0, scale 1); where the
+    product passes the largest fp32 number, the scale is infinite and that value's
+    code NaN."""
     M, K2 = x.shape
     K = K2 // 2
     if q is None or s is None:

@@ -139,7 +139,7 @@ int tile_args(Tile128Args &a, const RowsArgs &r, int BN, DeviceState *d) {
     a.nt = (r.N + BN - 1) / BN;
     // tile order: B passes once for each group of m-tiles, whose A is read from L2 then;
     // 32 MB is half of what one of the two L2 halves holds (8192 x 28672 x 8192, promotion /
-    // native: 32 MB 1406 / 1229 us, 16 MB 1396 / 1257, 64 MB 1496 / 1381)
+    // native, runs of some ms: 32 MB 1406 / 1229 us, 16 MB 1396 / 1257, 64 MB 1496 / 1381)
     const int64_t fit = (int64_t(32) << 20) / (static_cast<int64_t>(T128_BM) * r.K);
     a.group = static_cast<int>(fit < 1 ? 1 : fit > a.mt ? a.mt : fit);
     return FP8_OK;
@@ -176,8 +176,8 @@ int split_of(int64_t tiles, int KB, int sms) {
 // The form of one product.
 //
 // Rows: up to 8 rows always (1 x 4096 x 7168 6.4 us against 9.2 by tiles, 1 x 28672 x 8192
-// 37 against 47).  Up to 64 rows where B is small: each group of 16 rows costs the rows form
-// about 2.3 us + 0.24 us per MB of B, a launch of tiles 5.6 us + 0.14 us per MB in all
+// 37 against 47).  Up to 64 rows where B is small: the rows form costs about 2.3 us, and
+// 0.24 us per MB of B for each group of 16 rows; tiles cost 5.6 us + 0.14 us per MB in all
 // (16 x 4096 x 7168 9.3 / 9.2 us; 32 x 2048 x 4096 6.6 / 7.7; 64 x 1024 x 2048 4.3 / 7.0; 64
 // x 8192 x 512 9.8 / 4.6).
 //
@@ -206,6 +206,12 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
 // over 16 experts of 4096 x 7168 70 / 73 us, 96 rows 80 / 73; 32 over 8 of 1024 x 2048 4.9 /
 // 7.5; 256 over 64 of 4096 x 2048 86 / 83, 384 97 / 84).  256-column tiles where they can
 // fill the SMs (16 experts, 532 rows of 4096 x 7168: 77 us, 87 with 128 columns).
+// Uneven routing costs the rows form more, as an expert's rows are taken eight at a time one
+// after the other: all of them with one expert, against even, 195 / 264 us (256 rows over 64
+// of 4096 x 7168), 164 / 93 (1024 over 256 of 1024 x 2048), 388 / 161 (4096 over 1024 of 512
+// x 1024).  CTAs of their own for each 32 rows of an expert bring these to 113, 57 and 185,
+// but cost even routing, whose grid then has rows for pieces that do not exist, up to 17 %
+// (264, 96, 188).
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 4 * static_cast<int64_t>(a.E))

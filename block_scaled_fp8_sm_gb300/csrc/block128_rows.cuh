@@ -3,9 +3,9 @@
 //   C[m,n] = bf16( sum_kb sA[m][kb] sB[n/128][kb] sum_{k in kb} A[m,k] B[n,k] )
 //
 // With few rows the call is bound by reading B once (N K bytes) and by latency,
-// not by the tensor cores, so there is no staging: a CTA of eight warps owns 16
-// rows of B and all of K, warp w taking the K blocks w, w + 8, ...; each lane
-// loads 16-byte pieces of B (and of the tokens) straight into registers, which
+// not by the tensor cores, so there is no staging: a CTA of WARPS (four or eight)
+// warps owns 16 rows of B and all of K, warp w taking the K blocks w, w + WARPS, ...
+// and loading U of them ahead; each lane loads 16-byte pieces of B (and of the tokens) straight into registers, which
 // are the operands of mma.m16n8k32 (B's 16 rows as its M side, 8 tokens as its
 // N side).  The products of a 128-K block are summed by four MMAs from zero in
 // fp32, then acc += (sA sB) * sum in fp32; the warps' sums are added in
@@ -18,8 +18,9 @@
 // TB/s; the former 28.5, U = 2 and eight warps 26.8).  Experts, where each CTA first finds
 // its expert: four warps, U = 2, six CTAs, whose loads cover one another's starts (24 rows
 // over 64 experts of 4096 x 7168: 85.7 us, 6.5 TB/s; U = 4 and four CTAs 90; eight CTAs of
-// 64 registers 89).  With two groups of tokens (NT = 2) likewise: 16 x 4096 x 7168, cold,
-// eight warps and two CTAs 10.3 us (three 14.6); 16 x 16384 x 1024 four warps 6.4 us (7.4).
+// 64 registers 89).  Two groups of tokens (NT = 2) take twice the registers for them: eight
+// warps, U = 1 and two CTAs on an SM (16 x 4096 x 7168, cold, 10.3 us; three CTAs 14.6), or
+// four warps, U = 2 and four CTAs (16 x 16384 x 1024 6.4 us; the former 7.4).
 //
 // Every launch may be set up while the previous kernel ends (programmatic dependent
 // launch); NEXT, a launch whose CTAs all fit on the GPU at once (one token: 256), also lets

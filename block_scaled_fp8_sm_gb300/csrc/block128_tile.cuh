@@ -18,9 +18,10 @@
 // What bounds it: a partial's round trip.  The four MMAs of a block keep the tensor pipe
 // busy ~505 cycles, the epilogue needs ~660 for its eight load-and-FMA pieces and the
 // hand-over, and with two 256-column partials the sum of both and of the two signals is
-// paid every second block: ~870 cycles a block, the tensor pipe 55-65 % busy (4096^3 61 us,
-// 2250 TFLOP/s; 8192 x 28672 x 8192 1406 us, 2740, where power holds the clock near 1.8
-// GHz).  Measured and slower: more, narrower partials (128 columns 72 us: an N = 128 MMA
+// paid every second block: ~870 cycles a block, the tensor pipe 55-66 % busy (4096^3 61 us
+// alone, 65 in a loop of seconds; 8192 x 28672 x 8192 1360-1410 us, 2730-2830 TFLOP/s, in
+// runs of some ms, 1530-1560, 2470-2520, in such a loop, where power holds the clock near
+// 1.8 GHz).  Measured alone, and slower: more, narrower partials (128 columns 72 us: an N = 128 MMA
 // costs as much as N = 256), 192 columns with twelve epilogue warps (71), sixteen warps
 // (78), packed FMAs (67: the loaded values have to be moved into pairs), two pieces in
 // flight (61-70), scales staged in shared memory by the idle warps (73).  The role threads

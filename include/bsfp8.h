@@ -318,7 +318,9 @@ int64_t fp8_grouped_workspace_bytes(int32_t G);
  *
  * N a multiple of 8, K a multiple of 16 (the last block of either may be
  * partial), M any; all below 2^30.  A, B and C 16-byte aligned, sA and sB
- * 4-byte aligned.  Execution, errors and status as described at the top.
+ * 4-byte aligned.  Every pointer is memory of the current device.  Execution,
+ * errors and status as described at the top; consecutive calls on a stream
+ * overlap at their ends, and each reads what the one before it wrote.
  *
  * Modes: FP8_PATH_AUTO and FP8_PATH_PROMOTE take any finite scales: the
  * products of a 128-K block are summed by the tensor cores in fp32, then
