@@ -12,7 +12,7 @@
 // by the reciprocal of the pieces per row.  Loads in flight come from resident warps (64
 // of them an SM, 48 where the arithmetic needs 40 registers), not from pieces loaded ahead:
 // 16384 x 7168 gathered from 4096 tokens 36.6 us alone, 39 in a loop over other inputs (180
-// MB at the copy bandwidth 27; L2 serves the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 60.6 us in such a loop (49: integer and
+// MB at the copy bandwidth 27; L2 serves the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 58.0 us in such a loop (49: integer and
 // conversion work); two pieces ahead with half the warps 41 / 57 / 65.
 #pragma once
 #include <cuda_bf16.h>
@@ -46,39 +46,68 @@ __device__ __forceinline__ uint64_t f32x2_of(float lo, float hi) {
     return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi));
 }
 
-// silu(g) u on two values.  n = exp(-|g| / 2) = 2^t, t = -|g| log2(e) / 2: the product's
-// rounding error comes from an fma (Dekker's error-free product) and enters as 2^t (1 +
-// t_lo ln 2).  With r = 1 / (1 + n^2) and m = n for negative g, else 1, the sigmoid is m^2 r,
-// and the result (g m) (u m r): neither half leaves fp32's normal range where the result is
-// in it (at least 2^-100), since |g| m < 1 for negative g and, with the half of the
-// exponential, u m r is no smaller than the result; exp(g) itself is subnormal from g = -87
-// on, and g, u or g u may be out of range where the result is not.
+// silu(g) u on two values.  exp(-|g|) = 2^t, t = -|g| log2(e): the product's rounding
+// error comes from an fma (Dekker's error-free product) and enters as 2^t (1 + t_lo ln 2);
+// the sigmoid is r = 1 / (1 + e), or e r for negative g, so no exponential overflows.
+// |g| counts as at most 256, whose exponential is zero, so that the product stays finite.
+// Gates of kDeep and below are silu_mul2_deep's.
 __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
-    constexpr float kL = 0x1.715476p-1f, kLlo = 0x1.4ae0cp-27f, kLn2 = 0x1.62e43p-1f;   // log2(e) / 2 = kL + kLlo
+    constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;   // log2(e) = kL + kLlo
     uint32_t g0, g1;
     f32x2_unpack(g, g0, g1);
-    // |g|, at most 256: exp(-128) is zero in fp32, and the product below stays finite
     const uint64_t a = f32x2_of(fminf(fabsf(__uint_as_float(g0)), 256.0f), fminf(fabsf(__uint_as_float(g1)), 256.0f));
     const uint64_t t = mul_f32x2_rn(a, f32x2_of(-kL, -kL));
-    uint64_t lo = fma_f32x2_rn(a, f32x2_of(kL, kL), t);   // |g| log2(e) / 2 + t = -t_lo
+    uint64_t lo = fma_f32x2_rn(a, f32x2_of(kL, kL), t);   // |g| log2(e) + t = -t_lo
     lo = fma_f32x2_rn(a, f32x2_of(kLlo, kLlo), lo);
     uint32_t t0, t1;
     f32x2_unpack(t, t0, t1);
-    float n0, n1;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(n0) : "f"(__uint_as_float(t0)));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(n1) : "f"(__uint_as_float(t1)));
-    uint64_t n = f32x2_of(n0, n1);
-    n = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(-kLn2, -kLn2)), n, n);
-    uint32_t e0, e1, m0, m1;
-    f32x2_unpack(mul_f32x2_rn(n, n), e0, e1);
+    float e0, e1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(__uint_as_float(t0)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(__uint_as_float(t1)));
+    uint64_t e = f32x2_of(e0, e1);
+    e = fma_f32x2_rn(mul_f32x2_rn(lo, f32x2_of(-kLn2, -kLn2)), e, e);
+    uint32_t b0, b1;
+    f32x2_unpack(e, b0, b1);
     float r0, r1;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(1.0f + __uint_as_float(e0)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(1.0f + __uint_as_float(e1)));
-    f32x2_unpack(n, m0, m1);
-    m0 = static_cast<int32_t>(g0) < 0 ? m0 : 0x3F800000u;
-    m1 = static_cast<int32_t>(g1) < 0 ? m1 : 0x3F800000u;
-    const uint64_t m = f32x2_pack(m0, m1);
-    return mul_f32x2_rn(mul_f32x2_rn(g, m), mul_f32x2_rn(u, mul_f32x2_rn(m, f32x2_of(r0, r1))));
+    const float d0 = 1.0f + __uint_as_float(b0), d1 = 1.0f + __uint_as_float(b1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+    uint64_t r = f32x2_of(r0, r1);
+    const uint32_t n0 = static_cast<int32_t>(g0) < 0 ? b0 : 0x3F800000u;   // e for negative g, else 1
+    const uint32_t n1 = static_cast<int32_t>(g1) < 0 ? b1 : 0x3F800000u;
+    const uint64_t sig = mul_f32x2_rn(f32x2_pack(n0, n1), r);
+    return mul_f32x2_rn(mul_f32x2_rn(g, sig), u);
+}
+
+constexpr float kDeep = -64.0f;
+
+// The same for g <= kDeep: y of the values above it stays.  exp(g) gets subnormal from -87
+// on, and u may bring the result back into range, so each factor takes one half of the
+// exponent: with n = 2^(t / 2), y = (g n) (u n) (the sigmoid is n^2: 1 + n^2 rounds to 1).
+// |g n| < 1, so u n is larger than the result and has its bits as long as that is normal.
+__device__ __forceinline__ uint64_t silu_mul2_deep(uint64_t y, uint64_t g, uint64_t u) {
+    constexpr float kH = 0x1.715476p-1f, kHlo = 0x1.4ae0cp-27f, kLn2 = 0x1.62e43p-1f;   // log2(e) / 2 = kH + kHlo
+    uint32_t gw[2], uw[2], yw[2];
+    f32x2_unpack(g, gw[0], gw[1]);
+    f32x2_unpack(u, uw[0], uw[1]);
+    f32x2_unpack(y, yw[0], yw[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float gk = __uint_as_float(gw[k]), a = fminf(fabsf(gk), 256.0f);
+        const float t = a * -kH, lo = fmaf(a, kHlo, fmaf(a, kH, t));
+        float n;
+        asm("ex2.approx.f32 %0, %1;" : "=f"(n) : "f"(t));
+        n = fmaf(lo * -kLn2, n, n);
+        if (gk <= kDeep) yw[k] = __float_as_uint((gk * n) * (__uint_as_float(uw[k]) * n));
+    }
+    return f32x2_pack(yw[0], yw[1]);
+}
+
+// The lesser value of each half.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // The E4M3 codes of eight values, in order.
@@ -158,12 +187,22 @@ __global__ void __launch_bounds__(QTOK_THREADS, GATED || !POW2 ? 6 : 8) bsfp8_qu
         }
         if constexpr (GATED) {
             amax = 0.0f;
+            // the warp's least gate decides whether deep values are looked for (a value's bits do
+            // not depend on it; doing without a branch, both factors with half of the exponent
+            // everywhere, took 60.6 us and doubled the exponential's error)
+            uint32_t least = min_bf16x2(w[0][0], w[1][0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) least = min_bf16x2(least, min_bf16x2(w[0][i], w[1][i]));
+            const float lowest = fminf(__uint_as_float(least << 16), __uint_as_float(least & 0xFFFF0000u));
+            const bool deep = __any_sync(0xFFFFFFFFu, lowest <= kDeep);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t h[4] = {up[j].x, up[j].y, up[j].z, up[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    y[j][i] = silu_mul2(y[j][i], f32x2_pack(h[i] << 16, h[i] & 0xFFFF0000u));
+                    const uint64_t g = y[j][i], u = f32x2_pack(h[i] << 16, h[i] & 0xFFFF0000u);
+                    y[j][i] = silu_mul2(g, u);
+                    if (deep) y[j][i] = silu_mul2_deep(y[j][i], g, u);
                     uint32_t lo, hi;
                     f32x2_unpack(y[j][i], lo, hi);
                     amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(lo)), fabsf(__uint_as_float(hi))));

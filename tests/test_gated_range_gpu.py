@@ -1,9 +1,10 @@
 """The gated quantizer over the whole range of bf16 gates and ups, against silu(gate) up in
 64 bits.
 
-Error of the kernel's y: the sigmoid's exponential is the square of one taken at half the
-argument (2 ulp of 2^-23, twice: 2^-21; its correction and the square, three roundings of
-2^-24), 1 + e and the reciprocal (2^-24 and 2^-23), the products (four of 2^-24): together
+Error of the kernel's y, at most: the sigmoid's exponential, which for gates of -64 and
+below is the square of one taken at half the argument (2 ulp of 2^-23, twice: 2^-21; its
+correction and the square, three roundings of 2^-24), 1 + e and the reciprocal (2^-24 and
+2^-23), the products (four of 2^-24): together
 2^-21 + 2^-23 + 8 * 2^-24 = 1.125 * 2^-20.  The quotient by the scale adds an ulp, 2^-23:
 1.25 * 2^-20.  A code may be half a step and that much of the value off; a scale that much of
 itself, or, rounded up to a power of two, one power where the unrounded one is that near."""
@@ -122,3 +123,28 @@ def test_products_past_the_largest_number(bs, pow2):
         keep = ~np.isinf(got_s[:, b])
         cols = slice(b * 128, min(400, b * 128 + 128))
         _check(q[keep][:, cols], s[keep][:, b:b + 1], y[keep, cols], pow2, f"beside infinite values, piece {b}")
+
+
+@pytest.mark.parametrize("low,high", [(-60, -1), (-8, 8), (0, 20)])
+def test_ordinary_gates_are_as_exact_as_plain_arithmetic(bs, low, high):
+    """One value to a piece, read off its scale: the rms error against 64 bits, next to that
+    of the formula in plain fp32 operations.  Those round four times beside their exponential
+    (sum, quotient, product, scale); the kernel eight times at most (the exponential's
+    correction, the sum, a reciprocal of one ulp for two, three products, the scale): at most
+    sqrt(8 / 4) times the error, 1.42; 1.5 is accepted."""
+    g = torch.Generator().manual_seed(5)
+    P = 1 << 17
+    gate = (torch.rand(P, generator=g) * (high - low) + low).to(torch.bfloat16)
+    up = torch.randn(P, generator=g).to(torch.bfloat16)
+    x = torch.zeros(P // 16, 2, 16, 128, dtype=torch.bfloat16)
+    x[:, 0, :, 5], x[:, 1, :, 5] = gate.view(-1, 16), up.view(-1, 16)
+    _, s = bs.fp8_swiglu_quantize_tokens(x.view(P // 16, -1).to(DEV))
+    y = np.abs(_silu_mul(gate, up)) / 448.0
+    gate, up = gate.to(DEV).float(), up.to(DEV).float()
+    plain = (gate / (1 + torch.exp(-gate)) * up).abs()
+    plain = (plain / torch.full_like(plain, 448.0)).cpu().numpy().astype(np.float64)
+    keep = y > 2.0 ** -90
+    assert keep.mean() > 0.9
+    own, plain = (float(np.sqrt(np.mean(((v - y) / np.where(keep, y, 1.0))[keep] ** 2)))
+                  for v in (s.cpu().numpy().astype(np.float64).ravel(), plain))
+    assert own <= 1.5 * plain, (own, plain)
