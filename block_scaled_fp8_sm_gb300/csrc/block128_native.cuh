@@ -17,7 +17,7 @@
 //
 // 8192 x 28672 x 8192: 1125-1220 us (3150-3420 TFLOP/s, 82-89 % of twice the measured bf16
 // rate) in runs of some ms, against 1360-1410 by promotion, and 1280-1320 in a loop of
-// seconds, where power sets the clock, against 1530-1560.  Experts, runs of some ms: 16384
+// seconds, where power sets the clock, against 1530-1580.  Experts, runs of some ms: 16384
 // rows over 16 of 4096 x 7168 338 us (promotion 374), 4001 skewed rows over 32 of 4104 x
 // 2064 73 us (75).
 #pragma once

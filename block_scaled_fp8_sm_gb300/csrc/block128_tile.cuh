@@ -20,7 +20,7 @@
 // hand-over, and with two 256-column partials the sum of both and of the two signals is
 // paid every second block: ~870 cycles a block, the tensor pipe 55-66 % busy (4096^3 61 us
 // alone, 65 in a loop of seconds; 8192 x 28672 x 8192 1360-1410 us, 2730-2830 TFLOP/s, in
-// runs of some ms, 1530-1560, 2470-2520, in such a loop, where power holds the clock near
+// runs of some ms, 1530-1580, 2440-2520, in such a loop, where power holds the clock near
 // 1.8 GHz).  Measured alone, and slower: more, narrower partials (128 columns 72 us: an N = 128 MMA
 // costs as much as N = 256), 192 columns with twelve epilogue warps (71), sixteen warps
 // (78), packed FMAs (67: the loaded values have to be moved into pairs), two pieces in

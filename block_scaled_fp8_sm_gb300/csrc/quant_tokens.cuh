@@ -12,8 +12,9 @@
 // by the reciprocal of the pieces per row.  Loads in flight come from resident warps (64
 // of them an SM, 48 where the arithmetic needs 40 registers), not from pieces loaded ahead:
 // 16384 x 7168 gathered from 4096 tokens 36.6 us alone, 39 in a loop over other inputs (180
-// MB at the copy bandwidth 27; L2 serves the repeated tokens), all distinct 52 us (53), gated 16001 x 4096 58.0 us in such a loop (49: integer and
-// conversion work); two pieces ahead with half the warps 41 / 57 / 65.
+// MB at the copy bandwidth 27; L2 serves the repeated tokens), all distinct 52 us (53),
+// gated 16001 x 4096 58.0 us in such a loop (49: integer and conversion work); two pieces
+// ahead with half the warps 41 / 57 / 65.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
