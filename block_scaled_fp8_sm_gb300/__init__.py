@@ -14,12 +14,14 @@ import ctypes
 from . import _abi
 from ._abi import (FP8_PATH_AUTO, FP8_PATH_NATIVE, FP8_PATH_PROMOTE,  # noqa: F401
                    FP8_DEBUG_WAIT_LIMIT_CYCLES, FP8_DEBUG_WITHHOLD_STAGE, FP8_DEBUG_TRACE_BUFFER,
-                   FP8_MAX_GROUPS_PER_LAUNCH, FP8_MAX_EXPERTS, FP8_QUANT_POW2, fp8_group_desc)
+                   FP8_MAX_GROUPS_PER_LAUNCH, FP8_MAX_EXPERTS, FP8_QUANT_POW2, FP8_ACT_NONE,
+                   FP8_ACT_RELU, FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_SILU, FP8_TYPE_F32, FP8_TYPE_BF16,
+                   fp8_group_desc)
 
 __all__ = ["fp8_gemm_blockscaled", "fp8_gemm_blockscaled_noalloc", "fp8_gemm_grouped", "group_descs",
            "fp8_gemm_grouped_device", "fp8_grouped_workspace_bytes", "group_table", "fp8_gemm_pertoken",
            "fp8_quantize_blocks", "fp8_gemm_rowcol", "fp8_gemm_blockscaled_residual",
-           "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0", "fp8_gemm_block128", "fp8_gemm_experts",
+           "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0", "fp8_gemm_block128", "fp8_gemm_block128_fused", "fp8_gemm_experts",
            "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens", "fp8_status_query", "fp8_strerror", "fp8_version", "fp8_debug_set", "fp8_lib_shutdown",
            "Fp8Error", "library"]
 
@@ -196,9 +198,11 @@ class _Calls:
         import torch
         self.codes = frozenset((torch.uint8, torch.float8_e4m3fn))
         self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
+        self.floats = frozenset((torch.float32, torch.bfloat16))
         # the current device, and the current stream of a device
         self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         lib = library()
+        self.fused = lib.fp8_gemm_block128_fused
         self.block128, self.experts = lib.fp8_gemm_block128_ex, lib.fp8_gemm_experts_ex
         self.quantize, self.swiglu = lib.fp8_quantize_tokens, lib.fp8_swiglu_quantize_tokens
         _Calls.loaded = self
@@ -244,6 +248,42 @@ def fp8_gemm_block128(A, sA, B, sB, C, stream=None, mode=None):
                     d.stream(dev) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_gemm_block128")
+    return C
+
+
+def fp8_gemm_block128_fused(A, sA, B, sB, C, bias=None, act=FP8_ACT_NONE, residual=None, stream=None, mode=None):
+    """C = bf16(act(product + bias) + residual): fp8_gemm_block128 with the epilogue
+    done in fp32 before the one rounding.  bias: None or [N], float32 or bfloat16;
+    act: FP8_ACT_NONE, _RELU, _GELU (by the error function), _GELU_TANH or _SILU;
+    residual: None or bfloat16 [M,N], which may be C itself.  Other arguments as
+    fp8_gemm_block128."""
+    M, K = A.shape
+    N, kb = B.shape[0], (K + 127) // 128
+    if (B.shape != (N, K) or C.shape != (M, N) or sA.shape != (M, kb) or sB.shape != ((N + 127) // 128, kb)
+            or (bias is not None and bias.shape != (N,)) or (residual is not None and residual.shape != (M, N))):
+        raise ValueError("fp8_gemm_block128_fused: shapes of A, sA, B, sB, C, bias, residual do not match")
+    d = _Calls.loaded or _Calls()
+    dev = A.get_device()
+    if not (A.dtype in d.codes and B.dtype in d.codes and sA.dtype is d.f32 and sB.dtype is d.f32
+            and C.dtype is d.bf16 and A.is_contiguous() and sA.is_contiguous() and B.is_contiguous()
+            and sB.is_contiguous() and C.is_contiguous()
+            and dev >= 0 and sA.get_device() == dev and B.get_device() == dev and sB.get_device() == dev
+            and C.get_device() == dev and d.device() == dev
+            and (bias is None or (bias.dtype in d.floats and bias.is_contiguous() and bias.get_device() == dev))
+            and (residual is None or (residual.dtype is d.bf16 and residual.is_contiguous()
+                                      and residual.get_device() == dev))):
+        raise _refused("fp8_gemm_block128_fused", ("A", A, d.codes), ("sA", sA, d.f32), ("B", B, d.codes),
+                       ("sB", sB, d.f32), ("C", C, d.bf16),
+                       *([] if bias is None else [("bias", bias, d.floats)]),
+                       *([] if residual is None else [("residual", residual, d.bf16)]))
+    rc = d.fused(A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
+                 None if bias is None else bias.data_ptr(),
+                 FP8_TYPE_BF16 if bias is not None and bias.dtype is d.bf16 else FP8_TYPE_F32, act,
+                 None if residual is None else residual.data_ptr(), C.data_ptr(), M, N, K,
+                 FP8_PATH_AUTO if mode is None else mode,
+                 d.stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_gemm_block128_fused")
     return C
 
 

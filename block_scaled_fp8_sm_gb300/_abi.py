@@ -34,6 +34,15 @@ FP8_MAX_GROUPS_PER_LAUNCH = 64
 FP8_MAX_EXPERTS = 1024
 FP8_QUANT_POW2 = 1
 
+FP8_TYPE_F32 = 0
+FP8_TYPE_BF16 = 1
+
+FP8_ACT_NONE = 0
+FP8_ACT_RELU = 1
+FP8_ACT_GELU = 2
+FP8_ACT_GELU_TANH = 3
+FP8_ACT_SILU = 4
+
 # every symbol include/bsfp8.h declares
 EXPORTS = (
     "fp8_gemm_blockscaled", "fp8_gemm_blockscaled_ex", "fp8_gemm_grouped",
@@ -43,7 +52,7 @@ EXPORTS = (
     "fp8_gemm_grouped_device", "fp8_grouped_workspace_bytes", "fp8_gemm_pertoken", "fp8_gemm_pertoken_ex",
     "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0",
     "fp8_gemm_block128", "fp8_gemm_block128_ex", "fp8_gemm_experts", "fp8_gemm_experts_ex",
-    "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens",
+    "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens", "fp8_gemm_block128_fused",
 )
 
 
@@ -98,6 +107,8 @@ def load(path: str = None) -> ctypes.CDLL:
     lib.fp8_gemm_block128.restype = ci
     lib.fp8_gemm_block128_ex.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
     lib.fp8_gemm_block128_ex.restype = ci
+    lib.fp8_gemm_block128_fused.argtypes = [vp, vp, vp, vp, vp, ci, ci, vp, vp, i64, i64, i64, ci, vp]
+    lib.fp8_gemm_block128_fused.restype = ci
     lib.fp8_gemm_experts.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
     lib.fp8_gemm_experts.restype = ci
     lib.fp8_gemm_experts_ex.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, ci, vp]

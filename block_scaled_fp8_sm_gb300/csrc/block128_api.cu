@@ -16,10 +16,21 @@ namespace bsfp8 {
 
 namespace {
 
-template <int BN, bool SPLIT>
+template <int BN, bool SPLIT, bool FUSED>
 int set_tile_attrs() {
-    return cudaFuncSetAttribute(bsfp8_block128_tile<BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem128<BN>()) == cudaSuccess
+    return cudaFuncSetAttribute(bsfp8_block128_tile<BN, SPLIT, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem128<BN, FUSED>()) == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_CUDA;
+}
+
+template <bool FUSED>
+int set_attrs() {
+    if (set_tile_attrs<256, false, FUSED>() != FP8_OK || set_tile_attrs<128, false, FUSED>() != FP8_OK ||
+        set_tile_attrs<128, true, FUSED>() != FP8_OK)
+        return FP8_ERR_CUDA;
+    return cudaFuncSetAttribute(bsfp8_block128_native<FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem_n128<FUSED>()) == cudaSuccess
                ? FP8_OK
                : FP8_ERR_CUDA;
 }
@@ -27,13 +38,8 @@ int set_tile_attrs() {
 }  // namespace
 
 int block128_setup() {
-    if (set_tile_attrs<256, false>() != FP8_OK || set_tile_attrs<128, false>() != FP8_OK ||
-        set_tile_attrs<128, true>() != FP8_OK)
-        return FP8_ERR_CUDA;
-    return cudaFuncSetAttribute(bsfp8_block128_native, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_n128()) ==
-                   cudaSuccess
-               ? FP8_OK
-               : FP8_ERR_CUDA;
+    const int rc = set_attrs<false>();
+    return rc != FP8_OK ? rc : set_attrs<true>();
 }
 
 namespace {
@@ -91,13 +97,13 @@ int check_operands(const void *A, const float *sA, const void *B, const float *s
 }
 
 // ONE_WAVE: the caller knows that all CTAs fit on the GPU at once.
-template <int NT, int U, int WARPS, int CTAS, bool ONE_WAVE = false>
+template <int NT, int U, int WARPS, int CTAS, bool ONE_WAVE, bool FUSED>
 int launch_rows(const RowsArgs &a, int64_t groups, DeviceState *d, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.N + ROWS_N - 1) / ROWS_N), static_cast<unsigned>(groups));
     if (ONE_WAVE || static_cast<int64_t>(grid.x) * groups <= static_cast<int64_t>(CTAS) * d->sm_count)
-        return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, true>, grid, WARPS * 32, 0, 1, a, stream);
+        return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, true, FUSED>, grid, WARPS * 32, 0, 1, a, stream);
     if constexpr (!ONE_WAVE)
-        return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, false>, grid, WARPS * 32, 0, 1, a, stream);
+        return launch(bsfp8_block128_rows<NT, U, WARPS, CTAS, false, FUSED>, grid, WARPS * 32, 0, 1, a, stream);
 }
 
 RowsArgs rows_args(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
@@ -130,6 +136,7 @@ int tile_args(Tile128Args &a, const RowsArgs &r, int BN, DeviceState *d) {
     a.status = d->status;
     a.wait_limit = wait_limit();
     a.withhold = withheld_stage();
+    a.ep = r.ep;
     a.M = r.M;
     a.N = r.N;
     a.KB = r.KB;
@@ -146,23 +153,24 @@ int tile_args(Tile128Args &a, const RowsArgs &r, int BN, DeviceState *d) {
 }
 
 // `tiles`: how many there are, or, for experts, can be.
-template <int BN, bool SPLIT>
+template <int BN, bool SPLIT, bool FUSED>
 int launch_tile(const RowsArgs &r, int64_t tiles, int split, DeviceState *d, cudaStream_t stream) {
     Tile128Args a{};
     const int rc = tile_args(a, r, BN, d);
     if (rc != FP8_OK) return rc;
     // split: one tile per cluster; else persistent CTAs
     const int64_t ctas = SPLIT ? tiles * split : tiles < d->sm_count ? tiles : d->sm_count;
-    return launch(bsfp8_block128_tile<BN, SPLIT>, dim3(static_cast<unsigned>(ctas)), T128_THREADS, smem128<BN>(),
-                  split, a, stream);
+    return launch(bsfp8_block128_tile<BN, SPLIT, FUSED>, dim3(static_cast<unsigned>(ctas)), T128_THREADS,
+                  smem128<BN, FUSED>(), split, a, stream);
 }
 
+template <bool FUSED>
 int launch_native(const RowsArgs &r, int64_t tiles, DeviceState *d, cudaStream_t stream) {
     Tile128Args a{};
     const int rc = tile_args(a, r, N128_BN, d);
     if (rc != FP8_OK) return rc;
     const unsigned grid = static_cast<unsigned>(tiles < d->sm_count ? tiles : d->sm_count);
-    return launch(bsfp8_block128_native, dim3(grid), T128_THREADS, smem_n128(), 1, a, stream);
+    return launch(bsfp8_block128_native<FUSED>, dim3(grid), T128_THREADS, smem_n128<FUSED>(), 1, a, stream);
 }
 
 // CTAs that share a tile's K: as many as the GPU still has room for, four K blocks
@@ -183,22 +191,23 @@ int split_of(int64_t tiles, int KB, int sms) {
 //
 // Tiles of 128 x 256 once they fill the SMs (4096^3 61 us; 72 with 128 columns), else of
 // 128 x 128 with K split over clusters (37 x 4104 x 7184 10 us; 19 unsplit).
+template <bool FUSED>
 int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 8)
-        return (a.N + ROWS_N - 1) / ROWS_N <= 2 * d->sm_count ? launch_rows<1, 4, 8, 2, true>(a, 1, d, stream)
-                                                              : launch_rows<1, 4, 4, 4>(a, 1, d, stream);
+        return (a.N + ROWS_N - 1) / ROWS_N <= 2 * d->sm_count ? launch_rows<1, 4, 8, 2, true, FUSED>(a, 1, d, stream)
+                                                              : launch_rows<1, 4, 4, 4, false, FUSED>(a, 1, d, stream);
     const int64_t groups = (a.M + 15) / 16;
     if (!pinned && groups <= 4 && static_cast<int64_t>(a.N) * a.K * (24 * groups - 14) <= 330000000ll)
-        return (a.N + ROWS_N - 1) / ROWS_N * groups <= 2 * d->sm_count ? launch_rows<2, 1, 8, 2, true>(a, groups, d, stream)
-                                                                       : launch_rows<2, 2, 4, 4>(a, groups, d, stream);
+        return (a.N + ROWS_N - 1) / ROWS_N * groups <= 2 * d->sm_count ? launch_rows<2, 1, 8, 2, true, FUSED>(a, groups, d, stream)
+                                                                       : launch_rows<2, 2, 4, 4, false, FUSED>(a, groups, d, stream);
     const int64_t mt = (a.M + T128_BM - 1) / T128_BM;
     const int64_t wide = mt * ((a.N + 255) / 256), narrow = mt * ((a.N + 127) / 128);
-    if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
-    if (wide >= d->sm_count) return launch_tile<256, false>(a, wide, 1, d, stream);
+    if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native<FUSED>(a, wide, d, stream);
+    if (wide >= d->sm_count) return launch_tile<256, false, FUSED>(a, wide, 1, d, stream);
     const int split = pinned ? 1 : split_of(narrow, a.KB, d->sm_count);
-    if (split > 1) return launch_tile<128, true>(a, narrow, split, d, stream);
-    return launch_tile<128, false>(a, narrow, 1, d, stream);
+    if (split > 1) return launch_tile<128, true, FUSED>(a, narrow, split, d, stream);
+    return launch_tile<128, false, FUSED>(a, narrow, 1, d, stream);
 }
 
 // Experts: the row counts are on the device, so the rule goes by what is possible: at
@@ -215,14 +224,14 @@ int launch_product(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t str
 int launch_experts(const RowsArgs &a, int mode, DeviceState *d, cudaStream_t stream) {
     const bool pinned = mode == FP8_PATH_PROMOTE;
     if (!pinned && a.M <= 4 * static_cast<int64_t>(a.E))
-        return launch_rows<1, 2, 4, 6>(a, a.M < a.E ? a.M : a.E, d, stream);
+        return launch_rows<1, 2, 4, 6, false, false>(a, a.M < a.E ? a.M : a.E, d, stream);
     const int64_t most = (a.M < a.E ? a.M : a.E) + a.M / T128_BM;
     const int64_t wide = most * ((a.N + 255) / 256), narrow = most * ((a.N + 127) / 128);
-    if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native(a, wide, d, stream);
-    if (wide >= d->sm_count) return launch_tile<256, false>(a, wide, 1, d, stream);
+    if (wide >= d->sm_count && mode == FP8_PATH_NATIVE) return launch_native<false>(a, wide, d, stream);
+    if (wide >= d->sm_count) return launch_tile<256, false, false>(a, wide, 1, d, stream);
     const int split = pinned ? 1 : split_of(narrow, a.KB, d->sm_count);
-    if (split > 1) return launch_tile<128, true>(a, narrow, split, d, stream);
-    return launch_tile<128, false>(a, narrow, 1, d, stream);
+    if (split > 1) return launch_tile<128, true, false>(a, narrow, split, d, stream);
+    return launch_tile<128, false, false>(a, narrow, 1, d, stream);
 }
 
 template <bool GATED>
@@ -296,12 +305,40 @@ int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const fl
     if (K == 0) return zero_fill(C, M * N, stream);
     RowsArgs a = rows_args(A, sA, B, sB, C, M, N, K);
     a.status = d->status;
-    return guarded([&] { return launch_product(a, mode, d, stream); });
+    return guarded([&] { return launch_product<false>(a, mode, d, stream); });
 }
 
 int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float *sB, void *C, int64_t M, int64_t N,
                       int64_t K, cudaStream_t stream) {
     return fp8_gemm_block128_ex(A, sA, B, sB, C, M, N, K, FP8_PATH_AUTO, stream);
+}
+
+int fp8_gemm_block128_fused(const void *A, const float *sA, const void *B, const float *sB, const void *bias,
+                            int bias_type, int act, const void *R, void *C, int64_t M, int64_t N, int64_t K, int mode,
+                            cudaStream_t stream) {
+    int rc = check_sizes(M, N, K, mode);
+    if (rc != FP8_OK) return rc;
+    if ((bias_type != FP8_TYPE_F32 && bias_type != FP8_TYPE_BF16) || act < FP8_ACT_NONE || act > FP8_ACT_SILU)
+        return FP8_ERR_MODE;
+    if (M == 0 || N == 0) return FP8_OK;
+    rc = check_operands(A, sA, B, sB, C, K);
+    if (rc != FP8_OK) return rc;
+    if (!aligned(bias, 16) || !aligned(R, 16)) return FP8_ERR_ALIGN;
+    DeviceState *d = nullptr;
+    rc = device_setup(&d);
+    if (rc != FP8_OK) return rc;
+    RowsArgs a = rows_args(A, sA, B, sB, C, M, N, K);
+    a.status = d->status;
+    a.ep = Epilogue{bias, static_cast<const __nv_bfloat16 *>(R), bias_type == FP8_TYPE_BF16, act};
+    if (K > 0) return guarded([&] { return launch_product<true>(a, mode, d, stream); });
+    // no K: act(bias) + R by the rows form, whose loops over K are then empty; up to 65535 groups a launch
+    for (int64_t m = 0; m < M && rc == FP8_OK; m += 8 * 65535) {
+        a.M = static_cast<int>(M - m < 8 * 65535 ? M - m : 8 * 65535);
+        rc = launch_rows<1, 4, 4, 4, false, true>(a, (a.M + 7) / 8, d, stream);
+        a.C += static_cast<int64_t>(a.M) * N;
+        if (R) a.ep.R += static_cast<int64_t>(a.M) * N;
+    }
+    return rc;
 }
 
 int fp8_gemm_experts_ex(const void *A, const float *sA, const void *B, const float *sB, void *C,

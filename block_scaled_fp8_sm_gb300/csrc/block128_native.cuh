@@ -31,14 +31,16 @@ constexpr int N128_SF_A = 512, N128_SF_B = 128;                // bytes of lines
 constexpr int N128_SF_ENTRY = N128_SF_A + 2 * N128_SF_B;
 constexpr int N128_SF_COL0 = 256, N128_SF_COLS = 12;            // tensor memory: A 4 columns, B 4 per block
 
-struct CtrlN128 : Ctrl128<N128_BN> {
+template <bool FUSED>
+struct CtrlN128 : Control128<N128_BN, FUSED> {
     uint64_t sfull[N128_SF_RING], sempty[N128_SF_RING];
 };
 
+template <bool FUSED>
 constexpr int smem_n128() {
     using C = Cfg128<N128_BN>;
     return 1024 + C::STAGES * (C::A_BYTES + C::B_BYTES) + C::STG + N128_SF_RING * N128_SF_ENTRY +
-           static_cast<int>(sizeof(CtrlN128));
+           static_cast<int>(sizeof(CtrlN128<FUSED>));
 }
 
 __device__ __forceinline__ bool is_pow2(float v) {
@@ -46,6 +48,7 @@ __device__ __forceinline__ bool is_pow2(float v) {
     return (b & 0x007FFFFFu) == 0u && e != 0u && e < 255u;
 }
 
+template <bool FUSED>
 __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const __grid_constant__ Tile128Args a) {
     using C = Cfg128<N128_BN>;
     extern __shared__ uint8_t smem_raw[];
@@ -53,7 +56,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
     uint8_t *sm_a = smem, *sm_b = smem + C::STAGES * C::A_BYTES;
     uint8_t *stg = sm_b + C::STAGES * C::B_BYTES;
     uint8_t *sf = stg + C::STG;
-    CtrlN128 *ctl = reinterpret_cast<CtrlN128 *>(sf + N128_SF_RING * N128_SF_ENTRY);
+    using Ctl = CtrlN128<FUSED>;
+    Ctl *ctl = reinterpret_cast<Ctl *>(sf + N128_SF_RING * N128_SF_ENTRY);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -87,141 +91,146 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
     const uint32_t tmem = ctl->tmem;
     const int tiles = ctl->tiles, unit = static_cast<int>(blockIdx.x), units = static_cast<int>(gridDim.x);
 
-    if (warp == 0) {
-        if (elect_one()) {
-            int it = 0, s = 0, withheld = -1;
-            uint32_t ph = 1;
-            bool ok = true;
-            for (int t = unit; t < tiles && ok; t += units) {
-                const Tile128 tt = tile128<N128_BN>(a, ctl, t);
-                for (int kb = 0; kb < a.KB; ++kb) {
-                    ok = wait128(&ctl->empty[s], ph, ctl, a);
-                    if (!ok) break;
-                    if (it == a.withhold && blockIdx.x == 0) withheld = s;
-                    else load_stage<N128_BN>(a, &ctl->full[s], sm_a + s * C::A_BYTES, sm_b + s * C::B_BYTES, tt, kb);
-                    ++it;
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
-            }
-            // no load is in flight when the CTA leaves
-            for (int d = max(0, it - C::STAGES); d < it; ++d) {
-                if (d % C::STAGES == withheld) continue;
-                const long long t0 = clock64();
-                while (!mbar_try_wait(&ctl->full[d % C::STAGES], static_cast<uint32_t>(d / C::STAGES) & 1u))
-                    if (clock64() - t0 > a.wait_limit) break;
-            }
-        }
-    } else if (warp == 1) {
-        if (elect_one()) {
-            constexpr uint32_t idesc = idesc_mxf8f6f4(T128_BM, N128_BN, 0, 0);
-            int s = 0, f = 0;
-            uint32_t ph = 0, fph = 0, tph = 1;
-            bool ok = true, ready = false;
-            for (int t = unit; t < tiles && ok; t += units) {
-                ok = wait128(&ctl->tempty[0], tph, ctl, a);
-                if (!ok) break;
-                tph ^= 1u;
-                uint32_t sfa = 0;
-                for (int kb = 0; kb < a.KB; ++kb) {
-                    const uint32_t j = static_cast<uint32_t>(kb) & 3u;
-                    if (j == 0) {
-                        ok = wait128(&ctl->sfull[f], fph, ctl, a);
+    // FUSED: the epilogue warps hold a tile's 128 sums a thread (the split of block128_tile.cuh)
+    if (warp < 4) {
+        if constexpr (FUSED) setmaxnreg_dec<T128_ROLE_REGS>();
+        if (warp == 0) {
+            if (elect_one()) {
+                int it = 0, s = 0, withheld = -1;
+                uint32_t ph = 1;
+                bool ok = true;
+                for (int t = unit; t < tiles && ok; t += units) {
+                    const Tile128 tt = tile128<N128_BN>(a, ctl, t);
+                    for (int kb = 0; kb < a.KB; ++kb) {
+                        ok = wait128(&ctl->empty[s], ph, ctl, a);
                         if (!ok) break;
-                        tc_fence_after();
-                        // the slot's last readers, the MMAs of four entries ago, are done:
-                        // the stages loaded since then waited for them
-                        sfa = tmem + N128_SF_COL0 + f * N128_SF_COLS;
-                        const uint32_t lines = smem_u32(sf + f * N128_SF_ENTRY);
-                        tmem_cp_32x128b_warpx4(sfa, sdesc_sf_lines32(lines));
-                        tmem_cp_32x128b_warpx4(sfa + 4, sdesc_sf_lines(lines + N128_SF_A));
-                        tmem_cp_32x128b_warpx4(sfa + 8, sdesc_sf_lines(lines + N128_SF_A + N128_SF_B));
-                        mma_commit(&ctl->sempty[f]);
-                        if (++f == N128_SF_RING) {
-                            f = 0;
-                            fph ^= 1u;
+                        if (it == a.withhold && blockIdx.x == 0) withheld = s;
+                        else load_stage<N128_BN>(a, &ctl->full[s], sm_a + s * C::A_BYTES, sm_b + s * C::B_BYTES, tt, kb);
+                        ++it;
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
                         }
                     }
-                    if (!ready) ok = wait128(&ctl->full[s], ph, ctl, a);
+                }
+                // no load is in flight when the CTA leaves
+                for (int d = max(0, it - C::STAGES); d < it; ++d) {
+                    if (d % C::STAGES == withheld) continue;
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(&ctl->full[d % C::STAGES], static_cast<uint32_t>(d / C::STAGES) & 1u))
+                        if (clock64() - t0 > a.wait_limit) break;
+                }
+            }
+        } else if (warp == 1) {
+            if (elect_one()) {
+                constexpr uint32_t idesc = idesc_mxf8f6f4(T128_BM, N128_BN, 0, 0);
+                int s = 0, f = 0;
+                uint32_t ph = 0, fph = 0, tph = 1;
+                bool ok = true, ready = false;
+                for (int t = unit; t < tiles && ok; t += units) {
+                    ok = wait128(&ctl->tempty[0], tph, ctl, a);
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t ad = sdesc_k_sw128(smem_u32(sm_a + s * C::A_BYTES));
-                    const uint64_t bd = sdesc_k_sw128(smem_u32(sm_b + s * C::B_BYTES));
-                    const uint32_t id = idesc | (j << 4) | (j << 29);
-                    uint64_t *empty = &ctl->empty[s];
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    tph ^= 1u;
+                    uint32_t sfa = 0;
+                    for (int kb = 0; kb < a.KB; ++kb) {
+                        const uint32_t j = static_cast<uint32_t>(kb) & 3u;
+                        if (j == 0) {
+                            ok = wait128(&ctl->sfull[f], fph, ctl, a);
+                            if (!ok) break;
+                            tc_fence_after();
+                            // the slot's last readers, the MMAs of four entries ago, are done:
+                            // the stages loaded since then waited for them
+                            sfa = tmem + N128_SF_COL0 + f * N128_SF_COLS;
+                            const uint32_t lines = smem_u32(sf + f * N128_SF_ENTRY);
+                            tmem_cp_32x128b_warpx4(sfa, sdesc_sf_lines32(lines));
+                            tmem_cp_32x128b_warpx4(sfa + 4, sdesc_sf_lines(lines + N128_SF_A));
+                            tmem_cp_32x128b_warpx4(sfa + 8, sdesc_sf_lines(lines + N128_SF_A + N128_SF_B));
+                            mma_commit(&ctl->sempty[f]);
+                            if (++f == N128_SF_RING) {
+                                f = 0;
+                                fph ^= 1u;
+                            }
+                        }
+                        if (!ready) ok = wait128(&ctl->full[s], ph, ctl, a);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t ad = sdesc_k_sw128(smem_u32(sm_a + s * C::A_BYTES));
+                        const uint64_t bd = sdesc_k_sw128(smem_u32(sm_b + s * C::B_BYTES));
+                        const uint32_t id = idesc | (j << 4) | (j << 29);
+                        uint64_t *empty = &ctl->empty[s];
+                        if (++s == C::STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // the next stage is looked for while the pipe is busy
-                        if (i == 3) ready = mbar_test_wait(&ctl->full[s], ph);
-                        mma_mxf8(tmem, ad + 2 * i, bd + 2 * i, id, sfa, sfa + 4, (kb | i) != 0);
+                        for (int i = 0; i < 4; ++i) {
+                            // the next stage is looked for while the pipe is busy
+                            if (i == 3) ready = mbar_test_wait(&ctl->full[s], ph);
+                            mma_mxf8(tmem, ad + 2 * i, bd + 2 * i, id, sfa, sfa + 4, (kb | i) != 0);
+                        }
+                        mma_commit(empty);
                     }
-                    mma_commit(empty);
+                    if (!ok) break;
+                    mma_commit(&ctl->tfull[0]);
                 }
-                if (!ok) break;
-                mma_commit(&ctl->tfull[0]);
+                // all MMAs have completed before tensor memory is freed
+                mma_commit(&ctl->drain);
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&ctl->drain, 0))
+                    if (clock64() - t0 > a.wait_limit) break;
             }
-            // all MMAs have completed before tensor memory is freed
-            mma_commit(&ctl->drain);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&ctl->drain, 0))
-                if (clock64() - t0 > a.wait_limit) break;
-        }
-    } else if (warp < 4) {
-        // thread i writes the words of rows i and i + 64 (word w of line l: row 32 w + l)
-        // and one word of B's lines
-        const int i = (warp - 2) * 32 + lane;
-        const bool vec = (a.KB & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15) == 0;
-        int f = 0;
-        uint32_t fph = 1;
-        bool ok = true, bad = false;
-        for (int t = unit; t < tiles && ok; t += units) {
-            const Tile128 tt = tile128<N128_BN>(a, ctl, t);
-            const float *row[3];
-            row[0] = a.sA + static_cast<int64_t>(min(tt.m0 + i, tt.hi - 1)) * a.KB;
-            row[1] = a.sA + static_cast<int64_t>(min(tt.m0 + i + 64, tt.hi - 1)) * a.KB;
-            row[2] = a.sB + (static_cast<int64_t>(tt.e) * a.NB + min(tt.n0 / 128 + (warp - 2), a.NB - 1)) * a.KB;
-            for (int kb = 0; kb < a.KB; kb += 4) {
-                uint32_t word[3];
+        } else {
+            // thread i writes the words of rows i and i + 64 (word w of line l: row 32 w + l)
+            // and one word of B's lines
+            const int i = (warp - 2) * 32 + lane;
+            const bool vec = (a.KB & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.sA) | reinterpret_cast<uintptr_t>(a.sB)) & 15) == 0;
+            int f = 0;
+            uint32_t fph = 1;
+            bool ok = true, bad = false;
+            for (int t = unit; t < tiles && ok; t += units) {
+                const Tile128 tt = tile128<N128_BN>(a, ctl, t);
+                const float *row[3];
+                row[0] = a.sA + static_cast<int64_t>(min(tt.m0 + i, tt.hi - 1)) * a.KB;
+                row[1] = a.sA + static_cast<int64_t>(min(tt.m0 + i + 64, tt.hi - 1)) * a.KB;
+                row[2] = a.sB + (static_cast<int64_t>(tt.e) * a.NB + min(tt.n0 / 128 + (warp - 2), a.NB - 1)) * a.KB;
+                for (int kb = 0; kb < a.KB; kb += 4) {
+                    uint32_t word[3];
 #pragma unroll
-                for (int r = 0; r < 3; ++r) {
-                    float v[4];
-                    if (vec) {
-                        const float4 x = *reinterpret_cast<const float4 *>(row[r] + kb);
-                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                    } else {
+                    for (int r = 0; r < 3; ++r) {
+                        float v[4];
+                        if (vec) {
+                            const float4 x = *reinterpret_cast<const float4 *>(row[r] + kb);
+                            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = row[r][min(kb + j, a.KB - 1)];
+                            for (int j = 0; j < 4; ++j) v[j] = row[r][min(kb + j, a.KB - 1)];
+                        }
+                        word[r] = 0u;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            bad |= !is_pow2(v[j]);
+                            word[r] |= (__float_as_uint(v[j]) >> 23 & 0xFFu) << (8 * j);
+                        }
                     }
-                    word[r] = 0u;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        bad |= !is_pow2(v[j]);
-                        word[r] |= (__float_as_uint(v[j]) >> 23 & 0xFFu) << (8 * j);
+                    ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->sempty[f], fph, ctl, a));
+                    if (!ok) break;
+                    uint32_t *lines = reinterpret_cast<uint32_t *>(sf + f * N128_SF_ENTRY);
+                    lines[lane * 4 + (warp - 2)] = word[0];
+                    lines[lane * 4 + (warp - 2) + 2] = word[1];
+                    lines[(N128_SF_A + (warp - 2) * N128_SF_B) / 4 + lane] = word[2];
+                    fence_proxy_async_smem();   // the lines become visible to tcgen05.cp
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->sfull[f]);
+                    if (++f == N128_SF_RING) {
+                        f = 0;
+                        fph ^= 1u;
                     }
-                }
-                ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->sempty[f], fph, ctl, a));
-                if (!ok) break;
-                uint32_t *lines = reinterpret_cast<uint32_t *>(sf + f * N128_SF_ENTRY);
-                lines[lane * 4 + (warp - 2)] = word[0];
-                lines[lane * 4 + (warp - 2) + 2] = word[1];
-                lines[(N128_SF_A + (warp - 2) * N128_SF_B) / 4 + lane] = word[2];
-                fence_proxy_async_smem();   // the lines become visible to tcgen05.cp
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->sfull[f]);
-                if (++f == N128_SF_RING) {
-                    f = 0;
-                    fph ^= 1u;
                 }
             }
+            if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, STATUS_SCALE);
         }
-        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, STATUS_SCALE);
     } else {
+        if constexpr (FUSED) setmaxnreg_inc<T128_EPI_REGS>();
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::COLS;
         uint8_t *mine = stg + (warp - 4) * (32 * 64);
@@ -231,23 +240,41 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
             if (!__all_sync(0xFFFFFFFFu, wait128(&ctl->tfull[0], tph, ctl, a))) break;
             tph ^= 1u;
             tc_fence_after();
-            uint32_t w[C::COLS / 32][16];
+            if constexpr (FUSED) {   // the sums in registers: the accumulator is free before the epilogue's arithmetic
+                uint32_t p[C::COLS / 16][16];
 #pragma unroll
-            for (int x = 0; x < C::COLS / 32; ++x) {
-                uint32_t p[2][16];
-                tmem_ld_x16(taddr + 32 * x, p[0]);
-                tmem_ld_x16(taddr + 32 * x + 16, p[1]);
-                tmem_ld_wait_for(p[0]);
-                tmem_ld_wait_for(p[1]);
+                for (int x = 0; x < C::COLS / 16; ++x) tmem_ld_x16(taddr + 16 * x, p[x]);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    w[x][j] = bf16_pair(__uint_as_float(p[j >> 3][2 * (j & 7)]), __uint_as_float(p[j >> 3][2 * (j & 7) + 1]));
+                for (int x = 0; x < C::COLS / 16; ++x) tmem_ld_wait_for(p[x]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->tempty[0]);
+#pragma unroll
+                for (int x = 0; x < C::COLS / 16; ++x) {
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(p[x][j]);
+                    store_fused<16>(mine, a, tt, q, tt.n0 + h * C::COLS + 16 * x, v);
+                }
+            } else {
+                uint32_t w[C::COLS / 32][16];
+#pragma unroll
+                for (int x = 0; x < C::COLS / 32; ++x) {
+                    uint32_t p[2][16];
+                    tmem_ld_x16(taddr + 32 * x, p[0]);
+                    tmem_ld_x16(taddr + 32 * x + 16, p[1]);
+                    tmem_ld_wait_for(p[0]);
+                    tmem_ld_wait_for(p[1]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        w[x][j] = bf16_pair(__uint_as_float(p[j >> 3][2 * (j & 7)]), __uint_as_float(p[j >> 3][2 * (j & 7) + 1]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->tempty[0]);
+#pragma unroll
+                for (int x = 0; x < C::COLS / 32; ++x) store_rows32(mine, a, tt, q, tt.n0 + h * C::COLS + 32 * x, w[x]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->tempty[0]);
-#pragma unroll
-            for (int x = 0; x < C::COLS / 32; ++x) store_rows32(mine, a, tt, q, tt.n0 + h * C::COLS + 32 * x, w[x]);
         }
     }
 

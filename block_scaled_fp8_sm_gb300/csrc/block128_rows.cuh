@@ -2,6 +2,8 @@
 //
 //   C[m,n] = bf16( sum_kb sA[m][kb] sB[n/128][kb] sum_{k in kb} A[m,k] B[n,k] )
 //
+// (FUSED: bias, activation and residual before the rounding, epilogue.cuh.)
+//
 // With few rows the call is bound by reading B once (N K bytes) and by latency,
 // not by the tensor cores, so there is no staging: a CTA of WARPS (four or eight)
 // warps owns 16 rows of B and all of K, warp w taking the K blocks w, w + WARPS, ...
@@ -35,6 +37,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "status.h"
 
@@ -49,6 +52,7 @@ struct RowsArgs {
     const int32_t *offsets;   // [E + 1] on the device, or null: one product over all rows
     uint32_t *status;
     int M, N, K, KB, E;
+    Epilogue ep;              // FUSED kernels
 };
 
 constexpr int ROWS_N = 16;   // rows of B per CTA
@@ -113,7 +117,7 @@ __device__ __forceinline__ int busy_expert(const int32_t *offsets, int E, int T,
     return *found;
 }
 
-template <int NT, int U, int WARPS, int CTAS, bool NEXT>
+template <int NT, int U, int WARPS, int CTAS, bool NEXT, bool FUSED>
 __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const RowsArgs a) {
     __shared__ float red[WARPS][NT][4][32];
     __shared__ int counts[WARPS];
@@ -202,8 +206,11 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) bsfp8_block128_rows(const Ro
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) v += red[w][n][c][l];
-            if (m0 + j < hi && n0 + r < a.N)
-                a.C[static_cast<int64_t>(m0 + j) * a.N + n0 + r] = __float2bfloat16_rn(v);
+            if (m0 + j < hi && n0 + r < a.N) {
+                const int64_t at = static_cast<int64_t>(m0 + j) * a.N + n0 + r;
+                if constexpr (FUSED) v = finish(a.ep, v, n0 + r, at);
+                a.C[at] = __float2bfloat16_rn(v);
+            }
         }
         __syncthreads();
     }

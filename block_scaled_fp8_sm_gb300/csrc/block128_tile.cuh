@@ -68,6 +68,7 @@ struct Tile128Args {
     int M, N, KB, NB, E, mt, nt;
     int group;                // m-tiles whose A stays in L2 while B passes once
     int withhold;             // test hook: CTA 0 never loads this stage (-1: off)
+    Epilogue ep;              // FUSED kernels
 };
 
 template <int BN>
@@ -80,20 +81,25 @@ struct Cfg128 {
     static constexpr int STG = T128_EPI_WARPS * 32 * 64;   // 32 rows x 32 bf16 columns per epilogue warp
 };
 
-template <int BN>
+// EXPERTS: how many the launch can have (0: one product).
+template <int BN, int EXPERTS = T128_MAX_EXPERTS>
 struct Ctrl128 {
     uint64_t full[Cfg128<BN>::STAGES], empty[Cfg128<BN>::STAGES];
     uint64_t tfull[Cfg128<BN>::BUFS], tempty[Cfg128<BN>::BUFS], drain;
     uint32_t tmem;
     int abort, tiles;
-    int start[T128_MAX_EXPERTS + 1];   // experts: first tile of each,
-    int2 rows[T128_MAX_EXPERTS];       // and its rows
+    int start[EXPERTS + 1];   // experts: first tile of each,
+    int2 rows[EXPERTS + 1];   // and its rows
 };
 
-template <int BN>
+// FUSED kernels are for one product: no expert table, and twice the staging (fp32).
+template <int BN, bool FUSED>
+using Control128 = Ctrl128<BN, FUSED ? 0 : T128_MAX_EXPERTS>;
+
+template <int BN, bool FUSED>
 constexpr int smem128() {
-    return 1024 + Cfg128<BN>::STAGES * (Cfg128<BN>::A_BYTES + Cfg128<BN>::B_BYTES) + Cfg128<BN>::STG +
-           static_cast<int>(sizeof(Ctrl128<BN>));
+    return 1024 + Cfg128<BN>::STAGES * (Cfg128<BN>::A_BYTES + Cfg128<BN>::B_BYTES) +
+           Cfg128<BN>::STG * (FUSED ? 2 : 1) + static_cast<int>(sizeof(Control128<BN, FUSED>));
 }
 
 // Bounded wait: polls, and looks at the clock and the abort flag every 16 polls.
@@ -246,6 +252,48 @@ __device__ __forceinline__ void store_rows32(uint8_t *mine, const Tile128Args &a
     __syncwarp();
 }
 
+// P columns (32 or 16) of fp32 sums of each lane's row to C through P * 128 bytes of
+// staging, with bias, activation and residual: there a lane holds eight consecutive columns
+// of a row, so that the residual comes and C goes in whole sectors, and the activation's
+// code is there once for a piece and not once for each of a lane's 128 sums.
+template <int P>
+__device__ __forceinline__ void store_fused(uint8_t *mine, const Tile128Args &a, const Tile128 &tt, int q, int col,
+                                            const float *v) {
+    constexpr int CH = P / 4;            // 16-byte pieces of a staged row
+    constexpr int LR = P / 8;            // lanes of a row
+    constexpr int SH = P == 32 ? 0 : 1;  // rows in 128 bytes: 1 or 2
+    const int lane = threadIdx.x & 31;
+    const int c8 = lane & (LR - 1), n = col + 8 * c8;
+    uint4 r[LR];
+    int64_t at[LR];
+#pragma unroll
+    for (int i = 0; i < LR; ++i) {
+        const int m = tt.m0 + q * 32 + i * (32 / LR) + lane / LR;
+        at[i] = m < tt.hi && n < a.N ? static_cast<int64_t>(m) * a.N + n : -1;
+        r[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.ep.R && at[i] >= 0) r[i] = *reinterpret_cast<const uint4 *>(a.ep.R + at[i]);
+    }
+    float4 *row = reinterpret_cast<float4 *>(mine + lane * (P * 4));
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+        row[c ^ ((lane >> SH) & (CH - 1))] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < LR; ++i) {
+        const int rr = i * (32 / LR) + lane / LR, x = (rr >> SH) & (CH - 1);
+        const float4 *src = reinterpret_cast<const float4 *>(mine + rr * (P * 4));
+        const float4 lo = src[(2 * c8) ^ x], hi = src[(2 * c8 + 1) ^ x];
+        if (at[i] >= 0) {
+            float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+            finish<8>(a.ep, f, n, w);
+            *reinterpret_cast<uint4 *>(a.C + at[i]) =
+                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+        }
+    }
+    __syncwarp();
+}
+
 // First tile of each expert (a running sum over one warp), or the tile count of one
 // product.  Reports an offset table that decreases or leaves [0, M].
 template <typename Ctl>
@@ -303,14 +351,15 @@ __device__ __forceinline__ void load_stage(const Tile128Args &a, uint64_t *full,
     tma_load_2d(&a.tmB, full, db, kb * 128, tt.e * a.N + tt.n0);
 }
 
-template <int BN, bool SPLIT>
+template <int BN, bool SPLIT, bool FUSED>
 __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __grid_constant__ Tile128Args a) {
     using C = Cfg128<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sm_a = smem, *sm_b = smem + C::STAGES * C::A_BYTES;
     uint8_t *stg = sm_b + C::STAGES * C::B_BYTES;
-    Ctrl128<BN> *ctl = reinterpret_cast<Ctrl128<BN> *>(stg + C::STG);
+    using Ctl = Control128<BN, FUSED>;
+    Ctl *ctl = reinterpret_cast<Ctl *>(stg + C::STG * (FUSED ? 2 : 1));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank = 0, ranks = 1;
     if constexpr (SPLIT) {
@@ -424,7 +473,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int r = q * 32 + lane;   // row of the tile
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::COLS;
-        uint8_t *mine = stg + (warp - 4) * (32 * 64);
+        uint8_t *mine = stg + (warp - 4) * (32 * 64) * (FUSED ? 2 : 1);
         int b = 0;
         uint32_t bph = 0;
         bool ok = true;
@@ -487,6 +536,10 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 for (int j = 0; j < C::COLS / 4; ++j)
                     red[r * (BN / 4) + ((h * (C::COLS / 4) + j) ^ (r & 7))] =
                         make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+            } else if constexpr (FUSED) {
+#pragma unroll
+                for (int x = 0; x < C::COLS / 32; ++x)
+                    store_fused<32>(mine, a, cur, q, cur.n0 + h * C::COLS + 32 * x, acc + 32 * x);
             } else {
 #pragma unroll
                 for (int x = 0; x < C::COLS / 32; ++x) {
@@ -525,9 +578,22 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                     v[0].z += v[k].z;
                     v[0].w += v[k].w;
                 }
+                const int n = tt.n0 + 4 * c;
+                if constexpr (FUSED) {
+                    if (n < a.N) {
+                        uint32_t w[2] = {0u, 0u};
+                        if (a.ep.R) {
+                            const uint2 u = *reinterpret_cast<const uint2 *>(a.ep.R + static_cast<int64_t>(tt.m0 + r) * a.N + n);
+                            w[0] = u.x, w[1] = u.y;
+                        }
+                        float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                        finish<4>(a.ep, f, n, w);
+                        v[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    }
+                }
                 const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0].x, v[0].y), hi = __floats2bfloat162_rn(v[0].z, v[0].w);
-                if (tt.n0 + 4 * c < a.N)
-                    *reinterpret_cast<uint2 *>(a.C + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0 + 4 * c) =
+                if (n < a.N)
+                    *reinterpret_cast<uint2 *>(a.C + static_cast<int64_t>(tt.m0 + r) * a.N + n) =
                         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             }
         }

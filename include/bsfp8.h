@@ -344,6 +344,27 @@ int fp8_gemm_block128(const void *A, const float *sA, const void *B, const float
 int fp8_gemm_block128_ex(const void *A, const float *sA, const void *B, const float *sB, void *C,
                          int64_t M, int64_t N, int64_t K, int mode, cudaStream_t stream);
 
+/* The same product with bias, activation and residual in its epilogue, all in
+ * fp32 on the product's fp32 sums, rounded to bf16 once:
+ *
+ *   C[m,n] = bf16( act( sum + bias[n] ) + R[m,n] )
+ *
+ *   bias: [N] of bias_type (FP8_TYPE_F32 or FP8_TYPE_BF16), or NULL;
+ *   R:    bf16 [M, N], or NULL; may be C itself (an update in place), but must
+ *         not overlap C otherwise.
+ * act: FP8_ACT_RELU max(y, 0); FP8_ACT_GELU y Phi(y), Phi the normal
+ * distribution's integral; FP8_ACT_GELU_TANH 0.5 y (1 + tanh(sqrt(2/pi) (y +
+ * 0.044715 y^3))); FP8_ACT_SILU y / (1 + exp(-y)).
+ * A, B, C, bias and R 16-byte aligned.  Sizes, modes, order of the sums and
+ * errors as fp8_gemm_block128_ex (FP8_ERR_MODE for an unknown bias_type or
+ * act, too); without bias, activation and residual the results are its, bit
+ * for bit.  K == 0: the sum is 0, and act(bias) + R is written. */
+enum { FP8_TYPE_F32 = 0, FP8_TYPE_BF16 = 1 };
+enum { FP8_ACT_NONE = 0, FP8_ACT_RELU = 1, FP8_ACT_GELU = 2, FP8_ACT_GELU_TANH = 3, FP8_ACT_SILU = 4 };
+int fp8_gemm_block128_fused(const void *A, const float *sA, const void *B, const float *sB, const void *bias,
+                            int bias_type, int act, const void *R, void *C, int64_t M, int64_t N, int64_t K,
+                            int mode, cudaStream_t stream);
+
 /* The same product grouped by expert: the T rows of A are sorted by expert,
  * rows offsets[e] .. offsets[e+1]-1 are multiplied by B[e].
  *   A [T, K], sA [T, KB], C [T, N] as above; B [E, N, K], sB [E, NB, KB];
