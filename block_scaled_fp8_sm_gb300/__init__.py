@@ -16,13 +16,15 @@ from ._abi import (FP8_PATH_AUTO, FP8_PATH_NATIVE, FP8_PATH_PROMOTE,  # noqa: F4
                    FP8_DEBUG_WAIT_LIMIT_CYCLES, FP8_DEBUG_WITHHOLD_STAGE, FP8_DEBUG_TRACE_BUFFER,
                    FP8_MAX_GROUPS_PER_LAUNCH, FP8_MAX_EXPERTS, FP8_QUANT_POW2, FP8_ACT_NONE,
                    FP8_ACT_RELU, FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_SILU, FP8_TYPE_F32, FP8_TYPE_BF16,
+                   FP8_ROUTE_SIGMOID, FP8_ROUTE_ALL, FP8_MAX_TOP, FP8_MOE_MAX_TOKENS,
                    fp8_group_desc)
 
 __all__ = ["fp8_gemm_blockscaled", "fp8_gemm_blockscaled_noalloc", "fp8_gemm_grouped", "group_descs",
            "fp8_gemm_grouped_device", "fp8_grouped_workspace_bytes", "group_table", "fp8_gemm_pertoken",
            "fp8_quantize_blocks", "fp8_gemm_rowcol", "fp8_gemm_blockscaled_residual",
            "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0", "fp8_gemm_block128", "fp8_gemm_block128_fused", "fp8_gemm_experts",
-           "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens", "fp8_status_query", "fp8_strerror", "fp8_version", "fp8_debug_set", "fp8_lib_shutdown",
+           "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens", "fp8_moe_route", "fp8_moe_route_workspace_bytes",
+           "fp8_moe_layer", "fp8_moe_layer_workspace_bytes", "fp8_status_query", "fp8_strerror", "fp8_version", "fp8_debug_set", "fp8_lib_shutdown",
            "Fp8Error", "library"]
 
 
@@ -204,6 +206,7 @@ class _Calls:
         lib = library()
         self.fused = lib.fp8_gemm_block128_fused
         self.block128, self.experts = lib.fp8_gemm_block128_ex, lib.fp8_gemm_experts_ex
+        self.route, self.layer = lib.fp8_moe_route, lib.fp8_moe_layer
         self.quantize, self.swiglu = lib.fp8_quantize_tokens, lib.fp8_swiglu_quantize_tokens
         _Calls.loaded = self
 
@@ -378,6 +381,131 @@ def _token_operands(M, K, q, s, device, stream):
         q = torch.empty(M, K, dtype=torch.uint8, device=device) if q is None else q
         s = torch.empty(M, (K + 127) // 128, dtype=torch.float32, device=device) if s is None else s
     return q, s
+
+
+def fp8_moe_route_workspace_bytes(T: int, E: int, top: int) -> int:
+    return library().fp8_moe_route_workspace_bytes(int(T), int(E), int(top))
+
+
+def fp8_moe_route(logits, top, sigmoid=False, renormalize=True, scale=1.0, order=True, out=None, workspace=None,
+                  stream=None):
+    """The router of a mixture-of-experts layer: the ``top`` experts of each token by
+    its logits [T, E] (float32 or bfloat16, rows may be strided).  Returns (weights,
+    ids, offsets, rows, places), or (weights, ids) with order=False:
+
+    weights float32 [T, top]: softmax of the logits (sigmoid: their sigmoids) over the
+    chosen experts (renormalize=False: over all of them, the sigmoids as they are),
+    times scale; ids int32 [T, top]: the experts by descending logit, the lower expert
+    first of equal ones.  Logits of -inf or NaN are never chosen: where fewer than top
+    are left, ids are -1 and weights 0.  offsets int32 [E + 1], rows int32 [T * top],
+    places int32 [T, top]: the pairs (token, expert) in expert order, for
+    fp8_quantize_tokens(rows=rows) and fp8_gemm_experts(offsets); places[t, j] is where
+    pair (t, j) stands (-1: nowhere), and rows are -1 from offsets[E] on.
+
+    out: the tuple of an earlier call, to be written again; workspace: a uint8 CUDA
+    tensor of fp8_moe_route_workspace_bytes(T, E, top) bytes, one for each of the calls
+    that may overlap.  Both are allocated when not given (on ``stream``)."""
+    T, E = logits.shape
+    if out is None or (order and workspace is None):
+        out, workspace = _route_outputs(T, E, top, order, out, workspace, logits.device, stream)
+    weights, ids = out[:2]
+    if (weights.shape != (T, top) or ids.shape != (T, top) or len(out) != (5 if order else 2)
+            or (order and (out[2].shape != (E + 1,) or out[3].shape != (T * top,) or out[4].shape != (T, top)))):
+        raise ValueError("fp8_moe_route: out must be weights and ids [T, top], and with an order offsets [E + 1], "
+                         "rows [T * top] and places [T, top]")
+    d = _Calls.loaded or _Calls()
+    dev = logits.get_device()
+    if not (logits.dtype in d.floats and (logits.stride(1) == 1 or E <= 1) and weights.dtype is d.f32
+            and weights.is_contiguous() and dev >= 0 and weights.get_device() == dev and d.device() == dev
+            and all(t.dtype is d.i32 and t.is_contiguous() and t.get_device() == dev for t in out[1:])
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+        raise _refused("fp8_moe_route", ("logits", logits, d.floats), ("weights", weights, d.f32),
+                       *[("out", t, d.i32) for t in out[1:]],
+                       *([] if workspace is None else [("workspace", workspace, workspace.dtype)]))
+    offsets, rows, places = (t.data_ptr() for t in out[2:]) if order else (None, None, None)
+    rc = d.route(logits.data_ptr(), logits.stride(0) if T > 1 else E,
+                 FP8_TYPE_BF16 if logits.dtype is d.bf16 else FP8_TYPE_F32, T, E, top,
+                 (FP8_ROUTE_SIGMOID if sigmoid else 0) | (0 if renormalize else FP8_ROUTE_ALL), scale,
+                 weights.data_ptr(), ids.data_ptr(), offsets, rows, places,
+                 None if workspace is None else workspace.data_ptr(),
+                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                 d.stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_moe_route")
+    return out
+
+
+def _route_outputs(T, E, top, order, out, workspace, device, stream):
+    import torch
+    i32 = lambda *n: torch.empty(*n, dtype=torch.int32, device=device)   # noqa: E731
+    with _outputs_on(stream, device):
+        if out is None:
+            out = (torch.empty(T, top, dtype=torch.float32, device=device), i32(T, top))
+            if order:
+                out += (i32(E + 1), i32(T * top), i32(T, top))
+        if order and workspace is None:
+            workspace = torch.empty(fp8_moe_route_workspace_bytes(T, E, top), dtype=torch.uint8, device=device)
+    return out, workspace
+
+
+def fp8_moe_layer_workspace_bytes(T: int, top: int, I: int) -> int:   # noqa: E741
+    return library().fp8_moe_layer_workspace_bytes(int(T), int(top), int(I))
+
+
+def fp8_moe_layer(x, weights, ids, gate_up, s_gate_up, down, s_down, out=None, workspace=None, stream=None):
+    """A whole mixture-of-experts layer for up to FP8_MOE_MAX_TOKENS tokens:
+    out[t] = sum_j weights[t, j] down_e(silu(gate_e x_t) * up_e x_t), e = ids[t, j], as
+    bfloat16 [T, H], on unquantized activations x (bfloat16 [T, H]).
+
+    weights float32 and ids int32 [T, top] as fp8_moe_route makes them (an id outside
+    [0, E) takes no part); gate_up codes [E, 2I, H] (the gate's rows first) with scales
+    s_gate_up [E, ceil(2I/128), ceil(H/128)], down codes [E, H, I] with s_down
+    [E, ceil(H/128), ceil(I/128)]; H and I multiples of 16.  workspace: a uint8 CUDA
+    tensor of fp8_moe_layer_workspace_bytes(T, top, I) bytes, one for each of the calls
+    that may overlap.  out and workspace are allocated when not given (on ``stream``)."""
+    T, H = x.shape
+    E, I2 = gate_up.shape[:2]
+    top, I = weights.shape[-1], I2 // 2   # noqa: E741
+    hb = (H + 127) // 128
+    if T > FP8_MOE_MAX_TOKENS:
+        raise ValueError(f"fp8_moe_layer: {T} tokens; it takes up to {FP8_MOE_MAX_TOKENS} (more: fp8_quantize_tokens, "
+                         "fp8_gemm_experts and fp8_swiglu_quantize_tokens)")
+    if out is None or workspace is None:
+        out, workspace = _layer_outputs(T, top, H, I, out, workspace, x.device, stream)
+    if (weights.shape != (T, top) or ids.shape != (T, top) or I2 % 2 or gate_up.shape != (E, I2, H)
+            or down.shape != (E, H, I) or s_gate_up.shape != (E, (I2 + 127) // 128, hb)
+            or s_down.shape != (E, hb, (I + 127) // 128) or out.shape != (T, H)):
+        raise ValueError("fp8_moe_layer: shapes of x, weights, ids, gate_up, s_gate_up, down, s_down, out do not match")
+    d = _Calls.loaded or _Calls()
+    dev = x.get_device()
+    if not (x.dtype is d.bf16 and weights.dtype is d.f32 and ids.dtype is d.i32 and gate_up.dtype in d.codes
+            and s_gate_up.dtype is d.f32 and down.dtype in d.codes and s_down.dtype is d.f32 and out.dtype is d.bf16
+            and x.is_contiguous() and weights.is_contiguous() and ids.is_contiguous() and gate_up.is_contiguous()
+            and s_gate_up.is_contiguous() and down.is_contiguous() and s_down.is_contiguous() and out.is_contiguous()
+            and workspace.is_contiguous()
+            and dev >= 0 and weights.get_device() == dev and ids.get_device() == dev and gate_up.get_device() == dev
+            and s_gate_up.get_device() == dev and down.get_device() == dev and s_down.get_device() == dev
+            and out.get_device() == dev and workspace.get_device() == dev and d.device() == dev):
+        raise _refused("fp8_moe_layer", ("x", x, d.bf16), ("weights", weights, d.f32), ("ids", ids, d.i32),
+                       ("gate_up", gate_up, d.codes), ("s_gate_up", s_gate_up, d.f32), ("down", down, d.codes),
+                       ("s_down", s_down, d.f32), ("out", out, d.bf16), ("workspace", workspace, workspace.dtype))
+    rc = d.layer(x.data_ptr(), weights.data_ptr(), ids.data_ptr(), gate_up.data_ptr(), s_gate_up.data_ptr(),
+                 down.data_ptr(), s_down.data_ptr(), out.data_ptr(), T, top, E, H, I, workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(),
+                 d.stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error(rc, "fp8_moe_layer")
+    return out
+
+
+def _layer_outputs(T, top, H, I, out, workspace, device, stream):   # noqa: E741
+    import torch
+    with _outputs_on(stream, device):
+        if out is None:
+            out = torch.empty(T, H, dtype=torch.bfloat16, device=device)
+        if workspace is None:
+            workspace = torch.empty(fp8_moe_layer_workspace_bytes(T, top, I), dtype=torch.uint8, device=device)
+    return out, workspace
 
 
 class GroupDescs:

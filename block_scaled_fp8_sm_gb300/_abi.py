@@ -43,6 +43,11 @@ FP8_ACT_GELU = 2
 FP8_ACT_GELU_TANH = 3
 FP8_ACT_SILU = 4
 
+FP8_MAX_TOP = 32
+FP8_ROUTE_SIGMOID = 1
+FP8_ROUTE_ALL = 2
+FP8_MOE_MAX_TOKENS = 64
+
 # every symbol include/bsfp8.h declares
 EXPORTS = (
     "fp8_gemm_blockscaled", "fp8_gemm_blockscaled_ex", "fp8_gemm_grouped",
@@ -53,6 +58,7 @@ EXPORTS = (
     "fp8_gemm_blockscaled_quant", "fp8_gemm_pertoken_e8m0",
     "fp8_gemm_block128", "fp8_gemm_block128_ex", "fp8_gemm_experts", "fp8_gemm_experts_ex",
     "fp8_quantize_tokens", "fp8_swiglu_quantize_tokens", "fp8_gemm_block128_fused",
+    "fp8_moe_route", "fp8_moe_route_workspace_bytes", "fp8_moe_layer", "fp8_moe_layer_workspace_bytes",
 )
 
 
@@ -117,6 +123,14 @@ def load(path: str = None) -> ctypes.CDLL:
     lib.fp8_quantize_tokens.restype = ci
     lib.fp8_swiglu_quantize_tokens.argtypes = [vp, i64, vp, vp, i64, i64, ci, vp]
     lib.fp8_swiglu_quantize_tokens.restype = ci
+    lib.fp8_moe_route.argtypes = [vp, i64, ci, i64, i32, i32, ci, ctypes.c_float, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.fp8_moe_route.restype = ci
+    lib.fp8_moe_route_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.fp8_moe_route_workspace_bytes.restype = i64
+    lib.fp8_moe_layer.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, vp, i64, vp]
+    lib.fp8_moe_layer.restype = ci
+    lib.fp8_moe_layer_workspace_bytes.argtypes = [i64, i32, i64]
+    lib.fp8_moe_layer_workspace_bytes.restype = i64
     lib.fp8_status_query.argtypes = [vp, ctypes.POINTER(ci)]
     lib.fp8_status_query.restype = ci
     lib.fp8_strerror.argtypes = [ci]

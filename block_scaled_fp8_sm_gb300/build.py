@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libbsfp8.so")
 OBJ = os.path.join(HERE, "_build")
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["bsfp8_api.cu", "block128_api.cu"]
+SOURCES = ["bsfp8_api.cu", "block128_api.cu", "moe_api.cu"]
 
 
 def _nvcc() -> str:

@@ -44,40 +44,6 @@ int block128_setup() {
 
 namespace {
 
-constexpr int64_t kLim = int64_t(1) << 30;   // 32-bit indices in the kernels keep room for a tile past the end
-
-// Launches with programmatic stream serialization: the kernel's start overlaps the end of
-// the previous one of these kernels on the stream (each waits before it touches memory).
-template <typename Args>
-int launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, const Args &args, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[2] = {};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess) return FP8_OK;
-    (void)cudaGetLastError();   // reported here: not left for a later call
-    return FP8_ERR_CUDA;
-}
-
-// The tensor-map cache may fail to allocate: no exception leaves a C entry point.
-template <typename F>
-int guarded(F body) {
-    try {
-        return body();
-    } catch (...) {
-        return FP8_ERR_CUDA;
-    }
-}
-
 // Mode and sizes of both products.
 int check_sizes(int64_t M, int64_t N, int64_t K, int mode) {
     if (mode != FP8_PATH_AUTO && mode != FP8_PATH_NATIVE && mode != FP8_PATH_PROMOTE) return FP8_ERR_MODE;

@@ -117,6 +117,8 @@ int device_setup(DeviceState **out) {
     if (rc != FP8_OK) return rc;
     rc = block128_setup();
     if (rc != FP8_OK) return rc;
+    rc = moe_setup();
+    if (rc != FP8_OK) return rc;
     if (!d.status) {
         if (cudaMalloc(&d.status, 256) != cudaSuccess) return FP8_ERR_CUDA;
         // the clear lands before any kernel of a later call, whatever stream

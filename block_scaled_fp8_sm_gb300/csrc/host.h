@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "bsfp8.h"
+
 namespace bsfp8 {
 
 struct DeviceState {
@@ -37,5 +39,42 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 // Kernel attributes and other one-time work of the 128-granular entry points
 // (block128_api.cu); called by device_setup.
 int block128_setup();
+
+// The same of the mixture-of-experts entry points (moe_api.cu).
+int moe_setup();
+
+constexpr int64_t kLim = int64_t(1) << 30;   // 32-bit indices in the kernels keep room for a tile past the end
+
+// Launches with programmatic stream serialization: the kernel's start overlaps the end of
+// the previous one of these kernels on the stream (each waits before it touches memory).
+template <typename Args>
+int launch(void (*kernel)(Args), dim3 grid, int threads, int smem, int cluster, const Args &args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess) return FP8_OK;
+    (void)cudaGetLastError();   // reported here: not left for a later call
+    return FP8_ERR_CUDA;
+}
+
+// The tensor-map cache may fail to allocate: no exception leaves a C entry point.
+template <typename F>
+int guarded(F body) {
+    try {
+        return body();
+    } catch (...) {
+        return FP8_ERR_CUDA;
+    }
+}
 
 }  // namespace bsfp8

@@ -1,0 +1,186 @@
+// moe_api.cu -- host side of the mixture-of-experts entry points of include/bsfp8.h:
+// argument checks and launches of the router and of the layer for a few tokens.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bsfp8.h"
+#include "host.h"
+#include "moe_layer.cuh"
+#include "moe_route.cuh"
+
+namespace bsfp8 {
+
+namespace {
+
+template <int V>
+void (*pick_kernel(int type))(RouteArgs) {
+    return type == FP8_TYPE_BF16 ? bsfp8_route_pick<V, true> : bsfp8_route_pick<V, false>;
+}
+
+// A lane's experts: the least power of two that covers E.
+int lane_experts(int E) {
+    int v = 1;
+    while (32 * v < E) v *= 2;
+    return v;
+}
+
+void (*pick_kernel(int E, int type))(RouteArgs) {
+    switch (lane_experts(E)) {
+        case 1: return pick_kernel<1>(type);
+        case 2: return pick_kernel<2>(type);
+        case 4: return pick_kernel<4>(type);
+        case 8: return pick_kernel<8>(type);
+        case 16: return pick_kernel<16>(type);
+        default: return pick_kernel<32>(type);
+    }
+}
+
+bool set_shared(const void *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+// Tokens whose whole order one CTA makes.
+constexpr int64_t kOneCtaTokens = 64;
+
+// Tokens of a CTA of the ordered router: one CTA for few, else as even as the SMs allow.
+int64_t route_chunk(int64_t T) {
+    if (T <= kOneCtaTokens) return kOneCtaTokens;
+    const int64_t even = (T + ROUTE_CHUNKS - 1) / ROUTE_CHUNKS;
+    return even < ROUTE_WARPS ? ROUTE_WARPS : even;
+}
+
+int64_t route_chunks(int64_t T) { return T > 0 ? (T + route_chunk(T) - 1) / route_chunk(T) : 1; }
+
+bool layer_sizes(int64_t T, int32_t top, int64_t I) {
+    return T >= 0 && T <= FP8_MOE_MAX_TOKENS && top >= 1 && top <= FP8_MAX_TOP && I >= 0 && I < kLim && I % 16 == 0;
+}
+
+}  // namespace
+
+int moe_setup() {
+    for (int E = 32; E <= FP8_MAX_EXPERTS; E *= 2)
+        for (int type : {FP8_TYPE_F32, FP8_TYPE_BF16})
+            if (!set_shared(reinterpret_cast<const void *>(pick_kernel(E, type)), route_smem(E))) return FP8_ERR_CUDA;
+    return set_shared(reinterpret_cast<const void *>(bsfp8_route_order), route_smem(FP8_MAX_EXPERTS)) &&
+                   set_shared(reinterpret_cast<const void *>(bsfp8_moe_down),
+                              moe_down_shared(FP8_MOE_MAX_TOKENS, FP8_MAX_TOP, FP8_MAX_EXPERTS).bytes)
+               ? FP8_OK
+               : FP8_ERR_CUDA;
+}
+
+}  // namespace bsfp8
+
+using namespace bsfp8;
+
+static_assert(MOE_MAX_TOKENS == FP8_MOE_MAX_TOKENS && MOE_MAX_TOP == FP8_MAX_TOP && ROUTE_MAX_TOP == FP8_MAX_TOP &&
+                  MOE_MAX_EXPERTS == FP8_MAX_EXPERTS,
+              "limits of the kernels and of the header");
+
+extern "C" {
+
+int64_t fp8_moe_route_workspace_bytes(int64_t T, int32_t E, int32_t top) {
+    if (T < 0 || E < 1 || E > FP8_MAX_EXPERTS || top < 1 || top > FP8_MAX_TOP || top > E || T * top >= kLim) return 0;
+    const int64_t chunks = route_chunks(T);
+    return chunks > 1 ? 4 * (E + 1) * chunks : 0;
+}
+
+int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E, int32_t top, int flags, float scale,
+                  float *weights, int32_t *ids, int32_t *offsets, int32_t *rows, int32_t *places, void *workspace,
+                  int64_t workspace_bytes, cudaStream_t stream) {
+    if (type != FP8_TYPE_F32 && type != FP8_TYPE_BF16) return FP8_ERR_MODE;
+    if (flags & ~(FP8_ROUTE_SIGMOID | FP8_ROUTE_ALL)) return FP8_ERR_MODE;
+    if (T < 0 || T >= kLim || E < 1 || E > FP8_MAX_EXPERTS || top < 1 || top > FP8_MAX_TOP || top > E || ld < E ||
+        ld >= 2 * kLim || T * top >= kLim)
+        return FP8_ERR_SHAPE;
+    const bool order = offsets != nullptr;
+    if (!order && (rows || places)) return FP8_ERR_NULL;
+    if (T == 0 && !order) return FP8_OK;
+    if (T > 0 && (!logits || !weights || !ids || (order && (!rows || !places)))) return FP8_ERR_NULL;
+    const int64_t need = order ? fp8_moe_route_workspace_bytes(T, E, top) : 0;
+    if (need > 0 && !workspace) return FP8_ERR_NULL;
+    if (need > 0 && workspace_bytes < need) return FP8_ERR_SHAPE;
+    const int size = type == FP8_TYPE_F32 ? 4 : 2;
+    if (!aligned(logits, size) || !aligned(weights, 4) || !aligned(ids, 4) || !aligned(offsets, 4) ||
+        !aligned(rows, 4) || !aligned(places, 4) || (need > 0 && !aligned(workspace, 4)))
+        return FP8_ERR_ALIGN;
+    DeviceState *d = nullptr;
+    int rc = device_setup(&d);
+    if (rc != FP8_OK) return rc;
+    RouteArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.weights = weights;
+    a.ids = ids;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.places = places;
+    a.counts = static_cast<int32_t *>(workspace);
+    a.T = static_cast<int>(T);
+    a.E = E;
+    a.top = top;
+    a.sigmoid = (flags & FP8_ROUTE_SIGMOID) != 0;
+    a.all = (flags & FP8_ROUTE_ALL) != 0;
+    a.scale = scale;
+    // a lane loads its V neighbouring logits in pieces of up to 16 bytes, where every row
+    // starts and ends at such a piece's boundary
+    const int V = lane_experts(E), piece = V * size < 16 ? V * size : 16, values = piece / size;
+    a.vec = E % values == 0 && ld % values == 0 && aligned(logits, piece);
+    a.chunk = static_cast<int>(order ? route_chunk(T) : ROUTE_WARPS);
+    a.chunks = static_cast<int>(order ? route_chunks(T) : (T + ROUTE_WARPS - 1) / ROUTE_WARPS);
+    const int smem = order ? route_smem(E) : 0;
+    rc = launch(pick_kernel(E, type), dim3(static_cast<unsigned>(a.chunks)), ROUTE_THREADS, smem, 1, a, stream);
+    if (rc != FP8_OK || !order || a.chunks == 1) return rc;
+    return launch(bsfp8_route_order, dim3(static_cast<unsigned>(a.chunks)), ROUTE_THREADS, smem, 1, a, stream);
+}
+
+int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I) {
+    if (!layer_sizes(T, top, I)) return 0;
+    return T * top * (2 * I + I / 4);
+}
+
+int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
+                  const void *W2, const float *s2, void *out, int64_t T, int32_t top, int32_t E, int64_t H, int64_t I,
+                  void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+    if (!layer_sizes(T, top, I) || E < 0 || E > FP8_MAX_EXPERTS || H < 0 || H >= kLim || H % 16 != 0)
+        return FP8_ERR_SHAPE;
+    if (T == 0 || H == 0) return FP8_OK;
+    if (!out) return FP8_ERR_NULL;
+    if (!aligned(out, 16)) return FP8_ERR_ALIGN;
+    const bool work = E > 0 && I > 0;   // else the experts' sum is empty
+    if (work) {
+        if (!x || !weights || !ids || !W1 || !s1 || !W2 || !s2 || !workspace) return FP8_ERR_NULL;
+        if (workspace_bytes < fp8_moe_layer_workspace_bytes(T, top, I)) return FP8_ERR_SHAPE;
+        if (!aligned(x, 16) || !aligned(weights, 4) || !aligned(ids, 4) || !aligned(W1, 16) || !aligned(s1, 4) ||
+            !aligned(W2, 16) || !aligned(s2, 4) || !aligned(workspace, 16))
+            return FP8_ERR_ALIGN;
+    }
+    DeviceState *d = nullptr;
+    int rc = device_setup(&d);
+    if (rc != FP8_OK) return rc;
+    if (!work) return zero_fill(out, T * H, stream);
+    MoeArgs a{};
+    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.ids = ids;
+    a.w = weights;
+    a.W1 = static_cast<const uint8_t *>(W1);
+    a.W2 = static_cast<const uint8_t *>(W2);
+    a.s1 = s1;
+    a.s2 = s2;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.h = static_cast<__half *>(workspace);
+    a.hs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + T * top * 2 * I);
+    a.T = static_cast<int>(T);
+    a.top = top;
+    a.E = E;
+    a.H = static_cast<int>(H);
+    a.I = static_cast<int>(I);
+    const int64_t most = T * top < E ? T * top : E;
+    const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(most));
+    rc = launch(T <= 8 ? bsfp8_moe_up<1> : bsfp8_moe_up<2>, grid, MOE_THREADS, 0, 1, a, stream);
+    if (rc != FP8_OK) return rc;
+    return launch(bsfp8_moe_down, dim3(static_cast<unsigned>((H + MOE_DOWN_COLS - 1) / MOE_DOWN_COLS)), MOE_THREADS,
+                  moe_down_shared(a.T, top, E).bytes, 1, a, stream);
+}
+
+}  // extern "C"

@@ -415,6 +415,72 @@ int fp8_quantize_tokens(const void *x, int64_t ldx, int64_t x_rows, const int32_
 int fp8_swiglu_quantize_tokens(const void *x, int64_t ldx, void *q, float *s, int64_t M, int64_t K, int flags,
                                cudaStream_t stream);
 
+/* ------------------------------------------------ mixture of experts ----
+ * The router: for each token its `top` experts by logit, their weights, and the
+ * rows in expert order that fp8_quantize_tokens and fp8_gemm_experts take.
+ *   logits: [T, E] of type (FP8_TYPE_F32 or FP8_TYPE_BF16), rows of ld values.
+ *   ids:     int32 [T, top]: the experts by descending logit, equal logits in
+ *            ascending order of the expert.  A logit of -inf (or NaN) closes an
+ *            expert to the token: it is never taken.  Where fewer than top
+ *            are open, the last ids are -1 and their weights 0.
+ *   weights: fp32 [T, top]: softmax of the logits over the chosen experts, or
+ *            sigmoid of each divided by the chosen ones' sum
+ *            (FP8_ROUTE_SIGMOID); with FP8_ROUTE_ALL softmax over all open
+ *            experts, or the sigmoids themselves; times scale.
+ *   offsets: int32 [E+1], rows: int32 [T * top], places: int32 [T, top]; all
+ *            NULL: no order is made.  The pairs (token, expert) sorted by
+ *            expert, those of one expert by token and then by j: offsets[e] is
+ *            the first place of expert e and offsets[E] their number, rows[p]
+ *            the token at place p (-1 from offsets[E] on), places[t][j] the
+ *            place of pair (t, j) (-1 for an id of -1).  So
+ *            fp8_quantize_tokens with these rows makes the A of fp8_gemm_experts, and row
+ *            places[t][j] of its C is the j-th expert's result for token t.
+ * All but logits are written in full; weights, ids, offsets, rows and places must
+ * not overlap.  workspace: DEVICE memory of fp8_moe_route_workspace_bytes(T, E,
+ * top) bytes, 4-byte aligned, used with an order only (0 bytes: may be NULL);
+ * launches that overlap on the GPU need one each.
+ * 1 <= top <= min(E, FP8_MAX_TOP), E <= FP8_MAX_EXPERTS, ld >= E, T * top < 2^30.
+ * T == 0: nothing but offsets (zeros) is written.  Returns FP8_OK or FP8_ERR_SHAPE
+ * (a workspace that is too small, too) / FP8_ERR_NULL / FP8_ERR_ALIGN /
+ * FP8_ERR_MODE (type, flags) / FP8_ERR_CUDA. */
+#define FP8_MAX_TOP 32
+#define FP8_ROUTE_SIGMOID 1
+#define FP8_ROUTE_ALL 2
+int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E, int32_t top, int flags,
+                  float scale, float *weights, int32_t *ids, int32_t *offsets, int32_t *rows, int32_t *places,
+                  void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+int64_t fp8_moe_route_workspace_bytes(int64_t T, int32_t E, int32_t top);
+
+/* A whole mixture-of-experts layer for a few tokens (a decoding step), in two
+ * launches, on activations that are not quantized:
+ *
+ *   out[t] = bf16( sum_j weights[t][j] * D_e ( silu(G_e x_t) * (U_e x_t) ) ),  e = ids[t][j]
+ *
+ *   x:   bf16 [T, H];  out: bf16 [T, H], fully overwritten, no overlap with x.
+ *   W1:  E4M3 [E, 2I, H], rows [0, I) of an expert its gate G, rows [I, 2I) its
+ *        up U; s1: fp32 [E, ceil(2I/128), ceil(H/128)], one for each 128 x 128 block.
+ *   W2:  E4M3 [E, H, I], the down matrix D; s2: fp32 [E, ceil(H/128), ceil(I/128)].
+ *   ids: DEVICE int32 [T, top], weights: fp32 [T, top], as fp8_moe_route makes
+ *        them; read by the kernels only.  An id outside [0, E) takes no part (its
+ *        weight is not used); a token without any gets zeros.  An expert that a token
+ *        names twice counts with the sum of its weights.
+ * The products' sums, the gated activation and the weighted sum are fp32; between the two
+ * products the activation is held in 11 bits (fp16 with a power-of-two scale for 16 values).
+ * The sums' order is fixed: calls repeat bit for bit, and a token's result does not
+ * depend on the other tokens.
+ * T <= FP8_MOE_MAX_TOKENS (more: fp8_quantize_tokens, fp8_gemm_experts and
+ * fp8_swiglu_quantize_tokens), 1 <= top <= FP8_MAX_TOP, E <= FP8_MAX_EXPERTS, H and I
+ * multiples of 16 below 2^30.  x, W1, W2, out, workspace 16-byte, the others 4-byte
+ * aligned.  workspace: DEVICE memory of fp8_moe_layer_workspace_bytes(T, top, I)
+ * bytes; launches that overlap on the GPU need one each.  T == 0 or H == 0: nothing is
+ * enqueued; I == 0 or E == 0: out is zero-filled.  Returns FP8_OK or FP8_ERR_SHAPE (a
+ * workspace that is too small, too) / FP8_ERR_NULL / FP8_ERR_ALIGN / FP8_ERR_CUDA. */
+#define FP8_MOE_MAX_TOKENS 64
+int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
+                  const void *W2, const float *s2, void *out, int64_t T, int32_t top, int32_t E, int64_t H,
+                  int64_t I, void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I);
+
 /* Synchronises `stream`, then reads and clears the current device's status
  * words: the one the regular entry points write (including FP8_ERR_RECORD
  * from fp8_gemm_grouped_device) and word 0 of the
