@@ -8,6 +8,7 @@
 #include "host.h"
 #include "moe_layer.cuh"
 #include "moe_route.cuh"
+#include "moe_tile.cuh"
 
 namespace bsfp8 {
 
@@ -40,6 +41,26 @@ bool set_shared(const void *kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
+template <int NG>
+bool set_tile_shared() {
+    return set_shared(reinterpret_cast<const void *>(bsfp8_moe_tile<false, NG>), MT_SMEM) &&
+           set_shared(reinterpret_cast<const void *>(bsfp8_moe_tile<true, NG>), MT_SMEM);
+}
+
+// Both kernels of the layer for up to 8 NG tokens.
+template <int NG>
+int launch_tiles(MoeTileArgs &a, cudaStream_t stream) {
+    int rc = encode_kmajor(&a.tmW, a.W1, static_cast<int64_t>(a.E) * 2 * a.I, a.H, 16);
+    if (rc != FP8_OK) return rc;
+    a.ring = (MT_SMEM - smem_moe_fixed<false>(a.T, a.top, a.E)) / 1024 * 1024;
+    rc = launch(bsfp8_moe_tile<false, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
+    if (rc != FP8_OK) return rc;
+    rc = encode_kmajor(&a.tmW, a.W2, static_cast<int64_t>(a.E) * a.H, a.I, 128);
+    if (rc != FP8_OK) return rc;
+    a.ring = (MT_SMEM - smem_moe_fixed<true>(a.T, a.top, a.E)) / 1024 * 1024;
+    return launch(bsfp8_moe_tile<true, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
+}
+
 // Tokens whose whole order one CTA makes.
 constexpr int64_t kOneCtaTokens = 64;
 
@@ -64,7 +85,8 @@ int moe_setup() {
             if (!set_shared(reinterpret_cast<const void *>(pick_kernel(E, type)), route_smem(E))) return FP8_ERR_CUDA;
     return set_shared(reinterpret_cast<const void *>(bsfp8_route_order), route_smem(FP8_MAX_EXPERTS)) &&
                    set_shared(reinterpret_cast<const void *>(bsfp8_moe_down),
-                              moe_down_shared(FP8_MOE_MAX_TOKENS, FP8_MAX_TOP, FP8_MAX_EXPERTS).bytes)
+                              moe_down_shared(MOE_FEW_TOKENS, FP8_MAX_TOP, FP8_MAX_EXPERTS)) &&
+                   set_tile_shared<2>() && set_tile_shared<4>() && set_tile_shared<8>()
                ? FP8_OK
                : FP8_ERR_CUDA;
 }
@@ -136,7 +158,8 @@ int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E
 
 int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I) {
     if (!layer_sizes(T, top, I)) return 0;
-    return T * top * (2 * I + I / 4);
+    const int64_t h = T * top * (2 * I + I / 4);
+    return T <= MOE_FEW_TOKENS ? h : (h + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * 128 * 4 + MT_CTAS * 4;
 }
 
 int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
@@ -144,6 +167,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
                   void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
     if (!layer_sizes(T, top, I) || E < 0 || E > FP8_MAX_EXPERTS || H < 0 || H >= kLim || H % 16 != 0)
         return FP8_ERR_SHAPE;
+    if (E * 2 * I >= 2 * kLim || E * H >= 2 * kLim) return FP8_ERR_SHAPE;
     if (T == 0 || H == 0) return FP8_OK;
     if (!out) return FP8_ERR_NULL;
     if (!aligned(out, 16)) return FP8_ERR_ALIGN;
@@ -159,7 +183,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
     int rc = device_setup(&d);
     if (rc != FP8_OK) return rc;
     if (!work) return zero_fill(out, T * H, stream);
-    MoeArgs a{};
+    MoeTileArgs a{};
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.ids = ids;
     a.w = weights;
@@ -175,12 +199,23 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
     a.E = E;
     a.H = static_cast<int>(H);
     a.I = static_cast<int>(I);
+    if (T > MOE_FEW_TOKENS) {
+        uint8_t *rest = static_cast<uint8_t *>(workspace) + (T * top * (2 * I + I / 4) + 255) / 256 * 256;
+        a.part = reinterpret_cast<float *>(rest);
+        a.counters = reinterpret_cast<int *>(rest + int64_t(2) * MT_CTAS * T * 128 * 4);
+        a.status = d->status;
+        a.wait_limit = wait_limit();
+        return guarded([&] {
+            return T <= 16 ? launch_tiles<2>(a, stream) : T <= 32 ? launch_tiles<4>(a, stream) : launch_tiles<8>(a, stream);
+        });
+    }
+    const MoeArgs &few = a;
     const int64_t most = T * top < E ? T * top : E;
     const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(most));
-    rc = launch(T <= 8 ? bsfp8_moe_up<1> : bsfp8_moe_up<2>, grid, MOE_THREADS, 0, 1, a, stream);
+    rc = launch(bsfp8_moe_up<1>, grid, MOE_THREADS, 0, 1, few, stream);
     if (rc != FP8_OK) return rc;
     return launch(bsfp8_moe_down, dim3(static_cast<unsigned>((H + MOE_DOWN_COLS - 1) / MOE_DOWN_COLS)), MOE_THREADS,
-                  moe_down_shared(a.T, top, E).bytes, 1, a, stream);
+                  moe_down_shared(a.T, top, E), 1, few, stream);
 }
 
 }  // extern "C"

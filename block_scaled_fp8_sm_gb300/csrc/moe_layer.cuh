@@ -28,6 +28,7 @@
 
 namespace bsfp8 {
 
+constexpr int MOE_FEW_TOKENS = 8;   // the kernels of this file; more: moe_tile.cuh
 constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 32, MOE_MAX_EXPERTS = 1024;
 constexpr int MOE_WARPS = 8, MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_UP_COLS = 16;     // columns of h per CTA: 16 gate and 16 up rows
@@ -270,54 +271,62 @@ __global__ void __launch_bounds__(MOE_THREADS, NT == 1 ? 2 : 1) bsfp8_moe_up(con
     launch_dependents();
 }
 
-// Shared memory of the down kernel: entries of all experts, their lists, sums.
-struct MoeDownShared {
-    int entries, start, busy, pair, weight, sums, bytes;   // offsets
+// The experts' tokens, in shared memory.  An expert's entries stand from start[e] to
+// start[e + 1], one for each of its tokens.
+struct MoeLists {
+    int *start;          // [E + 1]
+    int *experts;        // how many are busy, the most tokens of one, and
+    uint16_t *busy;      // [E] which, ascending
+    uint16_t *pair;      // [pairs] the row of h: the token's first pair with the expert
+    uint16_t *token;     // [pairs]
+    float *weight;       // [pairs] the sum of the token's weights for the expert
 };
 
 __host__ __device__ constexpr int moe_pad16(int v) { return (v + 15) / 16 * 16; }
 
-__host__ __device__ inline MoeDownShared moe_down_shared(int T, int top, int E) {
-    MoeDownShared s{};
-    s.start = 0;                                           // int [E + 1]: first entry of each expert
-    s.busy = moe_pad16(4 * (E + 1));                       // uint16 [min(E, pairs)]
-    s.pair = s.busy + moe_pad16(2 * E);                    // uint16 [pairs]
-    s.weight = s.pair + moe_pad16(2 * T * top);            // float [pairs]
-    s.sums = s.weight + moe_pad16(4 * T * top);            // float [warps][T][columns + 8]
-    s.bytes = s.sums + 4 * MOE_WARPS * T * (MOE_DOWN_COLS + 8);
+struct MoeListsLayout {
+    int start, busy, pair, token, weight, bytes;   // offsets
+};
+
+__host__ __device__ inline MoeListsLayout moe_lists_layout(int T, int top, int E) {
+    MoeListsLayout s{};
+    s.start = 16;   // the number of busy experts is before it
+    s.busy = s.start + moe_pad16(4 * (E + 1));
+    s.pair = s.busy + moe_pad16(2 * E);
+    s.token = s.pair + moe_pad16(2 * T * top);
+    s.weight = s.token + moe_pad16(2 * T * top);
+    s.bytes = s.weight + moe_pad16(4 * T * top);
     return s;
 }
 
-// Down and the weighted sum: a CTA owns 32 columns of the output for all tokens and
-// passes over the busy experts in ascending order.  Each warp adds what its K blocks give
-// to sums of its own in shared memory.
-__global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_down(const MoeArgs a) {
-    extern __shared__ __align__(16) uint8_t moe_smem[];
-    __shared__ int experts;
-    const MoeDownShared o = moe_down_shared(a.T, a.top, a.E);
-    int *start = reinterpret_cast<int *>(moe_smem + o.start);
-    uint16_t *busy = reinterpret_cast<uint16_t *>(moe_smem + o.busy);
-    uint16_t *pair_of = reinterpret_cast<uint16_t *>(moe_smem + o.pair);
-    float *weight_of = reinterpret_cast<float *>(moe_smem + o.weight);
-    float *sums = reinterpret_cast<float *>(moe_smem + o.sums);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int pairs = a.T * a.top, n0 = static_cast<int>(blockIdx.x) * MOE_DOWN_COLS;
-    constexpr int LD = MOE_DOWN_COLS + 8;
-    for (int i = threadIdx.x; i <= a.E; i += MOE_THREADS) start[i] = 0;
-    for (int i = threadIdx.x; i < MOE_WARPS * a.T * LD; i += MOE_THREADS) sums[i] = 0.0f;
+__device__ __forceinline__ MoeLists moe_lists(uint8_t *at, int T, int top, int E) {
+    const MoeListsLayout o = moe_lists_layout(T, top, E);
+    MoeLists l;
+    l.experts = reinterpret_cast<int *>(at);
+    l.start = reinterpret_cast<int *>(at + o.start);
+    l.busy = reinterpret_cast<uint16_t *>(at + o.busy);
+    l.pair = reinterpret_cast<uint16_t *>(at + o.pair);
+    l.token = reinterpret_cast<uint16_t *>(at + o.token);
+    l.weight = reinterpret_cast<float *>(at + o.weight);
+    return l;
+}
+
+// Made by the whole CTA.  Entries are counted, then placed from the end of the expert's range
+// (their order does not matter: each is a column of its own).
+__device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l) {
+    const int lane = threadIdx.x & 31, threads = blockDim.x, pairs = a.T * a.top;
+    for (int i = threadIdx.x; i <= a.E; i += threads) l.start[i] = 0;
     __syncthreads();
-    wait_for_previous();
-    // entries of each expert: counted, then placed from the end of the expert's range (their
-    // order does not matter: each is a column of its own)
-    for (int p = threadIdx.x; p < pairs; p += MOE_THREADS) {
+    for (int p = threadIdx.x; p < pairs; p += threads) {
         const int e = a.ids[p];
-        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E) && first_of_token(a, p, e)) atomicAdd(&start[e], 1);
+        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E) && first_of_token(a, p, e)) atomicAdd(&l.start[e], 1);
     }
     __syncthreads();
-    if (warp == 0) {
-        int base = 0, used = 0;
+    if (threadIdx.x < 32) {
+        int base = 0, used = 0, most = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane, c = e < a.E ? start[e] : 0;
+            const int e = e0 + lane, c = e < a.E ? l.start[e] : 0;
+            most = max(most, c);
             int sum = c;
 #pragma unroll
             for (int k = 1; k < 32; k <<= 1) {
@@ -325,34 +334,58 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_down(const MoeArgs a
                 if (lane >= k) sum += v;
             }
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, c > 0);
-            if (e < a.E) start[e] = base + sum;   // the end of its range
-            if (c > 0) busy[used + __popc(mask & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
+            if (e < a.E) l.start[e] = base + sum;   // the end of its range
+            if (c > 0) l.busy[used + __popc(mask & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
             base += __shfl_sync(0xFFFFFFFFu, sum, 31);
             used += __popc(mask);
         }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
         if (lane == 0) {
-            experts = used;
-            start[a.E] = base;
+            l.experts[0] = used;
+            l.experts[1] = most;
+            l.start[a.E] = base;
         }
     }
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += MOE_THREADS) {
+    for (int p = threadIdx.x; p < pairs; p += threads) {
         const int e = a.ids[p];
         if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E) && first_of_token(a, p, e)) {
+            const int t = p / a.top;
             float w = 0.0f;
-            for (int q = p; q < p - p % a.top + a.top; ++q)
+            for (int q = p; q < (t + 1) * a.top; ++q)
                 if (a.ids[q] == e) w += a.w[q];
-            const int at = atomicSub(&start[e], 1) - 1;
-            pair_of[at] = static_cast<uint16_t>(p);
-            weight_of[at] = w;
+            const int at = atomicSub(&l.start[e], 1) - 1;
+            l.pair[at] = static_cast<uint16_t>(p);
+            l.token[at] = static_cast<uint16_t>(t);
+            l.weight[at] = w;
         }
     }
     __syncthreads();
+}
+
+// Shared memory of the down kernel: the lists, and sums [warps][T][columns + 8].
+__host__ __device__ inline int moe_down_shared(int T, int top, int E) {
+    return moe_lists_layout(T, top, E).bytes + 4 * MOE_WARPS * T * (MOE_DOWN_COLS + 8);
+}
+
+// Down and the weighted sum: a CTA owns 32 columns of the output for all tokens and
+// passes over the busy experts in ascending order.  Each warp adds what its K blocks give
+// to sums of its own in shared memory.
+__global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_down(const MoeArgs a) {
+    extern __shared__ __align__(16) uint8_t moe_smem[];
+    const MoeLists L = moe_lists(moe_smem, a.T, a.top, a.E);
+    float *sums = reinterpret_cast<float *>(moe_smem + moe_lists_layout(a.T, a.top, a.E).bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n0 = static_cast<int>(blockIdx.x) * MOE_DOWN_COLS;
+    constexpr int LD = MOE_DOWN_COLS + 8;
+    for (int i = threadIdx.x; i < MOE_WARPS * a.T * LD; i += MOE_THREADS) sums[i] = 0.0f;
+    wait_for_previous();
+    build_lists(a, L);
     const int KB = (a.I + 127) / 128, NB = (a.H + 127) / 128, chunks = a.I / 16;
     const bool second = n0 + 16 < a.H;   // H is a multiple of 16
     float *mine = sums + warp * a.T * LD;
-    for (int b = 0; b < experts; ++b) {
-        const int e = busy[b], first = start[e], n = start[e + 1] - first;
+    for (int b = 0; b < *L.experts; ++b) {
+        const int e = L.busy[b], first = L.start[e], n = L.start[e + 1] - first;
         const uint8_t *W = a.W2 + (static_cast<int64_t>(e) * a.H + n0 + g) * a.I + 16 * t;
         const float *s2 = a.s2 + (static_cast<int64_t>(e) * NB + n0 / 128) * KB;
         // K block kb of expert e belongs to warp (e KB + kb) mod warps
@@ -372,7 +405,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_down(const MoeArgs a
             for (int m0 = 0; m0 < n; m0 += 8) {
                 uint32_t xh[1][16];
                 float sc[2];
-                const int64_t pair = m0 + g < n ? pair_of[first + m0 + g] : -1;
+                const int64_t pair = m0 + g < n ? L.pair[first + m0 + g] : -1;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int k = kb * 128 + 64 * j + 16 * t;
@@ -407,8 +440,8 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_down(const MoeArgs a
                     const float s = sb * __shfl_sync(0xFFFFFFFFu, most, 8 * t + 4 * c);
                     const int m = m0 + 2 * t + c;
                     if (m < n) {
-                        const float f = s * weight_of[first + m];
-                        float *to = mine + pair_of[first + m] / a.top * LD + g;
+                        const float f = s * L.weight[first + m];
+                        float *to = mine + L.token[first + m] * LD + g;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             to[16 * i] = fmaf(f, p[0][i][c], to[16 * i]);
