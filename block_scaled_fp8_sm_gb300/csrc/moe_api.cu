@@ -52,12 +52,12 @@ template <int NG>
 int launch_tiles(MoeTileArgs &a, cudaStream_t stream) {
     int rc = encode_kmajor(&a.tmW, a.W1, static_cast<int64_t>(a.E) * 2 * a.I, a.H, 16);
     if (rc != FP8_OK) return rc;
-    a.ring = (MT_SMEM - smem_moe_fixed<false>(a.T, a.top, a.E)) / 1024 * 1024;
+    a.ring = (MT_SMEM - smem_moe_fixed<false, NG>(a.T, a.top, a.E)) / 1024 * 1024;
     rc = launch(bsfp8_moe_tile<false, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
     if (rc != FP8_OK) return rc;
     rc = encode_kmajor(&a.tmW, a.W2, static_cast<int64_t>(a.E) * a.H, a.I, 128);
     if (rc != FP8_OK) return rc;
-    a.ring = (MT_SMEM - smem_moe_fixed<true>(a.T, a.top, a.E)) / 1024 * 1024;
+    a.ring = (MT_SMEM - smem_moe_fixed<true, NG>(a.T, a.top, a.E)) / 1024 * 1024;
     return launch(bsfp8_moe_tile<true, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
 }
 

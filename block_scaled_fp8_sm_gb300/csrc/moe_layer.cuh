@@ -280,12 +280,14 @@ struct MoeLists {
     uint16_t *pair;      // [pairs] the row of h: the token's first pair with the expert
     uint16_t *token;     // [pairs]
     float *weight;       // [pairs] the sum of the token's weights for the expert
+    uint16_t *id;        // [pairs] while the lists are made: the pairs' experts,
+    uint8_t *number;     // [pairs] and their numbers among the expert's
 };
 
 __host__ __device__ constexpr int moe_pad16(int v) { return (v + 15) / 16 * 16; }
 
 struct MoeListsLayout {
-    int start, busy, pair, token, weight, bytes;   // offsets
+    int start, busy, pair, token, weight, id, number, bytes;   // offsets
 };
 
 __host__ __device__ inline MoeListsLayout moe_lists_layout(int T, int top, int E) {
@@ -295,7 +297,9 @@ __host__ __device__ inline MoeListsLayout moe_lists_layout(int T, int top, int E
     s.pair = s.busy + moe_pad16(2 * E);
     s.token = s.pair + moe_pad16(2 * T * top);
     s.weight = s.token + moe_pad16(2 * T * top);
-    s.bytes = s.weight + moe_pad16(4 * T * top);
+    s.id = s.weight + moe_pad16(4 * T * top);
+    s.number = s.id + moe_pad16(2 * T * top);
+    s.bytes = s.number + moe_pad16(T * top);
     return s;
 }
 
@@ -308,18 +312,28 @@ __device__ __forceinline__ MoeLists moe_lists(uint8_t *at, int T, int top, int E
     l.pair = reinterpret_cast<uint16_t *>(at + o.pair);
     l.token = reinterpret_cast<uint16_t *>(at + o.token);
     l.weight = reinterpret_cast<float *>(at + o.weight);
+    l.id = reinterpret_cast<uint16_t *>(at + o.id);
+    l.number = at + o.number;
     return l;
 }
 
-// Made by the whole CTA.  Entries are counted, then placed from the end of the expert's range
-// (their order does not matter: each is a column of its own).
+// Made by the whole CTA: the ids come to shared memory, each pair that is its token's first
+// with the expert takes a number there, and the ranges follow from how many there are (the
+// order in a range does not matter: each entry is a column of its own).
 __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l) {
     const int lane = threadIdx.x & 31, threads = blockDim.x, pairs = a.T * a.top;
+    constexpr uint16_t NONE = 0xFFFF;
     for (int i = threadIdx.x; i <= a.E; i += threads) l.start[i] = 0;
+    for (int p = threadIdx.x; p < pairs; p += threads) {
+        const uint32_t e = static_cast<uint32_t>(a.ids[p]);
+        l.id[p] = e < static_cast<uint32_t>(a.E) ? static_cast<uint16_t>(e) : NONE;
+    }
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += threads) {
-        const int e = a.ids[p];
-        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E) && first_of_token(a, p, e)) atomicAdd(&l.start[e], 1);
+        const uint16_t e = l.id[p];
+        bool first = e != NONE;
+        for (int q = p - p % a.top; q < p; ++q) first &= l.id[q] != e;
+        l.number[p] = first ? static_cast<uint8_t>(atomicAdd(&l.start[e], 1)) : 255;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -334,7 +348,7 @@ __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l)
                 if (lane >= k) sum += v;
             }
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, c > 0);
-            if (e < a.E) l.start[e] = base + sum;   // the end of its range
+            if (e < a.E) l.start[e] = base + sum - c;
             if (c > 0) l.busy[used + __popc(mask & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
             base += __shfl_sync(0xFFFFFFFFu, sum, 31);
             used += __popc(mask);
@@ -348,17 +362,14 @@ __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l)
     }
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += threads) {
-        const int e = a.ids[p];
-        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E) && first_of_token(a, p, e)) {
-            const int t = p / a.top;
-            float w = 0.0f;
-            for (int q = p; q < (t + 1) * a.top; ++q)
-                if (a.ids[q] == e) w += a.w[q];
-            const int at = atomicSub(&l.start[e], 1) - 1;
-            l.pair[at] = static_cast<uint16_t>(p);
-            l.token[at] = static_cast<uint16_t>(t);
-            l.weight[at] = w;
-        }
+        if (l.number[p] == 255) continue;
+        const int e = l.id[p], t = p / a.top, at = l.start[e] + l.number[p];
+        float w = a.w[p];
+        for (int q = p + 1; q < (t + 1) * a.top; ++q)
+            if (l.id[q] == e) w += a.w[q];
+        l.pair[at] = static_cast<uint16_t>(p);
+        l.token[at] = static_cast<uint16_t>(t);
+        l.weight[at] = w;
     }
     __syncthreads();
 }

@@ -18,7 +18,7 @@
 //
 // Up: a tile is 64 columns of h, 16 gate rows and 16 up rows in turn, so that a warp holds
 // both; CTAs take tiles in turn.  Down: a tile is 128 columns of the output with all busy
-// experts one after the other, summed in shared memory; the K blocks of all tiles are one
+// experts one after the other, summed in shared memory; the stages of all tiles are one
 // line, cut into equal pieces for the CTAs.  Where a cut goes through a tile, the parts go to
 // the workspace and the CTA that comes last adds them in order: no CTA waits for another,
 // and calls repeat bit for bit.
@@ -33,9 +33,9 @@ namespace bsfp8 {
 
 constexpr int MT_THREADS = 384;
 constexpr int MT_CTAS = 152;           // one for each SM
-constexpr int MT_MAX_STAGES = 12;
+constexpr int MT_MAX_STAGES = 6;
 constexpr int MT_MAKERS = 6;           // warps that make codes
-constexpr int MT_SX_RING = 16;         // slots of scales: stages and partials together
+constexpr int MT_SX_RING = 32;         // slots of scales: the K blocks of all stages and partials, and more
 constexpr int MT_SMEM = 232448;        // all that a CTA can have
 
 struct MoeTileArgs : MoeArgs {
@@ -51,29 +51,30 @@ struct MoeTileArgs : MoeArgs {
 template <bool DOWN, int NG>
 struct CfgMoe {
     static constexpr int PIECES = DOWN ? 3 : 2;
-    static constexpr int A_BYTES = 128 * 128;
-    // Tensor memory: partials of 8 NG columns, then 4 columns of scales for each code
-    static constexpr int STRIDE = 8 * NG;
-    static constexpr int BUFS = 4;
+    static constexpr int A_BYTES = 128 * 128;   // weights of a K block; a stage has two
+    // Tensor memory: partials of 8 NG columns for each of a stage's blocks, then 4 columns of
+    // scales for each code
+    static constexpr int STRIDE = 16 * NG;
+    static constexpr int BUFS = NG == 8 ? 3 : 4;
     static constexpr int SF = BUFS * STRIDE;
-    static constexpr int COLS = NG == 2 ? 128 : NG == 4 ? 256 : 512;
+    static constexpr int COLS = NG == 2 ? 256 : 512;
 };
 
-template <bool DOWN>
+template <bool DOWN, int NG>
 struct CtrlMoe {
     uint64_t full[MT_MAX_STAGES], empty[MT_MAX_STAGES];   // full: the weights and the codes
     uint64_t tfull[4], tempty[4], drain;
     uint32_t tmem;
     int abort, last;
     alignas(16) uint32_t sf[3][32];                     // the codes' scales: 1, 2^-5, 2^-10 as UE8M0 bytes
-    alignas(16) float sx[MT_SX_RING][MOE_MAX_TOKENS];   // read four at a time
-    alignas(16) float sums[DOWN ? MOE_MAX_TOKENS : 1][128];
+    alignas(16) float sx[MT_SX_RING][8 * NG];   // read four at a time
+    alignas(16) float sums[DOWN ? 8 * NG : 1][128];
 };
 
 // Shared memory beside the stages, which get the rest.
-template <bool DOWN>
+template <bool DOWN, int NG>
 inline int smem_moe_fixed(int T, int top, int E) {
-    return 1024 + moe_pad16(static_cast<int>(sizeof(CtrlMoe<DOWN>))) + moe_lists_layout(T, top, E).bytes;
+    return 1024 + moe_pad16(static_cast<int>(sizeof(CtrlMoe<DOWN, NG>))) + moe_lists_layout(T, top, E).bytes;
 }
 
 template <typename Ctl>
@@ -93,22 +94,22 @@ __device__ __forceinline__ bool wait_moe(uint64_t *bar, uint32_t parity, Ctl *ct
     }
 }
 
-// A run of K blocks of one expert in one tile.
+// A run of stages (two 128-K blocks each) of one expert in one tile.
 struct MoeSeg {
-    int b, c, k0, k1;   // number of the busy expert, tile, K blocks [k0, k1)
+    int b, c, k0, k1;   // number of the busy expert, tile, stages [k0, k1) of its K
     bool end;           // the tile's last
 };
 
 // The segments of this CTA in order; every role walks them alike.
 template <bool DOWN>
 struct MoeWalk {
-    int64_t pos, end, all;   // down: the K blocks of all tiles,
+    int64_t pos, end, all;   // down: the stages of all tiles,
     int ctas;                // and the CTAs that have some
-    int busy, KB, tiles;
+    int busy, KS, tiles;     // KS: stages of a tile's K
 
-    __device__ __forceinline__ MoeWalk(int busy_, int KB_, int tiles_) : busy(busy_), KB(KB_), tiles(tiles_) {
+    __device__ __forceinline__ MoeWalk(int busy_, int KS_, int tiles_) : busy(busy_), KS(KS_), tiles(tiles_) {
         if constexpr (DOWN) {
-            all = static_cast<int64_t>(tiles) * busy * KB;
+            all = static_cast<int64_t>(tiles) * busy * KS;
             ctas = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
             const bool in = static_cast<int>(blockIdx.x) < ctas;
             pos = in ? all * blockIdx.x / ctas : 0;
@@ -121,21 +122,21 @@ struct MoeWalk {
     __device__ __forceinline__ bool next(MoeSeg &s) {
         if (pos >= end) return false;
         if constexpr (DOWN) {
-            const int64_t per = static_cast<int64_t>(busy) * KB;
+            const int64_t per = static_cast<int64_t>(busy) * KS;
             const int64_t c = pos / per;
             const int in = static_cast<int>(pos - c * per);
             s.c = static_cast<int>(c);
-            s.b = in / KB;
-            s.k0 = in - s.b * KB;
-            s.k1 = static_cast<int>(min(static_cast<int64_t>(KB), s.k0 + (end - pos)));
-            s.end = s.b + 1 == busy && s.k1 == KB;
+            s.b = in / KS;
+            s.k0 = in - s.b * KS;
+            s.k1 = static_cast<int>(min(static_cast<int64_t>(KS), s.k0 + (end - pos)));
+            s.end = s.b + 1 == busy && s.k1 == KS;
             pos += s.k1 - s.k0;
         } else {
             const int i = static_cast<int>(pos);
             s.b = i / tiles;
             s.c = i - s.b * tiles;
             s.k0 = 0;
-            s.k1 = KB;
+            s.k1 = KS;
             s.end = true;
             pos += gridDim.x;
         }
@@ -166,49 +167,65 @@ __device__ __forceinline__ uint32_t take_codes(__half2 (&v)[2]) {
     return w;
 }
 
-// Scales of the weights' K blocks k .. k + 15 of a segment, one in a lane of each half of a
+// Scales of the weights' K blocks 2 k .. 2 k + 15 of a tile, one in a lane of each half of a
 // warp; sw: those of the thread's row, which are the same for a half.
-__device__ __forceinline__ float row_scales(const float *sw, const MoeSeg &s, int k) {
-    return sw[min(k + static_cast<int>(threadIdx.x & 15), s.k1 - 1)];
+__device__ __forceinline__ float row_scales(const float *sw, int KB, int k) {
+    return sw[min(2 * k + static_cast<int>(threadIdx.x & 15), KB - 1)];
 }
 
 __device__ __forceinline__ void store_bf16x4(__nv_bfloat16 *to, float4 v) {
     *reinterpret_cast<uint2 *>(to) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
 }
 
-// The epilogue's sum over the K blocks of a segment: acc[token].  next: its first scales.
+// The epilogue's sum over the stages of a segment: acc[token].  next: its first scales.
 template <bool DOWN, int NG, typename Ctl>
 __device__ __forceinline__ bool sum_blocks(const MoeTileArgs &a, Ctl *ctl, float (&acc)[8 * NG], const MoeSeg &s,
-                                           const float *sw, float next, int ng, uint32_t taddr, int &it, int &b, uint32_t &bph) {
+                                           const float *sw, float next, int KB, int ng, uint32_t taddr, int &it, int &b,
+                                           uint32_t &bph) {
     using C = CfgMoe<DOWN, NG>;
 #pragma unroll
     for (int j = 0; j < 8 * NG; ++j) acc[j] = 0.0f;
     const int lane = threadIdx.x & 31;
     float have = 0.0f;
-    for (int kb = s.k0; kb < s.k1; ++kb) {
-        const int in = (kb - s.k0) & 15;
+    for (int ks = s.k0; ks < s.k1; ++ks) {
+        const int in = 2 * (ks - s.k0) & 15;
         if (in == 0) {
             have = next;
-            next = row_scales(sw, s, kb + 16);
+            next = row_scales(sw, KB, ks + 8);
         }
-        const float w = __shfl_sync(0xFFFFFFFFu, have, (lane & 16) + in);
+        const float w0 = __shfl_sync(0xFFFFFFFFu, have, (lane & 16) + in);
+        const float w1 = __shfl_sync(0xFFFFFFFFu, have, (lane & 16) + in + 1);
         if (!__all_sync(0xFFFFFFFFu, wait_moe(&ctl->tfull[b], bph, ctl, a))) return false;
         tc_fence_after();
-        const float4 *sx = reinterpret_cast<const float4 *>(ctl->sx[it % MT_SX_RING]);
+        const bool two = 2 * ks + 1 < KB;
+        const float4 *sx0 = reinterpret_cast<const float4 *>(ctl->sx[2 * it % MT_SX_RING]);
+        const float4 *sx1 = reinterpret_cast<const float4 *>(ctl->sx[(2 * it + 1) % MT_SX_RING]);
 #pragma unroll
         for (int g = 0; g < NG; g += 2) {   // sixteen tokens at a time
             if (g < ng) {
-                uint32_t p[16];
+                uint32_t p[16], r[16];
                 tmem_ld_x16(taddr + b * C::STRIDE + 8 * g, p);
-                float f[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 v = sx[2 * g + j];
-                    f[4 * j] = w * v.x, f[4 * j + 1] = w * v.y, f[4 * j + 2] = w * v.z, f[4 * j + 3] = w * v.w;
-                }
+                if (two) tmem_ld_x16(taddr + b * C::STRIDE + 8 * NG + 8 * g, r);
                 tmem_ld_wait_for(p);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[8 * g + j] = fmaf(f[j], __uint_as_float(p[j]), acc[8 * g + j]);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 v = sx0[2 * g + j];
+                    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[8 * g + 4 * j + k] = fmaf(w0 * f[k], __uint_as_float(p[4 * j + k]), acc[8 * g + 4 * j + k]);
+                }
+                if (two) {
+                    tmem_ld_wait_for(r);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 v = sx1[2 * g + j];
+                        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            acc[8 * g + 4 * j + k] = fmaf(w1 * f[k], __uint_as_float(r[4 * j + k]), acc[8 * g + 4 * j + k]);
+                    }
+                }
             }
         }
         tc_fence_before();
@@ -226,7 +243,7 @@ __device__ __forceinline__ bool sum_blocks(const MoeTileArgs &a, Ctl *ctl, float
 template <bool DOWN, int NG>
 __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_constant__ MoeTileArgs a) {
     using C = CfgMoe<DOWN, NG>;
-    using Ctl = CtrlMoe<DOWN>;
+    using Ctl = CtrlMoe<DOWN, NG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + a.ring);
@@ -235,7 +252,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MT_MAX_STAGES; ++s) {
-            mbar_init(&ctl->full[s], 2);
+            mbar_init(&ctl->full[s], 3);   // the weights and the codes of two blocks
             mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 4; ++b) {
@@ -270,17 +287,19 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
-    // a stage: 128 rows of weights, and the codes of as many tokens as an expert has at most
-    const int busy = L.experts[0];
-    // (rows of eight tokens for each code; the MMA takes an even number of eights)
-    const int most = (L.experts[1] + 7) / 8, stage_bytes = C::A_BYTES + (C::PIECES * most + (most & 1)) * 1024;
+    // a stage: two K blocks of the weights' 128 rows, and the codes of as many tokens as an
+    // expert has at most (rows of eight tokens for each code; the MMA takes an even number)
+    const int busy = L.experts[0], most = (L.experts[1] + 7) / 8;
+    const int code_bytes = (C::PIECES * most + (most & 1)) * 1024;   // of a block
+    const int stage_bytes = 2 * (C::A_BYTES + code_bytes);
     const int stages = min(MT_MAX_STAGES, a.ring / stage_bytes);
-    // Warps that make codes.  Not more than stages: a maker that looked further ahead would
-    // meet an `empty` barrier two rounds behind, whose parity says that the stage is free.
-    const int makers = min(MT_MAKERS, stages);
-    const int K = DOWN ? a.I : a.H, KB = (K + 127) / 128;
+    // Warps that make codes, a block each in turn.  Not more than all stages have blocks: a
+    // maker that looked further ahead would meet an `empty` barrier two rounds behind, whose
+    // parity says that the stage is free.
+    const int makers = min(MT_MAKERS, 2 * stages);
+    const int K = DOWN ? a.I : a.H, KB = (K + 127) / 128, KS = (KB + 1) / 2;
     const int tiles = DOWN ? (a.H + 127) / 128 : (a.I + 63) / 64;
-    MoeWalk<DOWN> walk(busy, KB, tiles);
+    MoeWalk<DOWN> walk(busy, KS, tiles);
     const MoeWalk<DOWN> whole = walk;
     MoeSeg s;
 
@@ -293,19 +312,22 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 const int e = L.busy[s.b];
                 // up: pieces of 16 columns that exist
                 const int pieces = DOWN ? 0 : min(4, (a.I - s.c * 64) / 16);
-                for (int kb = s.k0; kb < s.k1; ++kb) {
+                for (int ks = s.k0; ks < s.k1; ++ks) {
                     ok = wait_moe(&ctl->empty[st], ph, ctl, a);
                     if (!ok) break;
-                    uint8_t *da = smem + st * stage_bytes;
-                    if constexpr (DOWN) {
-                        mbar_arrive_expect_tx(&ctl->full[st], C::A_BYTES);
-                        tma_load_2d(&a.tmW, &ctl->full[st], da, kb * 128, e * a.H + s.c * 128);
-                    } else {
-                        mbar_arrive_expect_tx(&ctl->full[st], pieces * 4096);
-                        for (int q = 0; q < pieces; ++q) {
-                            const int row = e * 2 * a.I + s.c * 64 + q * 16;
-                            tma_load_2d(&a.tmW, &ctl->full[st], da + q * 4096, kb * 128, row);
-                            tma_load_2d(&a.tmW, &ctl->full[st], da + q * 4096 + 2048, kb * 128, row + a.I);
+                    const int blocks = min(2, KB - 2 * ks);
+                    mbar_arrive_expect_tx(&ctl->full[st], blocks * (DOWN ? C::A_BYTES : pieces * 4096));
+                    for (int h = 0; h < blocks; ++h) {
+                        uint8_t *da = smem + st * stage_bytes + h * C::A_BYTES;
+                        const int k = (2 * ks + h) * 128;
+                        if constexpr (DOWN) {
+                            tma_load_2d(&a.tmW, &ctl->full[st], da, k, e * a.H + s.c * 128);
+                        } else {
+                            for (int q = 0; q < pieces; ++q) {
+                                const int row = e * 2 * a.I + s.c * 64 + q * 16;
+                                tma_load_2d(&a.tmW, &ctl->full[st], da + q * 4096, k, row);
+                                tma_load_2d(&a.tmW, &ctl->full[st], da + q * 4096 + 2048, k, row + a.I);
+                            }
                         }
                     }
                     ++it;
@@ -334,9 +356,10 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
             while (ok && walk.next(s)) {
                 const int e = L.busy[s.b], ng = (L.start[e + 1] - L.start[e] + 7) / 8;
                 const uint32_t idesc = idesc_mxf8f6f4(128, (8 * ng + 15) / 16 * 16, 0, 0);
-                for (int kb = s.k0; kb < s.k1; ++kb) {
-                    const uint64_t ad = sdesc_k_sw128(smem_u32(smem + st * stage_bytes));
-                    const uint64_t bd = sdesc_k_sw128(smem_u32(smem + st * stage_bytes + C::A_BYTES));
+                for (int ks = s.k0; ks < s.k1; ++ks) {
+                    const uint32_t at = smem_u32(smem + st * stage_bytes);
+                    const uint64_t ad = sdesc_k_sw128(at), bd = sdesc_k_sw128(at + 2 * C::A_BYTES);
+                    const int blocks = min(2, KB - 2 * ks);
                     ok = (ready || wait_moe(&ctl->full[st], ph, ctl, a)) && wait_moe(&ctl->tempty[b], bph, ctl, a);
                     if (!ok) break;
                     tc_fence_after();
@@ -345,15 +368,18 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                         st = 0;
                         ph ^= 1u;
                     }
+                    for (int h = 0; h < blocks; ++h) {
+                        const uint64_t ah = ad + h * (C::A_BYTES / 16), bh = bd + h * (code_bytes / 16);
+                        const uint32_t d = tmem + b * C::STRIDE + h * 8 * NG;
 #pragma unroll
-                    for (int p = 0; p < C::PIECES; ++p)
+                        for (int p = 0; p < C::PIECES; ++p)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // the next stage is looked for while the pipe is busy
-                            if (p == C::PIECES - 1 && i == 3) ready = mbar_test_wait(&ctl->full[st], ph);
-                            mma_mxf8(tmem + b * C::STRIDE, ad + 2 * i, bd + p * ng * 64 + 2 * i, idesc, tmem + C::SF,
-                                     tmem + C::SF + 4 * p, (p | i) != 0);
-                        }
+                            for (int i = 0; i < 4; ++i)
+                                mma_mxf8(d, ah + 2 * i, bh + p * ng * 64 + 2 * i, idesc, tmem + C::SF, tmem + C::SF + 4 * p,
+                                         (p | i) != 0);
+                        // the next stage is looked for while the pipe is busy
+                        if (h == 0) ready = mbar_test_wait(&ctl->full[st], ph);
+                    }
                     mma_commit(&ctl->tfull[b]);
                     mma_commit(empty);
                     mbar_arrive(&ctl->tfull[b]);   // the makers' scales are before this
@@ -371,22 +397,22 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
         }
     } else if (warp < 4 || warp >= 8) {
         if constexpr (DOWN) wait_for_previous();
-        // stage it is this warp's where it mod makers is its number; lane l makes the codes of the
+        // block `it` (two in a stage) is this warp's where it mod makers is its number; lane l makes the codes of the
         // values 4 l .. 4 l + 3 of each token, eight tokens at a time, the next ones in flight
         const int maker = warp < 4 ? warp - 2 : warp - 6;
         if (maker < makers) {
-            int it = maker, st = maker;
+            int it = maker, st = maker / 2, kb = 0, k1 = 0, first = 0, n = 0;   // K blocks [kb, k1) of the segment are ahead
             uint32_t ph = 1;
-            int kb = 0, first = 0, n = 0;
             uint2 v[8];
             float hs[8];
-            // `skip` K blocks on, into the segments that follow
+            // `skip` blocks on, into the segments that follow
             auto advance = [&](int skip) {
                 kb += skip;
-                while (kb >= s.k1) {
-                    const int over = kb - s.k1;
+                while (kb >= k1) {
+                    const int over = kb - k1;
                     if (!walk.next(s)) return false;
-                    kb = s.k0 + over;
+                    kb = 2 * s.k0 + over;
+                    k1 = 2 * s.k1;
                 }
                 const int e = L.busy[s.b];
                 first = L.start[e];
@@ -411,12 +437,11 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                     }
                 }
             };
-            s.k0 = s.k1 = 0;
             bool more = advance(maker);
             if (more) load(0);
             while (more) {
                 if (!__all_sync(0xFFFFFFFFu, wait_moe(&ctl->empty[st], ph, ctl, a))) break;
-                uint8_t *db = smem + st * stage_bytes + C::A_BYTES;
+                uint8_t *db = smem + st * stage_bytes + 2 * C::A_BYTES + (it & 1) * code_bytes;
                 float *sx = ctl->sx[it % MT_SX_RING];
                 const int rows = n, ng = (n + 7) / 8;
                 for (int g = 0; g < ng; ++g) {
@@ -463,8 +488,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 fence_proxy_async_smem();   // the codes become visible to the MMA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->full[st]);
+                st += ((it & 1) + makers) >> 1;
                 it += makers;
-                st += makers;
                 if (st >= stages) {
                     st -= stages;
                     ph ^= 1u;
@@ -485,7 +510,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
             auto begin = [&](const MoeSeg &v) {   // a segment's first scales
                 const int col = min(v.c * 64 + q * 16 + (lane & 15), a.I - 1);
                 sw = a.s1 + (static_cast<int64_t>(L.busy[v.b]) * NB + ((lane < 16 ? 0 : a.I) + col) / 128) * KB;
-                scales = row_scales(sw, v, v.k0);
+                scales = row_scales(sw, KB, v.k0);
             };
             bool more = walk.next(s);
             if (more) begin(s);
@@ -493,7 +518,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 const int e = L.busy[s.b], first = L.start[e], n = L.start[e + 1] - first, ng = (n + 7) / 8;
                 const int col = s.c * 64 + q * 16 + (lane & 15);   // lanes 0-15 hold its gate, 16-31 its up
                 float acc[8 * NG];
-                ok = sum_blocks<DOWN, NG>(a, ctl, acc, s, sw, scales, ng, taddr, it, b, bph);
+                ok = sum_blocks<DOWN, NG>(a, ctl, acc, s, sw, scales, KB, ng, taddr, it, b, bph);
                 if (!ok) break;
                 more = walk.next(s);
                 if (more) begin(s);   // on their way while this tile is finished
@@ -523,7 +548,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 }
             }
         } else {
-            const int64_t per = static_cast<int64_t>(busy) * KB, all = walk.all, G = walk.ctas;
+            const int64_t per = static_cast<int64_t>(busy) * KS, all = walk.all, G = walk.ctas;
             const int NB = (a.H + 127) / 128;
             if (busy == 0)   // no token has an expert
                 for (int c = blockIdx.x; c < tiles; c += gridDim.x)
@@ -535,7 +560,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
             float scales = 0.0f;
             auto begin = [&](const MoeSeg &v) {
                 sw = a.s2 + (static_cast<int64_t>(L.busy[v.b]) * NB + v.c) * KB;
-                scales = row_scales(sw, v, v.k0);
+                scales = row_scales(sw, KB, v.k0);
             };
             bool more = walk.next(ahead);
             if (more) begin(ahead);
@@ -548,7 +573,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 if (more) begin(ahead);
                 if (ok) {
                     float acc[8 * NG];
-                    ok = sum_blocks<DOWN, NG>(a, ctl, acc, s, now, now_scales, ng, taddr, it, b, bph);
+                    ok = sum_blocks<DOWN, NG>(a, ctl, acc, s, now, now_scales, KB, ng, taddr, it, b, bph);
                     if (ok) {
 #pragma unroll
                         for (int m = 0; m < 8 * NG; ++m)
@@ -562,7 +587,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 // the tile's end, or this CTA's.  A warp whose waits ran out comes here, too, so
                 // that the others do not wait for it
                 if (!named_bar_and(1, 128, ok)) break;
-                const int64_t t0 = s.c * per, t1 = t0 + per;   // the tile's K blocks in the line
+                const int64_t t0 = s.c * per, t1 = t0 + per;   // the tile's stages in the line
                 const bool part = t0 < whole.pos || t1 > whole.end;
                 // part: slot 1 of the CTA in which the tile starts, slot 0 of the others
                 const int a0 = static_cast<int>(((t0 + 1) * G - 1) / all), a1 = static_cast<int>((t1 * G - 1) / all);
