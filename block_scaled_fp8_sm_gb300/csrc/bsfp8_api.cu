@@ -178,6 +178,22 @@ int encode_kmajor_halves_raw(CUtensorMap *m, const void *base, int64_t rows, int
     return r == CUDA_SUCCESS ? FP8_OK : FP8_ERR_CUDA;
 }
 
+// The gate and up rows of all experts, [E, 2 I, K] bytes, seen as {K, 16 rows, gate or up, groups
+// of 16 rows}: a box {128, 16, 2, 8} brings 16 gate rows, the 16 up rows of the same columns, the
+// next 16 gate rows and so on.  The groups end with the last expert's gate rows, so that no up row past
+// the end is in the view.
+int encode_gate_up_raw(CUtensorMap *m, const void *base, int64_t E, int64_t I, int64_t K) {
+    const cuuint64_t k = static_cast<cuuint64_t>(K);
+    const cuuint64_t dims[4] = {k, 16u, 2u, static_cast<cuuint64_t>((2 * E - 1) * (I / 16))};
+    const cuuint64_t strides[3] = {k, static_cast<cuuint64_t>(I) * k, 16u * k};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(BK), 16u, 2u, 8u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FP8_OK : FP8_ERR_CUDA;
+}
+
 // bf16 output C (M x N, row-major) for the epilogue's TMA stores: box of
 // STG_COLS columns x BM rows, no swizzle; rows past M are clipped by the TMA.
 int encode_out_raw(CUtensorMap *m, void *C, int64_t M, int64_t N) {
@@ -208,7 +224,7 @@ int encode_outq_raw(CUtensorMap *m, void *Cq, int64_t M, int64_t N) {
 // those arguments stays valid whatever later happens to the memory behind it.
 // The cache saves the host ~2 us per map (a grouped call encodes one per group).
 struct MapKey {
-    int kind;   // 0: 2D K-major, 1: 3D K-major halves, 2: bf16 output, 3: E4M3 output
+    int kind;   // 0: 2D K-major, 1: 3D K-major halves, 2: bf16 output, 3: E4M3 output, 4: gate and up rows
     int box;
     const void *base;
     int64_t a, b;
@@ -252,6 +268,12 @@ int cached_map(CUtensorMap *m, const MapKey &k, Encode encode) {
 int encode_kmajor(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows) {
     return cached_map(m, MapKey{0, box_rows, base, rows, K},
                       [&](CUtensorMap *o) { return encode_kmajor_raw(o, base, rows, K, box_rows); });
+}
+
+int encode_gate_up(CUtensorMap *m, const void *base, int64_t E, int64_t I, int64_t K) {
+    // E * 2 I rows and I name the same memory for one pair (E, I) only
+    return cached_map(m, MapKey{4, static_cast<int>(I), base, E * 2 * I, K},
+                      [&](CUtensorMap *o) { return encode_gate_up_raw(o, base, E, I, K); });
 }
 
 namespace {

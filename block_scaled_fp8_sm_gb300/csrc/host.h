@@ -34,6 +34,10 @@ int zero_fill(void *C, int64_t elems, cudaStream_t stream);
 // bytes x box_rows rows, 128-byte swizzle; K and rows past the end read as 0.
 int encode_kmajor(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows);
 
+// Cached tensor map of experts' gate and up rows [E, 2 I, K] for boxes of 128 columns: 16 gate
+// rows and 16 up rows in turn, 128 K bytes, 128-byte swizzle; past the ends reads as 0.
+int encode_gate_up(CUtensorMap *m, const void *base, int64_t E, int64_t I, int64_t K);
+
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Kernel attributes and other one-time work of the 128-granular entry points

@@ -50,12 +50,12 @@ bool set_tile_shared() {
 // Both kernels of the layer for up to 8 NG tokens.
 template <int NG>
 int launch_tiles(MoeTileArgs &a, cudaStream_t stream) {
-    int rc = encode_kmajor(&a.tmW, a.W1, static_cast<int64_t>(a.E) * 2 * a.I, a.H, 16);
+    int rc = encode_gate_up(&a.tmW, a.W1, a.E, a.I, a.H);
     if (rc != FP8_OK) return rc;
     a.ring = (MT_SMEM - smem_moe_fixed<false, NG>(a.T, a.top, a.E)) / 1024 * 1024;
     rc = launch(bsfp8_moe_tile<false, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
     if (rc != FP8_OK) return rc;
-    rc = encode_kmajor(&a.tmW, a.W2, static_cast<int64_t>(a.E) * a.H, a.I, 128);
+    rc = encode_kmajor(&a.tmW, a.W2, static_cast<int64_t>(a.E) * a.H, a.I, MT_ROWS);
     if (rc != FP8_OK) return rc;
     a.ring = (MT_SMEM - smem_moe_fixed<true, NG>(a.T, a.top, a.E)) / 1024 * 1024;
     return launch(bsfp8_moe_tile<true, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
@@ -159,7 +159,7 @@ int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E
 int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I) {
     if (!layer_sizes(T, top, I)) return 0;
     const int64_t h = T * top * (2 * I + I / 4);
-    return T <= MOE_FEW_TOKENS ? h : (h + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * 128 * 4 + MT_CTAS * 4;
+    return T <= MOE_FEW_TOKENS ? h : (h + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + MT_CTAS * 4;
 }
 
 int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
@@ -202,7 +202,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
     if (T > MOE_FEW_TOKENS) {
         uint8_t *rest = static_cast<uint8_t *>(workspace) + (T * top * (2 * I + I / 4) + 255) / 256 * 256;
         a.part = reinterpret_cast<float *>(rest);
-        a.counters = reinterpret_cast<int *>(rest + int64_t(2) * MT_CTAS * T * 128 * 4);
+        a.counters = reinterpret_cast<int *>(rest + int64_t(2) * MT_CTAS * T * MT_ROWS * 4);
         a.status = d->status;
         a.wait_limit = wait_limit();
         return guarded([&] {

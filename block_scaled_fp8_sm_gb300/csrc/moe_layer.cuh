@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(MOE_THREADS, NT == 1 ? 2 : 1) bsfp8_moe_up(con
     launch_dependents();
 }
 
-// The experts' tokens, in shared memory.  An expert's entries stand from start[e] to
-// start[e + 1], one for each of its tokens.
+// The experts' tokens, in shared memory: one entry for each token of an expert, from start[e]
+// to start[e + 1].
 struct MoeLists {
     int *start;          // [E + 1]
-    int *experts;        // how many are busy, the most tokens of one, and
+    int *experts;        // how many are busy, and the most tokens of one
     uint16_t *busy;      // [E] which, ascending
     uint16_t *pair;      // [pairs] the row of h: the token's first pair with the expert
     uint16_t *token;     // [pairs]
