@@ -108,42 +108,49 @@ struct MoeSeg {
 // The segments of this CTA in order; every role walks them alike.
 template <bool DOWN>
 struct MoeWalk {
-    int64_t pos, end, all;   // down: the K blocks of all tiles,
-    int ctas;                // and the CTAs that have some
-    int busy, KB, tiles;
+    int64_t begin, end, all;   // up: tiles from here in steps of the grid; down: K blocks of the line
+    int64_t left;              // down: K blocks not walked yet
+    int ctas;                  // down: the CTAs that have some
+    int busy, KB, tiles, b, c, k;
 
     __device__ __forceinline__ MoeWalk(int busy_, int KB_, int tiles_) : busy(busy_), KB(KB_), tiles(tiles_) {
-        if constexpr (DOWN) {
-            all = static_cast<int64_t>(tiles) * busy * KB;
-            ctas = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
-            const bool in = static_cast<int>(blockIdx.x) < ctas;
-            pos = in ? all * blockIdx.x / ctas : 0;
-            end = in ? all * (blockIdx.x + 1) / ctas : 0;
-        } else {
-            pos = blockIdx.x;
-            end = static_cast<int64_t>(tiles) * busy;
+        all = static_cast<int64_t>(tiles) * busy * (DOWN ? KB : 1);
+        ctas = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
+        const bool in = static_cast<int>(blockIdx.x) < ctas;
+        begin = !in ? all : DOWN ? all * blockIdx.x / ctas : blockIdx.x;
+        end = in && DOWN ? all * (blockIdx.x + 1) / ctas : all;
+        left = DOWN ? end - begin : begin < all;
+        b = c = k = 0;
+        if (left > 0) {
+            const int64_t tile = DOWN ? begin / KB : begin;   // tiles of experts: down expert by expert, up column by column
+            k = DOWN ? static_cast<int>(begin - tile * KB) : 0;
+            b = static_cast<int>(DOWN ? tile % busy : tile / tiles);
+            c = static_cast<int>(DOWN ? tile / busy : tile % tiles);
         }
     }
     __device__ __forceinline__ bool next(MoeSeg &s) {
-        if (pos >= end) return false;
+        if (left <= 0) return false;
+        s.b = b;
+        s.c = c;
+        s.k0 = k;
         if constexpr (DOWN) {
-            const int64_t per = static_cast<int64_t>(busy) * KB;
-            const int64_t c = pos / per;
-            const int in = static_cast<int>(pos - c * per);
-            s.c = static_cast<int>(c);
-            s.b = in / KB;
-            s.k0 = in - s.b * KB;
-            s.k1 = static_cast<int>(min(static_cast<int64_t>(KB), s.k0 + (end - pos)));
-            s.end = s.b + 1 == busy && s.k1 == KB;
-            pos += s.k1 - s.k0;
+            s.k1 = static_cast<int>(min(static_cast<int64_t>(KB), k + left));
+            s.end = b + 1 == busy && s.k1 == KB;
+            left -= s.k1 - k;
+            k = 0;
+            if (++b == busy) {
+                b = 0;
+                ++c;
+            }
         } else {
-            const int i = static_cast<int>(pos);
-            s.b = i / tiles;
-            s.c = i - s.b * tiles;
-            s.k0 = 0;
             s.k1 = KB;
             s.end = true;
-            pos += gridDim.x;
+            c += gridDim.x;
+            while (c >= tiles) {
+                c -= tiles;
+                ++b;
+            }
+            left = b < busy;
         }
         return true;
     }
@@ -559,13 +566,21 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 if (ok) {
                     float acc[8 * NG];
                     ok = sum_blocks<DOWN, NG>(a, ctl, acc, s, now, now_scales, KB, ng, taddr, step, bufs, it, b, bph);
-                    if (ok) {
+                    if (ok) {   // four tokens at a time: they are different ones
 #pragma unroll
-                        for (int m = 0; m < 8 * NG; ++m)
-                            if (m < n) {
-                                float *to = &ctl->sums[L.token[first + m]][row];
-                                *to = fmaf(L.weight[first + m], acc[m], *to);
+                        for (int m = 0; m < 8 * NG; m += 4) {
+                            if (m >= n) break;
+                            float *to[4], v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int at = first + min(m + i, n - 1);
+                                to[i] = &ctl->sums[L.token[at]][row];
+                                v[i] = fmaf(L.weight[at], acc[m + i], *to[i]);
                             }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (m + i < n) *to[i] = v[i];
+                        }
                     }
                 }
                 if (!s.end && more) continue;
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 // that the others do not wait for it
                 if (!named_bar_and(1, 256, ok)) break;
                 const int64_t t0 = s.c * per, t1 = t0 + per;   // the tile's K blocks in the line
-                const bool part = t0 < whole.pos || t1 > whole.end;
+                const bool part = t0 < whole.begin || t1 > whole.end;
                 // part: slot 1 of the CTA in which the tile starts, slot 0 of the others
                 const int a0 = static_cast<int>(((t0 + 1) * G - 1) / all), a1 = static_cast<int>((t1 * G - 1) / all);
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == a0 ? 1 : 0);
@@ -599,20 +614,26 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 named_bar_sync(1, 256);
                 if (!last) continue;
                 __threadfence();
-                for (int t = warp - 4; t < a.T; t += 2 * MT_EPI_WARPS) {   // two tokens at a time
+                // two tokens and four parts at a time are on their way
+                for (int t = warp - 4; t < a.T; t += 2 * MT_EPI_WARPS) {
                     float4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int i = a0; i <= a1; ++i) {
-                        const float4 *from = parts + (static_cast<int64_t>(i) * 2 + (i == a0 ? 1 : 0)) * a.T * LD;
+                    const int u1 = min(t + MT_EPI_WARPS, a.T - 1);
+                    for (int i = a0; i <= a1; i += 4) {
+                        float4 w[4][4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int u = t + (k >> 1) * MT_EPI_WARPS;
-                            if (u < a.T) {
-                                const float4 w = __ldcg(from + u * LD + 32 * (k & 1));
-                                v[k].x += w.x, v[k].y += w.y, v[k].z += w.z, v[k].w += w.w;
-                            }
+                        for (int x = 0; x < 4; ++x) {
+                            const int from = min(i + x, a1);
+                            const float4 *at = parts + (static_cast<int64_t>(from) * 2 + (from == a0 ? 1 : 0)) * a.T * LD;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[x][k] = __ldcg(at + (k >> 1 ? u1 : t) * LD + 32 * (k & 1));
                         }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (i + x <= a1)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) v[k].x += w[x][k].x, v[k].y += w[x][k].y, v[k].z += w[x][k].z, v[k].w += w[x][k].w;
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
