@@ -30,7 +30,7 @@ int set_attrs() {
         set_tile_attrs<128, true, FUSED>() != FP8_OK)
         return FP8_ERR_CUDA;
     return cudaFuncSetAttribute(bsfp8_block128_native<FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_n128<FUSED>()) == cudaSuccess
+                                smem_n128()) == cudaSuccess
                ? FP8_OK
                : FP8_ERR_CUDA;
 }
@@ -136,7 +136,7 @@ int launch_native(const RowsArgs &r, int64_t tiles, DeviceState *d, cudaStream_t
     const int rc = tile_args(a, r, N128_BN, d);
     if (rc != FP8_OK) return rc;
     const unsigned grid = static_cast<unsigned>(tiles < d->sm_count ? tiles : d->sm_count);
-    return launch(bsfp8_block128_native<FUSED>, dim3(grid), T128_THREADS, smem_n128<FUSED>(), 1, a, stream);
+    return launch(bsfp8_block128_native<FUSED>, dim3(grid), T128_THREADS, smem_n128(), 1, a, stream);
 }
 
 // CTAs that share a tile's K: as many as the GPU still has room for, four K blocks

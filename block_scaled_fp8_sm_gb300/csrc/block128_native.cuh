@@ -31,16 +31,14 @@ constexpr int N128_SF_A = 512, N128_SF_B = 128;                // bytes of lines
 constexpr int N128_SF_ENTRY = N128_SF_A + 2 * N128_SF_B;
 constexpr int N128_SF_COL0 = 256, N128_SF_COLS = 12;            // tensor memory: A 4 columns, B 4 per block
 
-template <bool FUSED>
-struct CtrlN128 : Control128<N128_BN, FUSED> {
+struct CtrlN128 : Ctrl128<N128_BN> {
     uint64_t sfull[N128_SF_RING], sempty[N128_SF_RING];
 };
 
-template <bool FUSED>
 constexpr int smem_n128() {
     using C = Cfg128<N128_BN>;
     return 1024 + C::STAGES * (C::A_BYTES + C::B_BYTES) + C::STG + N128_SF_RING * N128_SF_ENTRY +
-           static_cast<int>(sizeof(CtrlN128<FUSED>));
+           static_cast<int>(sizeof(CtrlN128));
 }
 
 __device__ __forceinline__ bool is_pow2(float v) {
@@ -56,8 +54,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
     uint8_t *sm_a = smem, *sm_b = smem + C::STAGES * C::A_BYTES;
     uint8_t *stg = sm_b + C::STAGES * C::B_BYTES;
     uint8_t *sf = stg + C::STG;
-    using Ctl = CtrlN128<FUSED>;
-    Ctl *ctl = reinterpret_cast<Ctl *>(sf + N128_SF_RING * N128_SF_ENTRY);
+    CtrlN128 *ctl = reinterpret_cast<CtrlN128 *>(sf + N128_SF_RING * N128_SF_ENTRY);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -250,11 +247,17 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->tempty[0]);
 #pragma unroll
-                for (int x = 0; x < C::COLS / 16; ++x) {
-                    float v[16];
+                for (int x = 0; x < C::COLS / 32; ++x) {
+                    const int col = tt.n0 + h * C::COLS + 32 * x;
+                    float v[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(p[x][j]);
-                    store_fused<16>(mine, a, tt, q, tt.n0 + h * C::COLS + 16 * x, v);
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(p[2 * x + (j >> 4)][j & 15]);
+                    fuse_rows32(a, lane_bias(a, col), v);
+                    add_residual(a, tt, q, col, v);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+                    store_rows32(mine, a, tt, q, col, w);
                 }
             } else {
                 uint32_t w[C::COLS / 32][16];

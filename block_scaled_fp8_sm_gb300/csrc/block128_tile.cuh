@@ -92,14 +92,16 @@ struct Ctrl128 {
     int2 rows[EXPERTS + 1];   // and its rows
 };
 
-// FUSED kernels are for one product: no expert table, and twice the staging (fp32).
+// FUSED kernels are for one product: no expert table, and the residual's pieces of 32 rows x 32
+// columns (2 KB for each epilogue warp) beside the staging.
 template <int BN, bool FUSED>
 using Control128 = Ctrl128<BN, FUSED ? 0 : T128_MAX_EXPERTS>;
+constexpr int T128_RESIDUAL = T128_EPI_WARPS * 32 * 64;
 
 template <int BN, bool FUSED>
 constexpr int smem128() {
-    return 1024 + Cfg128<BN>::STAGES * (Cfg128<BN>::A_BYTES + Cfg128<BN>::B_BYTES) +
-           Cfg128<BN>::STG * (FUSED ? 2 : 1) + static_cast<int>(sizeof(Control128<BN, FUSED>));
+    return 1024 + Cfg128<BN>::STAGES * (Cfg128<BN>::A_BYTES + Cfg128<BN>::B_BYTES) + Cfg128<BN>::STG +
+           (FUSED ? T128_RESIDUAL : 0) + static_cast<int>(sizeof(Control128<BN, FUSED>));
 }
 
 // Bounded wait: polls, and looks at the clock and the abort flag every 16 polls.
@@ -252,46 +254,83 @@ __device__ __forceinline__ void store_rows32(uint8_t *mine, const Tile128Args &a
     __syncwarp();
 }
 
-// P columns (32 or 16) of fp32 sums of each lane's row to C through P * 128 bytes of
-// staging, with bias, activation and residual: there a lane holds eight consecutive columns
-// of a row, so that the residual comes and C goes in whole sectors, and the activation's
-// code is there once for a piece and not once for each of a lane's 128 sums.
-template <int P>
-__device__ __forceinline__ void store_fused(uint8_t *mine, const Tile128Args &a, const Tile128 &tt, int q, int col,
-                                            const float *v) {
-    constexpr int CH = P / 4;            // 16-byte pieces of a staged row
-    constexpr int LR = P / 8;            // lanes of a row
-    constexpr int SH = P == 32 ? 0 : 1;  // rows in 128 bytes: 1 or 2
-    const int lane = threadIdx.x & 31;
-    const int c8 = lane & (LR - 1), n = col + 8 * c8;
-    uint4 r[LR];
-    int64_t at[LR];
-#pragma unroll
-    for (int i = 0; i < LR; ++i) {
-        const int m = tt.m0 + q * 32 + i * (32 / LR) + lane / LR;
-        at[i] = m < tt.hi && n < a.N ? static_cast<int64_t>(m) * a.N + n : -1;
-        r[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.ep.R && at[i] >= 0) r[i] = *reinterpret_cast<const uint4 *>(a.ep.R + at[i]);
+// The lane, read where it is used: what depends on it is then computed there and not kept in
+// registers over the K loop, which has none to spare.
+__device__ __forceinline__ int lane_here() {
+    int lane;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+    return lane;
+}
+
+// The residual of a tile comes to L2 (the producer, a tile ahead of its epilogue), and a piece
+// of it (32 rows, 32 columns) to shared memory while the epilogue does something else.
+__device__ __forceinline__ void prefetch_residual(const Tile128Args &a, const Tile128 &tt, int cols) {
+    if (!a.ep.R) return;
+    const int bytes = min(cols, a.N - tt.n0) * 2, rows = min(T128_BM, tt.hi - tt.m0);
+    for (int r = 0; r < rows; ++r)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.ep.R + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0),
+                     "r"(bytes)
+                     : "memory");
+}
+
+__device__ __forceinline__ void fetch_residual(uint8_t *res, const Tile128Args &a, const Tile128 &tt, int q, int col) {
+    if (!a.ep.R) return;
+    const int lane = lane_here();
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2), c = lane & 3, mm = tt.m0 + q * 32 + rr, n = col + 8 * c;
+        if (mm < tt.hi && n < a.N)
+            cp_async_16(smem_u32(res + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)), a.ep.R + static_cast<int64_t>(mm) * a.N + n, 16);
     }
-    float4 *row = reinterpret_cast<float4 *>(mine + lane * (P * 4));
+}
+
+// Bias and activation of 32 columns of each lane's row, in place; bias: the lane's column's.
+// What is written here, and below, so that the K loop keeps its registers (with any of these it
+// took 16 to 26 % longer, moving or spilling its sums): the residual's row 16 bytes at a time,
+// its fetch after the K loop, and arithmetic in place, the sums not exchanged in fp32.
+__device__ __forceinline__ void fuse_rows32(const Tile128Args &a, float bias, float (&v)[32]) {
+    if (a.ep.bias) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-        row[c ^ ((lane >> SH) & (CH - 1))] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        for (int c = 0; c < 32; ++c) v[c] += __shfl_sync(0xFFFFFFFFu, bias, c);
+    }
+    activate(v, a.ep.act);
+}
+
+// The bias of column col + lane.
+__device__ __forceinline__ float lane_bias(const Tile128Args &a, int col) {
+    const int n = col + lane_here();
+    if (!a.ep.bias || n >= a.N) return 0.0f;
+    return a.ep.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.ep.bias)[n])
+                          : static_cast<const float *>(a.ep.bias)[n];
+}
+
+__device__ __forceinline__ void add8(float *v, const uint4 r) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] += bf16_lo(w[i]);
+        v[2 * i + 1] += bf16_hi(w[i]);
+    }
+}
+
+// The residual of these columns: of a piece that was fetched, or straight from memory.
+__device__ __forceinline__ void add_fetched_residual(const uint8_t *res, const Tile128Args &a, float (&v)[32]) {
+    if (!a.ep.R) return;
+    const int lane = lane_here();
+    cp_async_wait_all();
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < LR; ++i) {
-        const int rr = i * (32 / LR) + lane / LR, x = (rr >> SH) & (CH - 1);
-        const float4 *src = reinterpret_cast<const float4 *>(mine + rr * (P * 4));
-        const float4 lo = src[(2 * c8) ^ x], hi = src[(2 * c8 + 1) ^ x];
-        if (at[i] >= 0) {
-            float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-            finish<8>(a.ep, f, n, w);
-            *reinterpret_cast<uint4 *>(a.C + at[i]) =
-                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
-        }
-    }
+    for (int c = 0; c < 4; ++c) add8(v + 8 * c, *reinterpret_cast<const uint4 *>(res + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)));
     __syncwarp();
+}
+
+__device__ __forceinline__ void add_residual(const Tile128Args &a, const Tile128 &tt, int q, int col, float (&v)[32]) {
+    if (!a.ep.R) return;
+    const int mm = tt.m0 + q * 32 + lane_here();
+    const uint4 *from = reinterpret_cast<const uint4 *>(a.ep.R + static_cast<int64_t>(mm) * a.N + col);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (mm < tt.hi && col + 8 * c < a.N) add8(v + 8 * c, from[c]);
 }
 
 // First tile of each expert (a running sum over one warp), or the tile count of one
@@ -359,7 +398,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
     uint8_t *sm_a = smem, *sm_b = smem + C::STAGES * C::A_BYTES;
     uint8_t *stg = sm_b + C::STAGES * C::B_BYTES;
     using Ctl = Control128<BN, FUSED>;
-    Ctl *ctl = reinterpret_cast<Ctl *>(stg + C::STG * (FUSED ? 2 : 1));
+    Ctl *ctl = reinterpret_cast<Ctl *>(stg + C::STG + (FUSED ? T128_RESIDUAL : 0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank = 0, ranks = 1;
     if constexpr (SPLIT) {
@@ -410,6 +449,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 bool ok = true;
                 for (int t = unit; t < tiles && ok; t += units) {
                     const Tile128 tt = tile128<BN>(a, ctl, t);
+                    if constexpr (FUSED && !SPLIT) prefetch_residual(a, tt, BN);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         ok = wait128(&ctl->empty[s], ph, ctl, a);
                         if (!ok) break;
@@ -473,7 +513,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int r = q * 32 + lane;   // row of the tile
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::COLS;
-        uint8_t *mine = stg + (warp - 4) * (32 * 64) * (FUSED ? 2 : 1);
+        uint8_t *mine = stg + (warp - 4) * (32 * 64);
+        uint8_t *res = mine + C::STG;   // FUSED
         int b = 0;
         uint32_t bph = 0;
         bool ok = true;
@@ -524,8 +565,6 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             }
             if (!ok) break;
             const Tile128 cur = tt;
-            // the next tile's first scales are on their way while this one is stored
-            if (t + units < tiles) begin(t + units);
             if constexpr (SPLIT) {
                 // the partial sums go to the operand ring's memory (nothing is in
                 // flight there any more: the last partial came after the last load),
@@ -536,19 +575,24 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 for (int j = 0; j < C::COLS / 4; ++j)
                     red[r * (BN / 4) + ((h * (C::COLS / 4) + j) ^ (r & 7))] =
                         make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-            } else if constexpr (FUSED) {
-#pragma unroll
-                for (int x = 0; x < C::COLS / 32; ++x)
-                    store_fused<32>(mine, a, cur, q, cur.n0 + h * C::COLS + 32 * x, acc + 32 * x);
             } else {
+                if constexpr (FUSED) fetch_residual(res, a, cur, q, cur.n0 + h * C::COLS);
 #pragma unroll
                 for (int x = 0; x < C::COLS / 32; ++x) {
+                    const int col = cur.n0 + h * C::COLS + 32 * x;
+                    if constexpr (FUSED) {
+                        float(&v)[32] = *reinterpret_cast<float (*)[32]>(acc + 32 * x);
+                        fuse_rows32(a, lane_bias(a, col), v);
+                        add_fetched_residual(res, a, v);
+                        if (x + 1 < C::COLS / 32) fetch_residual(res, a, cur, q, col + 32);
+                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = bf16_pair(acc[32 * x + 2 * j], acc[32 * x + 2 * j + 1]);
-                    store_rows32(mine, a, cur, q, cur.n0 + h * C::COLS + 32 * x, w);
+                    store_rows32(mine, a, cur, q, col, w);
                 }
             }
+            if (t + units < tiles) begin(t + units);
         }
     }
 
@@ -581,13 +625,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 const int n = tt.n0 + 4 * c;
                 if constexpr (FUSED) {
                     if (n < a.N) {
-                        uint32_t w[2] = {0u, 0u};
-                        if (a.ep.R) {
-                            const uint2 u = *reinterpret_cast<const uint2 *>(a.ep.R + static_cast<int64_t>(tt.m0 + r) * a.N + n);
-                            w[0] = u.x, w[1] = u.y;
-                        }
                         float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-                        finish<4>(a.ep, f, n, w);
+                        finish4(a.ep, f, n, static_cast<int64_t>(tt.m0 + r) * a.N);
                         v[0] = make_float4(f[0], f[1], f[2], f[3]);
                     }
                 }

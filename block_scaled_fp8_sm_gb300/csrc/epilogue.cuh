@@ -6,16 +6,18 @@
 // The activations are evaluated in fp32 on ex2.approx and rcp.approx (2 ulp each) and are
 // off by less than 2^-14 relative wherever the result is a normal bf16 number, a thirtieth
 // of the half step of the rounding that follows:
-//   silu(y)      = y s(y log2(e)), gelu_tanh(y) = y s(2 log2(e) sqrt(2/pi) (y + 0.044715 y^3)),
-//     s(t) = 1 / (1 + 2^-t), from 2^-|t| only, so that nothing overflows and the tail of
-//     negative y keeps its relative precision;
-//   gelu(y)      = y Phi(y), Phi the normal distribution's integral: Phi(-z) = 2^q(z) with
-//     q a polynomial of degree 9, the minimax fit of log2 Phi(-z) on [0, 14.3] (beyond it
-//     Phi(-z) is below the smallest fp32 number): at most 4.2e-5 relative up to z = 6 and
-//     8.8e-5 after; Phi(z) = 1 - Phi(-z).
+//   silu(y) = y s(y), gelu_tanh(y) = y s(2 sqrt(2/pi) (y + 0.044715 y^3)), s the logistic
+//     function, from the exponential of the negative side only, so that nothing overflows and the
+//     tail of negative y keeps its relative precision;
+//   gelu(y) = y Phi(y), Phi the normal distribution's integral: Phi(-z) = 2^q(z) with q a
+//     polynomial of degree 9, the minimax fit of log2 Phi(-z) on [0, 14.3] (beyond it Phi(-z)
+//     is below the smallest fp32 number): at most 4.2e-5 relative up to z = 6 and 8.8e-5
+//     after; Phi(z) = 1 - Phi(-z).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
+
+#include "ptx.cuh"
 
 namespace bsfp8 {
 
@@ -28,33 +30,37 @@ struct Epilogue {
     int bias_bf16, act;
 };
 
-__device__ __forceinline__ float ex2(float x) {
+__device__ __forceinline__ float ex2(float x) {   // results below 2^-126 are 0
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-__device__ __forceinline__ float rcp(float x) {
+__device__ __forceinline__ float rcp(float x) {   // 1 <= x <= 4 here
     float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// y / (1 + 2^-t)
-__device__ __forceinline__ float times_sigmoid2(float y, float t) {
-    const float e = ex2(-fabsf(t)), r = rcp(1.0f + e);
-    return y * (t < 0.0f ? e * r : r);
+// y / (1 + 2^-2t), t = y (a + b y^2); silu: a = log2(e) / 2, b = 0; gelu_tanh: a = log2(e)
+// sqrt(2/pi), b = 0.044715 a.  2^-2|t| is the square of n = 2^-|t|, so that the subnormal part of
+// its range is there; y^2 is kept finite (b = 0 times infinity is NaN).  Two at once with one
+// reciprocal, 1 / d0 = d1 / (d0 d1), d in [1, 2]: the special-function unit then has three
+// operations for two values and not four.
+// Written for scalar registers: packed pairs (f32x2) move the sums of the tile kernels' K loop
+// about (19 % longer).
+__device__ __forceinline__ void sigmoid_gate2(float &y0, float &y1, float a, float b) {
+    const float t0 = y0 * fmaf(b, fminf(y0 * y0, 1e30f), a), t1 = y1 * fmaf(b, fminf(y1 * y1, 1e30f), a);
+    const float n0 = ex2(-fabsf(t0)), n1 = ex2(-fabsf(t1));
+    const float d0 = fmaf(n0, n0, 1.0f), d1 = fmaf(n1, n1, 1.0f), r = rcp(d0 * d1);
+    y0 *= (t0 < 0.0f ? n0 * n0 : 1.0f) * (d1 * r);
+    y1 *= (t1 < 0.0f ? n1 * n1 : 1.0f) * (d0 * r);
 }
 
-__device__ __forceinline__ float silu(float y) { return times_sigmoid2(y, y * 1.44269504f); }
-
-__device__ __forceinline__ float gelu_tanh(float y) {
-    constexpr float k = 2.30220819f;   // 2 log2(e) sqrt(2/pi)
-    return times_sigmoid2(y, y * fmaf(k * 0.044715f, y * y, k));
-}
-
+// The polynomial has 32 added, taken back after ex2, so that Phi may be a subnormal number; at
+// z = 15 it is 0, however large y is.
 __device__ __forceinline__ float gelu(float y) {
-    const float z = fminf(fabsf(y), 14.3f);
+    const float z = fminf(fabsf(y), 15.0f);
     float q = -0x1.98ee82p-30f;
     q = fmaf(q, z, 0x1.ee0552p-24f);
     q = fmaf(q, z, -0x1.052edcp-18f);
@@ -64,12 +70,12 @@ __device__ __forceinline__ float gelu(float y) {
     q = fmaf(q, z, -0x1.b4e9e0p-5f);
     q = fmaf(q, z, -0x1.d69808p-2f);
     q = fmaf(q, z, -0x1.268e82p+0f);
-    q = fmaf(q, z, -0x1.0003ccp+0f);
-    const float p = ex2(q) * y;        // NaN stays NaN by y
+    q = fmaf(q, z, 31.0f - 0x1.e6p-15f);
+    const float p = ex2(q) * 0x1p-32f * y;   // NaN stays NaN
     return y < 0.0f ? p : y - p;
 }
 
-// The activation of N values; one branch for all of them.
+// The activation of N values (an even number); one branch for all of them.
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
     if (act == ACT_RELU) {
@@ -78,12 +84,11 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
     } else if (act == ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
-    } else if (act == ACT_GELU_TANH) {
+    } else if (act != ACT_NONE) {
+        const float a = act == ACT_SILU ? 0.5f * 1.44269504f : 0.5f * 2.30220819f;
+        const float b = act == ACT_SILU ? 0.0f : 0.044715f * 0.5f * 2.30220819f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = gelu_tanh(v[i]);
-    } else if (act == ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = silu(v[i]);
+        for (int i = 0; i < N; i += 2) sigmoid_gate2(v[i], v[i + 1], a, b);
     }
 }
 
@@ -95,44 +100,27 @@ __device__ __forceinline__ float finish(const Epilogue &e, float v, int n, int64
     if (e.bias)
         v += e.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(e.bias)[n])
                          : static_cast<const float *>(e.bias)[n];
-    float one[1] = {v};
-    activate(one, e.act);
-    if (e.R) one[0] += __bfloat162float(e.R[at]);
-    return one[0];
+    float two[2] = {v, 0.0f};
+    activate(two, e.act);
+    if (e.R) two[0] += __bfloat162float(e.R[at]);
+    return two[0];
 }
 
-// N (4 or 8) values in a row: columns n .., a multiple of N, with the residual's words r.
-template <int N>
-__device__ __forceinline__ void finish(const Epilogue &e, float (&v)[N], int n, const uint32_t (&r)[N / 2]) {
+// Four values in a row: columns n .., a multiple of 4, of the row whose place in C is `at`.
+__device__ __forceinline__ void finish4(const Epilogue &e, float (&v)[4], int n, int64_t at) {
+    uint2 r = make_uint2(0u, 0u);
+    if (e.R) r = *reinterpret_cast<const uint2 *>(e.R + at + n);
     if (e.bias) {
         if (e.bias_bf16) {
-            const uint32_t *b = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(e.bias) + n);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const uint32_t w = b[i];
-                v[2 * i] += bf16_lo(w);
-                v[2 * i + 1] += bf16_hi(w);
-            }
+            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(e.bias) + n);
+            v[0] += bf16_lo(w.x), v[1] += bf16_hi(w.x), v[2] += bf16_lo(w.y), v[3] += bf16_hi(w.y);
         } else {
-            const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(e.bias) + n);
-#pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const float4 w = b[i];
-                v[4 * i] += w.x;
-                v[4 * i + 1] += w.y;
-                v[4 * i + 2] += w.z;
-                v[4 * i + 3] += w.w;
-            }
+            const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(e.bias) + n);
+            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
         }
     }
     activate(v, e.act);
-    if (e.R) {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            v[2 * i] += bf16_lo(r[i]);
-            v[2 * i + 1] += bf16_hi(r[i]);
-        }
-    }
+    if (e.R) v[0] += bf16_lo(r.x), v[1] += bf16_hi(r.x), v[2] += bf16_lo(r.y), v[3] += bf16_hi(r.y);
 }
 
 }  // namespace bsfp8

@@ -139,7 +139,10 @@ __device__ __forceinline__ bool first_of_token(const MoeArgs &a, int p, int e) {
 // silu(g) * u.  Deep in the negative gates the exponential's two halves go to one factor
 // each, so that a large u brings back what the exponential alone would lose.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    const float t = g * 1.44269504f, n = ex2(-0.5f * fabsf(t)), r = rcp(fmaf(n, n, 1.0f));
+    const float t = g * 1.44269504f;
+    float n;   // 2^(-|t| / 2), subnormal numbers included
+    asm("ex2.approx.f32 %0, %1;" : "=f"(n) : "f"(-0.5f * fabsf(t)));
+    const float r = rcp(fmaf(n, n, 1.0f));
     return t < 0.0f ? (g * n) * (u * n) * r : (g * r) * u;
 }
 

@@ -177,6 +177,9 @@ __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// All of this thread's copies have landed (other threads' need a barrier after it).
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy reads (TMA, tcgen05.mma, tcgen05.cp).
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -369,6 +372,9 @@ __device__ __forceinline__ uint64_t f32x2_pack(uint32_t lo, uint32_t hi) {
 }
 __device__ __forceinline__ void f32x2_unpack(uint64_t v, uint32_t &lo, uint32_t &hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f32x2_of(float lo, float hi) {
+    return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi));
 }
 // acc = a * b + acc on both halves, each an fp32 fma rounded to nearest even
 // (the packed form issues one instruction for two lanes of work).

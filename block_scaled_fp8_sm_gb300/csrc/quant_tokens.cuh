@@ -43,10 +43,6 @@ __device__ __forceinline__ float pow2_up(float s) {
     return __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u);
 }
 
-__device__ __forceinline__ uint64_t f32x2_of(float lo, float hi) {
-    return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi));
-}
-
 // silu(g) u on two values.  exp(-|g|) = 2^t, t = -|g| log2(e): the product's rounding
 // error comes from an fma (Dekker's error-free product) and enters as 2^t (1 + t_lo ln 2);
 // the sigmoid is r = 1 / (1 + e), or e r for negative g, so no exponential overflows.
