@@ -104,7 +104,7 @@ extern "C" {
 int64_t fp8_moe_route_workspace_bytes(int64_t T, int32_t E, int32_t top) {
     if (T < 0 || E < 1 || E > FP8_MAX_EXPERTS || top < 1 || top > FP8_MAX_TOP || top > E || T * top >= kLim) return 0;
     const int64_t chunks = route_chunks(T);
-    return chunks > 1 ? 4 * (E + 1) * chunks : 0;
+    return chunks > 1 ? int64_t(4) * E * chunks : 0;
 }
 
 int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E, int32_t top, int flags, float scale,

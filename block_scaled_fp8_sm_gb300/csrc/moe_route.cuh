@@ -10,7 +10,9 @@
 // What bounds it: one pass over the logits (16384 x 64 fp32: 4.2 MB), in practice the
 // selection's instructions and, for few tokens, latency.  A warp owns a token and a lane V
 // neighbouring experts, so that the lowest lane of equal maxima holds the lowest expert: a
-// pick is one warp maximum over the lanes' own maxima and one vote.  The expert order is a
+// pick is one warp maximum over the lanes' own maxima and one vote.  A lane's own experts are
+// sorted first, up to eight of them, so that its next maximum is a shift (16001 tokens, 8 of 256:
+// searching them again for each pick took twice the instructions).  The expert order is a
 // counting sort: integer counts of each CTA's tokens, and in the second kernel each CTA's
 // base from the counts of the CTAs before it; nothing depends on the order in which atomics
 // arrive.
@@ -22,7 +24,7 @@
 
 namespace bsfp8 {
 
-constexpr int ROUTE_THREADS = 512, ROUTE_WARPS = ROUTE_THREADS / 32;
+constexpr int ROUTE_THREADS = 1024, ROUTE_WARPS = ROUTE_THREADS / 32;
 constexpr int ROUTE_MAX_TOP = 32;       // a lane for each pick
 constexpr int ROUTE_CHUNKS = 152;       // CTAs of the ordered form: one for each SM
 
@@ -34,7 +36,7 @@ struct RouteArgs {
     int32_t *offsets;         // [E + 1], or null: no order
     int32_t *rows;            // [T * top]
     int32_t *places;          // [T, top]
-    int32_t *counts;          // [E + 1][chunks]: pairs of each chunk's tokens (the last: without an expert)
+    int32_t *counts;          // [E][chunks]: pairs of each chunk's tokens
     int T, E, top, chunk, chunks;   // chunk: tokens of a CTA
     int sigmoid, all, vec;    // all: weights over all experts; vec: rows allow vector loads
     float scale;
@@ -109,24 +111,83 @@ __device__ __forceinline__ void load_keys(const RouteArgs &a, int64_t token, uin
 // exp(v - m) with m the row's largest; v == m covers a row of infinities.
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : expf(v - m); }
 
-// A token's picks: lane j < top writes pick j and returns its expert (-1: none left).
+// Sorts the lane's keys, the largest first, and their numbers (four bits each in `at`) with
+// them; returns false where equal keys may be out of order.  Merge exchange (Batcher, 1968;
+// Knuth, The Art of Computer Programming 3, 5.2.2, algorithm M).
 template <int V>
-__device__ __forceinline__ int pick(const RouteArgs &a, int64_t token, uint32_t (&key)[V]) {
+__device__ __forceinline__ bool sort_keys(uint32_t (&key)[V], uint32_t &at) {
+    uint32_t n[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) n[i] = i;
+#pragma unroll
+    for (int p = V / 2; p > 0; p /= 2) {
+        int q = V / 2, r = 0, d = p;
+#pragma unroll
+        for (int step = 0; step < 4; ++step) {
+            if (d > 0) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i + d < V && (i & p) == r) {
+                        const bool swap = key[i + d] > key[i];
+                        const uint32_t hi = max(key[i], key[i + d]), lo = min(key[i], key[i + d]);
+                        const uint32_t a = swap ? n[i + d] : n[i], b = swap ? n[i] : n[i + d];
+                        key[i] = hi, key[i + d] = lo, n[i] = a, n[i + d] = b;
+                    }
+                if (q == p) break;
+                d = q - p;
+                q /= 2;
+                r = p;
+            }
+        }
+    }
+    at = 0u;
+    bool distinct = true;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        at |= n[i] << (4 * i);
+        if (i > 0) distinct &= key[i] != key[i - 1] || key[i] == 0u;
+    }
+    return distinct;
+}
+
+// A token's picks: lane j < top gets pick j, its expert (-1: none left) and its key.
+template <int V>
+__device__ __forceinline__ void pick(const RouteArgs &a, uint32_t (&key)[V], uint32_t head, int &id, uint32_t &mine) {
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31;
-    uint32_t head = 0u;
+    id = -1;
+    mine = 0u;
+    uint32_t at = 0u;
+    bool sorted = false;
+    if constexpr (V >= 2 && V <= 8) {
+        uint32_t k[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) head = max(head, key[i]);
-    float sum = 0.0f;
-    if (a.all && !a.sigmoid) {   // the softmax's sum over every open expert
-        const float m = key_logit(__reduce_max_sync(ALL, head));
+        for (int i = 0; i < V; ++i) k[i] = key[i];
+        sorted = __all_sync(ALL, sort_keys<V>(k, at));
+        if (sorted) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum += key[i] ? exp_below(key_logit(key[i]), m) : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
+            for (int i = 0; i < V; ++i) key[i] = k[i];
+        }
     }
-    int id = -1, at = 0;
-    uint32_t mine = 0u;
+    if (sorted) {
+        for (int j = 0; j < a.top; ++j) {
+            const uint32_t best = __reduce_max_sync(ALL, key[0]);
+            if (best == 0u) break;
+            const int src = __ffs(__ballot_sync(ALL, key[0] == best)) - 1;
+            const int e = src * V + (__shfl_sync(ALL, at, src) & 15);
+            if (lane == src) {
+#pragma unroll
+                for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+                key[V - 1] = 0u;
+                at >>= 4;
+            }
+            if (lane == j) {
+                id = e;
+                mine = best;
+            }
+        }
+        return;
+    }
     for (int j = 0; j < a.top; ++j) {
         const uint32_t best = __reduce_max_sync(ALL, head);
         if (best == 0u) break;
@@ -149,22 +210,39 @@ __device__ __forceinline__ int pick(const RouteArgs &a, int64_t token, uint32_t 
             mine = best;
         }
     }
-    const float v = key_logit(mine), top = __shfl_sync(ALL, v, 0);
-    float p = 0.0f;
-    if (mine) {
-        if (!a.sigmoid) {
-            p = exp_below(v, top);
-        } else if (v > 0.0f) {
-            p = 1.0f / (1.0f + expf(-v));
-        } else {   // over the chosen ones: all scaled by exp(-m), so that their sum is not lost
-            const float m = a.all ? 0.0f : fminf(top, 0.0f);
-            p = expf(v - m) / (1.0f + expf(v));
-        }
-    }
-    if (!a.all) {
-        sum = p;
+}
+
+// Picks and weights of a token, written by lane j < top; returns its expert.
+template <int V>
+__device__ __forceinline__ int route_token(const RouteArgs &a, int64_t token, uint32_t (&key)[V]) {
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    uint32_t head = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) head = max(head, key[i]);
+    float sum = 0.0f;
+    if (a.all && !a.sigmoid) {   // the softmax's sum over every open expert
+        const float m = key_logit(__reduce_max_sync(ALL, head));
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += key[i] ? exp_below(key_logit(key[i]), m) : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
+    }
+    int id;
+    uint32_t mine;
+    pick<V>(a, key, head, id, mine);
+    const float v = key_logit(mine), top = __shfl_sync(ALL, v, 0);
+    float p = 0.0f;
+    if (!a.sigmoid) {
+        p = exp_below(v, top);
+    } else {   // over the chosen ones: all scaled by exp(-m), m the largest below 0, so that their sum is not lost
+        const float e = expf(-fabsf(v)), m = a.all ? 0.0f : fminf(top, 0.0f);
+        p = (m < 0.0f ? expf(v - m) : v > 0.0f ? 1.0f : e) / (1.0f + e);
+    }
+    if (!mine) p = 0.0f;
+    if (!a.all) {
+        sum = p;
+        for (int o = 1; o < a.top; o <<= 1) sum += __shfl_xor_sync(ALL, sum, o);   // the lanes from top on have zeros
     }
     if (lane < a.top) {
         const bool divide = !a.all || !a.sigmoid;
@@ -198,140 +276,160 @@ __device__ __forceinline__ void scan_exclusive(int *v, int n, int *seg) {
 }
 
 // The pairs of warp `warp` of a CTA's [p0, p1): contiguous, so that the order is stable.
-__device__ __forceinline__ void warp_pairs(int64_t p0, int64_t p1, int warp, int64_t &lo, int64_t &hi) {
-    const int64_t per = (p1 - p0 + ROUTE_WARPS - 1) / ROUTE_WARPS;
+__device__ __forceinline__ void warp_pairs(int p0, int p1, int warp, int &lo, int &hi) {
+    const int per = (p1 - p0 + ROUTE_WARPS - 1) / ROUTE_WARPS;
     lo = min(p1, p0 + warp * per);
     hi = min(p1, lo + per);
 }
 
-// wh[warp][bucket] += the warp's pairs of each bucket (E: without an expert).
-__device__ __forceinline__ void count_pairs(const RouteArgs &a, int64_t p0, int64_t p1, int *wh) {
+// Words of a row of wh: E and the total, an odd number, so that a column meets all banks.
+__host__ __device__ constexpr int route_ld(int E) { return (E + 1) | 1; }
+
+// wh[warp][e] += the warp's pairs of each expert.
+__device__ __forceinline__ void count_pairs(const RouteArgs &a, int p0, int p1, int *wh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int *mine = wh + warp * (a.E + 1);
-    int64_t lo, hi;
+    int *mine = wh + warp * route_ld(a.E);
+    int lo, hi;
     warp_pairs(p0, p1, warp, lo, hi);
-    for (int64_t p = lo + lane; p - lane < hi; p += 32) {
-        int e = p < hi ? a.ids[p] : -2;
-        if (e == -1) e = a.E;
+    for (int p = lo + lane; p - lane < hi; p += 32) {
+        const int e = p < hi ? a.ids[p] : -1;
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
         if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
     }
 }
 
-// Places and rows of the CTA's pairs; wh[warp][bucket] is the next place there.
-__device__ __forceinline__ void place_pairs(const RouteArgs &a, int64_t p0, int64_t p1, int *wh) {
+// Places and rows of the CTA's pairs; wh[warp][e] is the next place there.
+__device__ __forceinline__ void place_pairs(const RouteArgs &a, int p0, int p1, int *wh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int *mine = wh + warp * (a.E + 1);
-    int64_t lo, hi;
+    int *mine = wh + warp * route_ld(a.E);
+    int lo, hi;
     warp_pairs(p0, p1, warp, lo, hi);
-    for (int64_t p = lo + lane; p - lane < hi; p += 32) {
-        int e = p < hi ? a.ids[p] : -2;
-        const bool none = e == -1;
-        if (none) e = a.E;
+    for (int p = lo + lane; p - lane < hi; p += 32) {
+        const int e = p < hi ? a.ids[p] : -1;
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        const int at = e >= 0 ? mine[e] + __popc(same & ((1u << lane) - 1u)) : 0;
+        const int at = e >= 0 ? mine[e] + __popc(same & ((1u << lane) - 1u)) : -1;
         __syncwarp();
         if (e >= 0) {
             if (lane == __ffs(same) - 1) mine[e] += __popc(same);
-            a.rows[at] = none ? -1 : static_cast<int32_t>(p / a.top);
-            a.places[p] = none ? -1 : at;
+            a.rows[at] = static_cast<int>(static_cast<uint32_t>(p) / static_cast<uint32_t>(a.top));
         }
+        if (p < hi) a.places[p] = at;
         __syncwarp();
     }
 }
 
-constexpr int route_smem(int E) { return ((ROUTE_WARPS + 1) * (E + 1) + (E + 1 + 31) / 32) * 4; }
+// The rows from the number of pairs with an expert on, shared out over the CTAs.
+__device__ __forceinline__ void fill_rows(const RouteArgs &a, int used) {
+    for (int p = used + static_cast<int>(blockIdx.x * ROUTE_THREADS + threadIdx.x); p < a.T * a.top;
+         p += static_cast<int>(gridDim.x * ROUTE_THREADS))
+        a.rows[p] = -1;
+}
+
+// wh[w][e] of each warp w becomes `first` and what the warps before it have; returns all of them.
+__device__ __forceinline__ int warp_starts(int *wh, int ld, int e, int first) {
+    static_assert(ROUTE_WARPS == 32, "a lane for each warp");
+    const int lane = threadIdx.x & 31, x = wh[lane * ld + e];
+    int sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    wh[lane * ld + e] = first + sum - x;
+    return __shfl_sync(0xFFFFFFFFu, sum, 31);
+}
+
+constexpr int route_smem(int E) { return ((ROUTE_WARPS + 1) * route_ld(E) + (E + 1 + 31) / 32) * 4; }
 
 // Picks of a CTA's tokens.  With an order: their counts, or, when there is one CTA, the
 // whole order.
 template <int V, bool BF16>
-__global__ void __launch_bounds__(ROUTE_THREADS) bsfp8_route_pick(const RouteArgs a) {
-    extern __shared__ int sh[];   // wh[ROUTE_WARPS][E + 1], base[E + 1], seg
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = a.E + 1;
-    int *wh = sh, *base = sh + ROUTE_WARPS * n, *seg = base + n;
+__global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_pick(const RouteArgs a) {
+    extern __shared__ int sh[];   // wh[ROUTE_WARPS][ld], base[ld], seg
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = a.E + 1, ld = route_ld(a.E);
+    int *wh = sh, *base = sh + ROUTE_WARPS * ld, *seg = base + ld;
     const int t0 = static_cast<int>(blockIdx.x) * a.chunk, t1 = min(a.T, t0 + a.chunk);
     const bool one = a.offsets && gridDim.x == 1;
     if (a.offsets)
-        for (int i = threadIdx.x; i < (one ? (ROUTE_WARPS + 1) * n : n); i += ROUTE_THREADS)
-            (one ? wh : base)[i] = 0;
+        for (int i = threadIdx.x; i < (one ? (ROUTE_WARPS + 1) * ld : ld); i += ROUTE_THREADS) (one ? wh : base)[i] = 0;
     wait_for_previous();
     launch_dependents();
     __syncthreads();
     for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) {
         uint32_t key[V];
         load_keys<V, BF16>(a, t, key);
-        const int id = pick<V>(a, t, key);
-        if (a.offsets && !one && lane < a.top) atomicAdd(&base[id < 0 ? a.E : id], 1);
+        const int id = route_token<V>(a, t, key);
+        if (a.offsets && !one && id >= 0) atomicAdd(&base[id], 1);
     }
     if (!a.offsets) return;
     __syncthreads();
     if (!one) {
-        for (int e = threadIdx.x; e < n; e += ROUTE_THREADS)
+        for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS)
             a.counts[static_cast<int64_t>(e) * a.chunks + blockIdx.x] = base[e];
         return;
     }
-    const int64_t pairs = static_cast<int64_t>(a.T) * a.top;
+    const int pairs = a.T * a.top;   // below 2^30
     count_pairs(a, 0, pairs, wh);
     __syncthreads();
-    for (int e = threadIdx.x; e < n; e += ROUTE_THREADS) {
-        int sum = 0;
-        for (int w = 0; w < ROUTE_WARPS; ++w) sum += wh[w * n + e];
-        base[e] = sum;
+    for (int e = warp; e < a.E; e += ROUTE_WARPS) {
+        const int total = warp_starts(wh, ld, e, 0);
+        if (lane == 0) base[e] = total;
     }
     __syncthreads();
     scan_exclusive(base, n, seg);
-    for (int e = threadIdx.x; e < n; e += ROUTE_THREADS) {
-        int at = base[e];
-        a.offsets[e] = at;
-        for (int w = 0; w < ROUTE_WARPS; ++w) {
-            const int c = wh[w * n + e];
-            wh[w * n + e] = at;
-            at += c;
-        }
-    }
+    for (int i = threadIdx.x; i < ROUTE_WARPS * ld; i += ROUTE_THREADS) wh[i] += base[i % ld];
+    for (int e = threadIdx.x; e < n; e += ROUTE_THREADS) a.offsets[e] = base[e];
+    fill_rows(a, base[a.E]);
     __syncthreads();
     place_pairs(a, 0, pairs, wh);
 }
 
 // The order of the pairs of chunk blockIdx.x from the counts of all chunks.
-__global__ void __launch_bounds__(ROUTE_THREADS) bsfp8_route_order(const RouteArgs a) {
+__global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_order(const RouteArgs a) {
     extern __shared__ int sh[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = a.E + 1;
-    int *wh = sh, *base = sh + ROUTE_WARPS * n, *seg = base + n;
-    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.chunk * a.top;
-    const int64_t p1 = min(static_cast<int64_t>(a.T) * a.top, p0 + static_cast<int64_t>(a.chunk) * a.top);
-    for (int i = threadIdx.x; i < ROUTE_WARPS * n; i += ROUTE_THREADS) wh[i] = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = a.E + 1, ld = route_ld(a.E);
+    int *wh = sh, *base = sh + ROUTE_WARPS * ld, *seg = base + ld;
+    const int p0 = static_cast<int>(blockIdx.x) * a.chunk * a.top, p1 = min(a.T * a.top, p0 + a.chunk * a.top);
+    for (int i = threadIdx.x; i < (ROUTE_WARPS + 1) * ld; i += ROUTE_THREADS) wh[i] = 0;
     wait_for_previous();
     launch_dependents();
     __syncthreads();
     count_pairs(a, p0, p1, wh);
     __syncthreads();
-    // a warp for each bucket: all of it, and what the chunks before this one have of it
-    for (int e = warp; e < n; e += ROUTE_WARPS) {
-        int all = 0, before = 0;
-        for (int c = lane; c < a.chunks; c += 32) {
-            const int x = a.counts[static_cast<int64_t>(e) * a.chunks + c];
-            all += x;
-            if (c < static_cast<int>(blockIdx.x)) before += x;
-        }
-        all = __reduce_add_sync(0xFFFFFFFFu, all);
-        before = __reduce_add_sync(0xFFFFFFFFu, before);
-        if (lane == 0) {
-            base[e] = all;
-            int at = before;   // relative to the bucket's first place, which is known after the scan
-            for (int w = 0; w < ROUTE_WARPS; ++w) {
-                const int x = wh[w * n + e];
-                wh[w * n + e] = at;
-                at += x;
+    // a warp for four experts at a time: all of each, what the chunks before this one have of it,
+    // and (a lane for each warp's part) where the warps' pairs start
+    constexpr int LOADS = (ROUTE_CHUNKS + 31) / 32;
+    for (int e0 = warp * 4; e0 < a.E; e0 += ROUTE_WARPS * 4) {
+        int x[4][LOADS];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int c = lane + 32 * i;
+                x[k][i] = e0 + k < a.E && c < a.chunks ? a.counts[static_cast<int64_t>(e0 + k) * a.chunks + c] : 0;
             }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (e0 + k >= a.E) break;
+            int all = 0, before = 0;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                all += x[k][i];
+                before += lane + 32 * i < static_cast<int>(blockIdx.x) ? x[k][i] : 0;
+            }
+            all = __reduce_add_sync(0xFFFFFFFFu, all);
+            before = __reduce_add_sync(0xFFFFFFFFu, before);
+            warp_starts(wh, ld, e0 + k, before);
+            if (lane == 0) base[e0 + k] = all;
         }
     }
     __syncthreads();
     scan_exclusive(base, n, seg);
-    for (int i = threadIdx.x; i < ROUTE_WARPS * n; i += ROUTE_THREADS) wh[i] += base[i % n];
+    for (int i = threadIdx.x; i < ROUTE_WARPS * ld; i += ROUTE_THREADS) wh[i] += base[i % ld];
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < n; e += ROUTE_THREADS) a.offsets[e] = base[e];
+    fill_rows(a, base[a.E]);
     __syncthreads();
     place_pairs(a, p0, p1, wh);
 }
