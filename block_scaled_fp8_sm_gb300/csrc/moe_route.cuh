@@ -9,13 +9,16 @@
 //
 // What bounds it: one pass over the logits (16384 x 64 fp32: 4.2 MB), in practice the
 // selection's instructions and, for few tokens, latency.  A warp owns a token and a lane V
-// neighbouring experts, so that the lowest lane of equal maxima holds the lowest expert: a
-// pick is one warp maximum over the lanes' own maxima and one vote.  A lane's own experts are
-// sorted first, up to eight of them, so that its next maximum is a shift (16001 tokens, 8 of 256:
-// searching them again for each pick took twice the instructions).  The expert order is a
-// counting sort: integer counts of each CTA's tokens, and in the second kernel each CTA's
-// base from the counts of the CTAs before it; nothing depends on the order in which atomics
-// arrive.
+// neighbouring experts, so that the lowest lane of equal maxima holds the lowest expert.
+//
+// Up to two experts a lane: a pick is one warp maximum over the lanes' own maxima and one vote.
+// More: the `top`-th largest of the lanes' own maxima is a bound that at least top logits reach
+// and few others do; those that do (up to 32) come to a lane each, which counts the ones
+// before it (16001 tokens, 8 of 256: 336 instructions a token for 640 by picks).
+//
+// The expert order is a counting sort: integer counts of each CTA's tokens, and in the second
+// kernel each CTA's base from the counts of the CTAs before it; nothing depends on the order in
+// which atomics arrive.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -111,86 +114,23 @@ __device__ __forceinline__ void load_keys(const RouteArgs &a, int64_t token, uin
 // exp(v - m) with m the row's largest; v == m covers a row of infinities.
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : expf(v - m); }
 
-// Sorts the lane's keys, the largest first, and their numbers (four bits each in `at`) with
-// them; returns false where equal keys may be out of order.  Merge exchange (Batcher, 1968;
-// Knuth, The Art of Computer Programming 3, 5.2.2, algorithm M).
-template <int V>
-__device__ __forceinline__ bool sort_keys(uint32_t (&key)[V], uint32_t &at) {
-    uint32_t n[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) n[i] = i;
-#pragma unroll
-    for (int p = V / 2; p > 0; p /= 2) {
-        int q = V / 2, r = 0, d = p;
-#pragma unroll
-        for (int step = 0; step < 4; ++step) {
-            if (d > 0) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i + d < V && (i & p) == r) {
-                        const bool swap = key[i + d] > key[i];
-                        const uint32_t hi = max(key[i], key[i + d]), lo = min(key[i], key[i + d]);
-                        const uint32_t a = swap ? n[i + d] : n[i], b = swap ? n[i] : n[i + d];
-                        key[i] = hi, key[i + d] = lo, n[i] = a, n[i + d] = b;
-                    }
-                if (q == p) break;
-                d = q - p;
-                q /= 2;
-                r = p;
-            }
-        }
-    }
-    at = 0u;
-    bool distinct = true;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        at |= n[i] << (4 * i);
-        if (i > 0) distinct &= key[i] != key[i - 1] || key[i] == 0u;
-    }
-    return distinct;
-}
+// What a lane has of a token's picks: the expert and key of pick `slot` (below top), or none.
+struct Pick {
+    int id, slot;
+    uint32_t key, best;   // best: the largest key of all
+};
 
-// A token's picks: lane j < top gets pick j, its expert (-1: none left) and its key.
+// One pick after the other; pick j goes to lane j.  head: the lane's largest key.
 template <int V>
-__device__ __forceinline__ void pick(const RouteArgs &a, uint32_t (&key)[V], uint32_t head, int &id, uint32_t &mine) {
+__device__ __forceinline__ Pick pick_each(int top, uint32_t (&key)[V], uint32_t head) {
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31;
-    id = -1;
-    mine = 0u;
-    uint32_t at = 0u;
-    bool sorted = false;
-    if constexpr (V >= 2 && V <= 8) {
-        uint32_t k[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) k[i] = key[i];
-        sorted = __all_sync(ALL, sort_keys<V>(k, at));
-        if (sorted) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = k[i];
-        }
-    }
-    if (sorted) {
-        for (int j = 0; j < a.top; ++j) {
-            const uint32_t best = __reduce_max_sync(ALL, key[0]);
-            if (best == 0u) break;
-            const int src = __ffs(__ballot_sync(ALL, key[0] == best)) - 1;
-            const int e = src * V + (__shfl_sync(ALL, at, src) & 15);
-            if (lane == src) {
-#pragma unroll
-                for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-                key[V - 1] = 0u;
-                at >>= 4;
-            }
-            if (lane == j) {
-                id = e;
-                mine = best;
-            }
-        }
-        return;
-    }
-    for (int j = 0; j < a.top; ++j) {
+    Pick r{-1, lane, 0u, 0u};
+    int at = 0;
+    for (int j = 0; j < top; ++j) {
         const uint32_t best = __reduce_max_sync(ALL, head);
         if (best == 0u) break;
+        if (j == 0) r.best = best;
         const int src = __ffs(__ballot_sync(ALL, head == best)) - 1;
         if (lane == src) {   // the lowest of its experts with this value is taken
             bool taken = false;
@@ -206,17 +146,64 @@ __device__ __forceinline__ void pick(const RouteArgs &a, uint32_t (&key)[V], uin
         }
         const int e = src * V + __shfl_sync(ALL, at, src);
         if (lane == j) {
-            id = e;
-            mine = best;
+            r.id = e;
+            r.key = best;
         }
     }
+    return r;
 }
 
-// Picks and weights of a token, written by lane j < top; returns its expert.
+// All picks at once, by a bound; false (and nothing done) where more than 32 keys reach it.
 template <int V>
-__device__ __forceinline__ int route_token(const RouteArgs &a, int64_t token, uint32_t (&key)[V]) {
+__device__ __forceinline__ bool pick_all(int top, const uint32_t (&key)[V], uint32_t head, uint2 *mine, Pick &r) {
     constexpr uint32_t ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31;
+    uint32_t bound = 1u;   // fewer lanes than top with an open expert: every open one
+    r = Pick{-1, 32, 0u, 0u};
+    for (int j = 0; j < top; ++j) {
+        const uint32_t best = __reduce_max_sync(ALL, head);
+        if (j == 0) r.best = best;
+        bound = max(best, 1u);
+        if (best == 0u) break;
+        if (lane == __ffs(__ballot_sync(ALL, head == best)) - 1) head = 0u;
+    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += key[i] >= bound;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(ALL, sum, o);
+        if (lane >= o) sum += v;
+    }
+    const int all = __shfl_sync(ALL, sum, 31);
+    if (all > 32) return false;
+    int at = sum - n;   // in the order of the experts
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (key[i] >= bound) mine[at++] = make_uint2(key[i], static_cast<uint32_t>(lane * V + i));
+    __syncwarp();
+    const uint2 own = lane < all ? mine[lane] : make_uint2(0u, 0u);
+    __syncwarp();
+    int before = 0;
+    for (int c = 0; c < all; ++c) {
+        const uint32_t k = __shfl_sync(ALL, own.x, c);
+        before += k > own.x || (k == own.x && c < lane);
+    }
+    if (lane < all && before < top) {
+        r.id = static_cast<int>(own.y);
+        r.key = own.x;
+        r.slot = before;
+    }
+    // slots without an expert go to lanes without one
+    if (lane >= all && lane < top) r.slot = lane;
+    return true;
+}
+
+// Picks and weights of a token; returns the lane's expert (-1: none).
+template <int V>
+__device__ __forceinline__ int route_token(const RouteArgs &a, int64_t token, uint32_t (&key)[V], uint2 *mine) {
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
     uint32_t head = 0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) head = max(head, key[i]);
@@ -228,28 +215,32 @@ __device__ __forceinline__ int route_token(const RouteArgs &a, int64_t token, ui
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
     }
-    int id;
-    uint32_t mine;
-    pick<V>(a, key, head, id, mine);
-    const float v = key_logit(mine), top = __shfl_sync(ALL, v, 0);
+    Pick r;
+    if constexpr (V <= 2) {
+        r = pick_each<V>(a.top, key, head);
+    } else {
+        if (!pick_all<V>(a.top, key, head, mine, r)) r = pick_each<V>(a.top, key, head);
+    }
+    const float v = key_logit(r.key), top = key_logit(r.best);
     float p = 0.0f;
     if (!a.sigmoid) {
         p = exp_below(v, top);
     } else {   // over the chosen ones: all scaled by exp(-m), m the largest below 0, so that their sum is not lost
         const float e = expf(-fabsf(v)), m = a.all ? 0.0f : fminf(top, 0.0f);
-        p = (m < 0.0f ? expf(v - m) : v > 0.0f ? 1.0f : e) / (1.0f + e);
+        p = __fdividef(m < 0.0f ? expf(v - m) : v > 0.0f ? 1.0f : e, 1.0f + e);
     }
-    if (!mine) p = 0.0f;
+    if (!r.key) p = 0.0f;
     if (!a.all) {
         sum = p;
-        for (int o = 1; o < a.top; o <<= 1) sum += __shfl_xor_sync(ALL, sum, o);   // the lanes from top on have zeros
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
     }
-    if (lane < a.top) {
+    if (r.slot < a.top) {
         const bool divide = !a.all || !a.sigmoid;
-        a.ids[token * a.top + lane] = id;
-        a.weights[token * a.top + lane] = mine ? (divide ? p / sum : p) * a.scale : 0.0f;
+        a.ids[token * a.top + r.slot] = r.id;
+        a.weights[token * a.top + r.slot] = r.key ? (divide ? __fdividef(p, sum) : p) * a.scale : 0.0f;   // sum is in [0.5, E]
     }
-    return id;
+    return r.id;
 }
 
 // Exclusive sums of v[0 .. n) in place, by the whole CTA; seg: a word for each 32 of them.
@@ -299,8 +290,8 @@ __device__ __forceinline__ void count_pairs(const RouteArgs &a, int p0, int p1, 
     }
 }
 
-// Places and rows of the CTA's pairs; wh[warp][e] is the next place there.
-__device__ __forceinline__ void place_pairs(const RouteArgs &a, int p0, int p1, int *wh) {
+// Places and rows of the CTA's pairs; base[e] + wh[warp][e] is the next place there.
+__device__ __forceinline__ void place_pairs(const RouteArgs &a, int p0, int p1, int *wh, const int *base) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int *mine = wh + warp * route_ld(a.E);
     int lo, hi;
@@ -308,7 +299,7 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int p0, int p1, 
     for (int p = lo + lane; p - lane < hi; p += 32) {
         const int e = p < hi ? a.ids[p] : -1;
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        const int at = e >= 0 ? mine[e] + __popc(same & ((1u << lane) - 1u)) : -1;
+        const int at = e >= 0 ? base[e] + mine[e] + __popc(same & ((1u << lane) - 1u)) : -1;
         __syncwarp();
         if (e >= 0) {
             if (lane == __ffs(same) - 1) mine[e] += __popc(same);
@@ -349,6 +340,8 @@ __global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_pick(const Route
     extern __shared__ int sh[];   // wh[ROUTE_WARPS][ld], base[ld], seg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = a.E + 1, ld = route_ld(a.E);
     int *wh = sh, *base = sh + ROUTE_WARPS * ld, *seg = base + ld;
+    __shared__ uint2 candidates[V > 2 ? ROUTE_WARPS : 1][32];
+    uint2 *mine = candidates[V > 2 ? warp : 0];
     const int t0 = static_cast<int>(blockIdx.x) * a.chunk, t1 = min(a.T, t0 + a.chunk);
     const bool one = a.offsets && gridDim.x == 1;
     if (a.offsets)
@@ -359,14 +352,14 @@ __global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_pick(const Route
     for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) {
         uint32_t key[V];
         load_keys<V, BF16>(a, t, key);
-        const int id = route_token<V>(a, t, key);
+        const int id = route_token<V>(a, t, key, mine);
         if (a.offsets && !one && id >= 0) atomicAdd(&base[id], 1);
     }
     if (!a.offsets) return;
     __syncthreads();
     if (!one) {
         for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS)
-            a.counts[static_cast<int64_t>(e) * a.chunks + blockIdx.x] = base[e];
+            a.counts[e * a.chunks + blockIdx.x] = base[e];
         return;
     }
     const int pairs = a.T * a.top;   // below 2^30
@@ -378,11 +371,9 @@ __global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_pick(const Route
     }
     __syncthreads();
     scan_exclusive(base, n, seg);
-    for (int i = threadIdx.x; i < ROUTE_WARPS * ld; i += ROUTE_THREADS) wh[i] += base[i % ld];
     for (int e = threadIdx.x; e < n; e += ROUTE_THREADS) a.offsets[e] = base[e];
     fill_rows(a, base[a.E]);
-    __syncthreads();
-    place_pairs(a, 0, pairs, wh);
+    place_pairs(a, 0, pairs, wh, base);
 }
 
 // The order of the pairs of chunk blockIdx.x from the counts of all chunks.
@@ -402,13 +393,12 @@ __global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_order(const Rout
     constexpr int LOADS = (ROUTE_CHUNKS + 31) / 32;
     for (int e0 = warp * 4; e0 < a.E; e0 += ROUTE_WARPS * 4) {
         int x[4][LOADS];
+        const int32_t *from = a.counts + e0 * a.chunks + lane;   // below 2^18
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int c = lane + 32 * i;
-                x[k][i] = e0 + k < a.E && c < a.chunks ? a.counts[static_cast<int64_t>(e0 + k) * a.chunks + c] : 0;
-            }
+            for (int i = 0; i < LOADS; ++i)
+                x[k][i] = e0 + k < a.E && lane + 32 * i < a.chunks ? from[k * a.chunks + 32 * i] : 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (e0 + k >= a.E) break;
@@ -426,12 +416,10 @@ __global__ void __launch_bounds__(ROUTE_THREADS, 1) bsfp8_route_order(const Rout
     }
     __syncthreads();
     scan_exclusive(base, n, seg);
-    for (int i = threadIdx.x; i < ROUTE_WARPS * ld; i += ROUTE_THREADS) wh[i] += base[i % ld];
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < n; e += ROUTE_THREADS) a.offsets[e] = base[e];
     fill_rows(a, base[a.E]);
-    __syncthreads();
-    place_pairs(a, p0, p1, wh);
+    place_pairs(a, p0, p1, wh, base);
 }
 
 }  // namespace bsfp8
