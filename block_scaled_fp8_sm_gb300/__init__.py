@@ -408,27 +408,38 @@ def fp8_moe_route(logits, top, sigmoid=False, renormalize=True, scale=1.0, order
     T, E = logits.shape
     if out is None or (order and workspace is None):
         out, workspace = _route_outputs(T, E, top, order, out, workspace, logits.device, stream)
-    weights, ids = out[:2]
-    if (weights.shape != (T, top) or ids.shape != (T, top) or len(out) != (5 if order else 2)
-            or (order and (out[2].shape != (E + 1,) or out[3].shape != (T * top,) or out[4].shape != (T, top)))):
-        raise ValueError("fp8_moe_route: out must be weights and ids [T, top], and with an order offsets [E + 1], "
-                         "rows [T * top] and places [T, top]")
+    if len(out) != (5 if order else 2):
+        raise ValueError("fp8_moe_route: out must be (weights, ids, offsets, rows, places), or (weights, ids) without an order")
     d = _Calls.loaded or _Calls()
     dev = logits.get_device()
-    if not (logits.dtype in d.floats and (logits.stride(1) == 1 or E <= 1) and weights.dtype is d.f32
-            and weights.is_contiguous() and dev >= 0 and weights.get_device() == dev and d.device() == dev
-            and all(t.dtype is d.i32 and t.is_contiguous() and t.get_device() == dev for t in out[1:])
-            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+    weights, ids = out[0], out[1]
+    pairs = (T, top)
+    good = (weights.shape == pairs and ids.shape == pairs and logits.dtype in d.floats
+            and (logits.stride(1) == 1 or E <= 1) and weights.dtype is d.f32 and ids.dtype is d.i32
+            and weights.is_contiguous() and ids.is_contiguous()
+            and dev >= 0 and weights.get_device() == dev and ids.get_device() == dev and d.device() == dev)
+    at, space, size = (None, None, None), None, 0
+    if order:
+        offsets, rows, places = out[2], out[3], out[4]
+        good = (good and offsets.shape == (E + 1,) and rows.shape == (T * top,) and places.shape == pairs
+                and offsets.dtype is d.i32 and rows.dtype is d.i32 and places.dtype is d.i32
+                and offsets.is_contiguous() and rows.is_contiguous() and places.is_contiguous()
+                and workspace.is_contiguous() and offsets.get_device() == dev and rows.get_device() == dev
+                and places.get_device() == dev and workspace.get_device() == dev)
+        at = (offsets.data_ptr(), rows.data_ptr(), places.data_ptr())
+        space, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if not good:
+        shapes = [pairs, pairs, (E + 1,), (T * top,), pairs]
+        if any(tuple(t.shape) != shape for t, shape in zip(out, shapes)):
+            raise ValueError("fp8_moe_route: out must be weights and ids [T, top], and with an order offsets [E + 1], "
+                             "rows [T * top] and places [T, top]")
         raise _refused("fp8_moe_route", ("logits", logits, d.floats), ("weights", weights, d.f32),
                        *[("out", t, d.i32) for t in out[1:]],
-                       *([] if workspace is None else [("workspace", workspace, workspace.dtype)]))
-    offsets, rows, places = (t.data_ptr() for t in out[2:]) if order else (None, None, None)
+                       *([("workspace", workspace, workspace.dtype)] if order else []))
     rc = d.route(logits.data_ptr(), logits.stride(0) if T > 1 else E,
                  FP8_TYPE_BF16 if logits.dtype is d.bf16 else FP8_TYPE_F32, T, E, top,
                  (FP8_ROUTE_SIGMOID if sigmoid else 0) | (0 if renormalize else FP8_ROUTE_ALL), scale,
-                 weights.data_ptr(), ids.data_ptr(), offsets, rows, places,
-                 None if workspace is None else workspace.data_ptr(),
-                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                 weights.data_ptr(), ids.data_ptr(), at[0], at[1], at[2], space, size,
                  d.stream(dev) if stream is None else _stream(stream))
     if rc:
         raise Fp8Error(rc, "fp8_moe_route")

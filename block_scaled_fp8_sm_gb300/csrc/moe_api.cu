@@ -84,8 +84,6 @@ int moe_setup() {
         for (int type : {FP8_TYPE_F32, FP8_TYPE_BF16})
             if (!set_shared(reinterpret_cast<const void *>(pick_kernel(E, type)), route_smem(E))) return FP8_ERR_CUDA;
     return set_shared(reinterpret_cast<const void *>(bsfp8_route_order), route_smem(FP8_MAX_EXPERTS)) &&
-                   set_shared(reinterpret_cast<const void *>(bsfp8_moe_down),
-                              moe_down_shared(MOE_FEW_TOKENS, FP8_MAX_TOP, FP8_MAX_EXPERTS)) &&
                    set_tile_shared<2>() && set_tile_shared<4>() && set_tile_shared<8>()
                ? FP8_OK
                : FP8_ERR_CUDA;
@@ -210,12 +208,14 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
         });
     }
     const MoeArgs &few = a;
-    const int64_t most = T * top < E ? T * top : E;
-    const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(most));
-    rc = launch(bsfp8_moe_up<1>, grid, MOE_THREADS, 0, 1, few, stream);
+    const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(T * top));
+    const bool two = T * top <= 64;   // words of pairs: two, or eight
+    rc = launch(two ? bsfp8_moe_up<2> : bsfp8_moe_up<8>, grid, MOE_THREADS, 0, 1, few, stream);
     if (rc != FP8_OK) return rc;
-    return launch(bsfp8_moe_down, dim3(static_cast<unsigned>((H + MOE_DOWN_COLS - 1) / MOE_DOWN_COLS)), MOE_THREADS,
-                  moe_down_shared(a.T, top, E), 1, few, stream);
+    // one wave: four blocks of a warp on their way; more: three CTAs on an SM
+    const unsigned ctas = static_cast<unsigned>(H / MOE_DOWN_COLS);
+    const auto down = !two ? bsfp8_moe_down<2, 2, 8> : ctas <= 2u * d->sm_count ? bsfp8_moe_down<4, 2, 2> : bsfp8_moe_down<2, 3, 2>;
+    return launch(down, dim3(ctas), MOE_THREADS, 0, 1, few, stream);
 }
 
 }  // extern "C"

@@ -32,7 +32,7 @@ constexpr int MOE_FEW_TOKENS = 8;   // the kernels of this file; more: moe_tile.
 constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 32, MOE_MAX_EXPERTS = 1024;
 constexpr int MOE_WARPS = 8, MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_UP_COLS = 16;     // columns of h per CTA: 16 gate and 16 up rows
-constexpr int MOE_DOWN_COLS = 32;   // columns of the output per CTA
+constexpr int MOE_DOWN_COLS = 16;   // columns of the output per CTA
 
 struct MoeArgs {
     const __nv_bfloat16 *x;   // [T, H]
@@ -100,40 +100,20 @@ __device__ __forceinline__ float block_to_half(const uint4 (&x)[4], uint32_t (&r
     return inverse;
 }
 
-// The sums of two 16-row pieces (a, b: row g, row g + 8 of each) of a weight's 128-K block
-// with N groups of eight tokens.
-template <int N>
-__device__ __forceinline__ void block_products(float (&p)[N][2][4], const uint4 (&a)[2][2], const uint4 (&b)[2][2],
-                                               const uint32_t (&x)[N][16]) {
+// The sums of a 16-row piece (a: row g, b: row g + 8) of a weight's 128-K block with eight tokens.
+__device__ __forceinline__ void block_product(float (&p)[4], const uint4 (&a)[2], const uint4 (&b)[2],
+                                              const uint32_t (&x)[16]) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int c = 0; c < 4; ++c) p[c] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t wa[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+        const uint32_t wb[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) p[n][i][c] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t wa[4] = {a[i][j].x, a[i][j].y, a[i][j].z, a[i][j].w};
-            const uint32_t wb[4] = {b[i][j].x, b[i][j].y, b[i][j].z, b[i][j].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t a0 = half2_of_e4m3x2(wa[c]), a1 = half2_of_e4m3x2(wb[c]);
-                const uint32_t a2 = half2_of_e4m3x2_hi(wa[c]), a3 = half2_of_e4m3x2_hi(wb[c]);
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-                    mma_f16_16x8x16(p[n][i], a0, a1, a2, a3, x[n][8 * j + 2 * c], x[n][8 * j + 2 * c + 1]);
-            }
-        }
-}
-
-// Whether pair p = (t, j) is the first of its token with this expert (the later ones only
-// add their weight to it).
-__device__ __forceinline__ bool first_of_token(const MoeArgs &a, int p, int e) {
-    for (int q = p - p % a.top; q < p; ++q)
-        if (a.ids[q] == e) return false;
-    return true;
+        for (int c = 0; c < 4; ++c)
+            mma_f16_16x8x16(p, half2_of_e4m3x2(wa[c]), half2_of_e4m3x2(wb[c]), half2_of_e4m3x2_hi(wa[c]),
+                            half2_of_e4m3x2_hi(wb[c]), x[8 * j + 2 * c], x[8 * j + 2 * c + 1]);
+    }
 }
 
 // silu(g) * u.  Deep in the negative gates the exponential's two halves go to one factor
@@ -146,132 +126,279 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return t < 0.0f ? (g * n) * (u * n) * r : (g * r) * u;
 }
 
-// Gate and up: a CTA owns 16 columns of h of one busy expert, and all of its tokens, eight
-// times NT at a time.  MMA piece i holds gate rows 8 i .. 8 i + 7 and the up rows of the same
-// columns, so that a thread has both numbers of an h.
-template <int NT>
-__global__ void __launch_bounds__(MOE_THREADS, NT == 1 ? 2 : 1) bsfp8_moe_up(const MoeArgs a) {
-    __shared__ uint32_t bits[MOE_MAX_EXPERTS / 32];
-    __shared__ int found, count;
-    __shared__ uint16_t list[MOE_MAX_TOKENS];   // pairs: one for each of the expert's tokens
-    __shared__ float red[MOE_WARPS][NT][2][4][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int pairs = a.T * a.top, n0 = static_cast<int>(blockIdx.x) * MOE_UP_COLS;
-    if (threadIdx.x < MOE_MAX_EXPERTS / 32) bits[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) found = -1, count = 0;
-    __syncthreads();
-    wait_for_previous();
-    for (int p = threadIdx.x; p < pairs; p += MOE_THREADS) {
-        const uint32_t e = static_cast<uint32_t>(a.ids[p]);
-        if (e < static_cast<uint32_t>(a.E)) atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    if (warp == 0) {   // the blockIdx.y-th busy expert
-        const uint32_t b = bits[lane];
-        int sum = __popc(b);
+// Up to eight tokens are the columns of every MMA, whichever of them an expert has.  An expert's
+// tokens as a warp sees them: bit p of the mask is pair p = (token, j), 32 PW pairs at most.
+template <int PW>
+struct MoePairs {
+    uint32_t bits[PW];   // the same in every lane
+    // The token's pairs with the expert, bit j for pair (token, j).
+    __device__ __forceinline__ uint32_t of(int token, int top) const {
+        const int at = token * top;
+        uint32_t lo = 0u, hi = 0u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += v;
+        for (int i = 0; i < PW; ++i) {
+            if (i == at >> 5) lo = bits[i];
+            if (i == (at >> 5) + 1) hi = bits[i];
         }
-        const int k = static_cast<int>(blockIdx.y) - (sum - __popc(b));
-        if (k >= 0 && k < __popc(b)) {
-            uint32_t left = b;
-            for (int i = 0; i < k; ++i) left &= left - 1u;
-            found = 32 * lane + __ffs(left) - 1;
-        }
+        return __funnelshift_r(lo, hi, at & 31) & (top == 32 ? 0xFFFFFFFFu : (1u << top) - 1u);
     }
-    __syncthreads();
-    const int e = found;
-    if (e < 0) return;
-    for (int p = threadIdx.x; p < pairs; p += MOE_THREADS)
-        if (a.ids[p] == e && first_of_token(a, p, e)) list[atomicAdd(&count, 1)] = static_cast<uint16_t>(p);
-    __syncthreads();
-    const int n = count, KB = (a.H + 127) / 128, NB = (2 * a.I + 127) / 128;
+    // The first of them, or -1.
+    __device__ __forceinline__ int first(int token, int top) const {
+        const uint32_t w = of(token, top);
+        return w ? token * top + __ffs(w) - 1 : -1;
+    }
+};
+
+// Pairs with expert e; own: the lane's ids (pair 32 i + lane), -1 past the end.
+template <int PW>
+__device__ __forceinline__ MoePairs<PW> pairs_of(const int (&own)[PW], int e) {
+    MoePairs<PW> m;
+#pragma unroll
+    for (int i = 0; i < PW; ++i) m.bits[i] = __ballot_sync(0xFFFFFFFFu, own[i] == e);
+    return m;
+}
+
+template <int PW>
+__device__ __forceinline__ void load_ids(const MoeArgs &a, int (&own)[PW]) {
+    const int pairs = a.T * a.top, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < PW; ++i) own[i] = 32 * i + lane < pairs ? a.ids[32 * i + lane] : -1;
+}
+
+// Gate and up: a CTA owns 16 columns of h of one expert, for all of its tokens.  The CTAs of
+// pair blockIdx.y do this where it is the first of all with its expert, and leave otherwise.
+// MMA piece i holds gate rows 8 i .. 8 i + 7 and the up rows of the same columns, so that a
+// thread has both numbers of an h.  A warp has the weights of its next block on their way
+// while it works on one.
+template <int PW>
+__global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_up(const MoeArgs a) {
+    __shared__ float red[MOE_WARPS][2][4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n0 = static_cast<int>(blockIdx.x) * MOE_UP_COLS;
+    wait_for_previous();
+    int own[PW];
+    load_ids<PW>(a, own);
+    const int e = a.ids[blockIdx.y];
+    if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.E)) return;
+    const int KB = (a.H + 127) / 128, NB = (2 * a.I + 127) / 128;
     const uint8_t *W = a.W1 + (static_cast<int64_t>(e) * 2 * a.I + n0 + g) * a.H + 16 * t;
     const int64_t up = static_cast<int64_t>(a.I) * a.H, eight = static_cast<int64_t>(8) * a.H;
+    uint4 wg[2][2], wu[2][2];
+    auto load = [&](int kb) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = kb * 128 + 64 * j;
+            const bool in = k + 16 * t < a.H;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                wg[i][j] = load16_if(W + i * eight + k, in);
+                wu[i][j] = load16_if(W + up + i * eight + k, in);
+            }
+        }
+    };
+    const MoePairs<PW> m = pairs_of<PW>(own, e);
+    {   // an earlier pair has this expert: its CTAs do the work
+        bool earlier = false;
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+            const int left = static_cast<int>(blockIdx.y) - 32 * i;
+            earlier |= left > 0 && (m.bits[i] & (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u)) != 0u;
+        }
+        if (earlier) return;
+    }
+    if (warp < KB) load(warp);
+    const int pair = m.first(g, a.top);   // of this lane's token (none from T on)
+    const __nv_bfloat16 *x = a.x + static_cast<int64_t>(g) * a.H + 16 * t;
     const float *sg = a.s1 + (static_cast<int64_t>(e) * NB + n0 / 128) * KB;
     const float *su = a.s1 + (static_cast<int64_t>(e) * NB + (a.I + n0) / 128) * KB;
-    for (int m0 = 0; m0 < n; m0 += 8 * NT) {
-        float acc[NT][2][4];
-        const __nv_bfloat16 *x[NT];
+    float acc[2][4];
 #pragma unroll
-        for (int k = 0; k < NT; ++k) {
-            const int m = m0 + 8 * k + g;
-            x[k] = m < n ? a.x + static_cast<int64_t>(list[m] / a.top) * a.H + 16 * t : nullptr;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    for (int kb = warp; kb < KB; kb += MOE_WARPS) {
+        uint4 xr[4], now[4][2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[k][i][c] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+            const int k = kb * 128 + 64 * j;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                xr[2 * j + c] = load16_if(reinterpret_cast<const uint8_t *>(x + k + 8 * c), k + 16 * t < a.H && pair >= 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) now[2 * i][j] = wg[i][j], now[2 * i + 1][j] = wu[i][j];
         }
-        for (int kb = warp; kb < KB; kb += MOE_WARPS) {
-            uint4 wg[2][2], wu[2][2], xr[NT][4];
+        const float s_gate = sg[kb], s_up = su[kb];
+        if (kb + MOE_WARPS < KB) load(kb + MOE_WARPS);
+        uint32_t xh[16];
+        const float inverse = block_to_half(xr, xh);
+        // columns 2 t and 2 t + 1: the tokens of lanes 8 t and 8 t + 4
+        const float i0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * t), i1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * t + 4);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int k = kb * 128 + 64 * j;
-                const bool in = k + 16 * t < a.H;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    wg[i][j] = load16_if(W + i * eight + k, in);
-                    wu[i][j] = load16_if(W + up + i * eight + k, in);
-                }
-#pragma unroll
-                for (int m = 0; m < NT; ++m)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        xr[m][2 * j + c] = load16_if(reinterpret_cast<const uint8_t *>(x[m] + k + 8 * c), in && x[m]);
-            }
-            const float s_gate = sg[kb], s_up = su[kb];
-            uint32_t xh[NT][16];
-            float inverse[NT], p[NT][2][4];
-#pragma unroll
-            for (int m = 0; m < NT; ++m) inverse[m] = block_to_half(xr[m], xh[m]);
-            block_products<NT>(p, wg, wu, xh);
-#pragma unroll
-            for (int m = 0; m < NT; ++m) {   // columns 2 t and 2 t + 1: the tokens of lanes 8 t and 8 t + 4
-                const float i0 = __shfl_sync(0xFFFFFFFFu, inverse[m], 8 * t);
-                const float i1 = __shfl_sync(0xFFFFFFFFu, inverse[m], 8 * t + 4);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    acc[m][i][0] = fmaf(s_gate * i0, p[m][i][0], acc[m][i][0]);
-                    acc[m][i][1] = fmaf(s_gate * i1, p[m][i][1], acc[m][i][1]);
-                    acc[m][i][2] = fmaf(s_up * i0, p[m][i][2], acc[m][i][2]);
-                    acc[m][i][3] = fmaf(s_up * i1, p[m][i][3], acc[m][i][3]);
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+            float p[4];
+            block_product(p, now[2 * i], now[2 * i + 1], xh);
+            acc[i][0] = fmaf(s_gate * i0, p[0], acc[i][0]);
+            acc[i][1] = fmaf(s_gate * i1, p[1], acc[i][1]);
+            acc[i][2] = fmaf(s_up * i0, p[2], acc[i][2]);
+            acc[i][3] = fmaf(s_up * i1, p[3], acc[i][3]);
         }
-#pragma unroll
-        for (int k = 0; k < NT; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) red[warp][k][i][c][lane] = acc[k][i][c];
-        __syncthreads();
-        // sixteen threads have a token's columns
-        for (int i = threadIdx.x; i < NT * 128; i += MOE_THREADS) {
-            const int col = i & 15, m = i >> 4, k = m >> 3, tok = m & 7;
-            const int piece = col >> 3, c = tok & 1, l = (col & 7) * 4 + (tok >> 1);
-            float gate = 0.0f, upv = 0.0f;
-#pragma unroll
-            for (int w = 0; w < MOE_WARPS; ++w) {
-                gate += red[w][k][piece][c][l];
-                upv += red[w][k][piece][2 + c][l];
-            }
-            const float v = silu_mul(gate, upv);
-            float amax = fabsf(v);
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            float inverse;
-            const float s = scale_to_half(amax, inverse);
-            if (m0 + m < n) {
-                const int64_t pair = list[m0 + m];
-                a.h[pair * a.I + n0 + col] = __float2half_rn(v * s);
-                if (col == 0) a.hs[pair * (a.I / 16) + n0 / 16] = inverse;
-            }
-        }
-        __syncthreads();
     }
     launch_dependents();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) red[warp][i][c][lane] = acc[i][c];
+    __syncthreads();
+    // sixteen threads have a token's columns
+    if (threadIdx.x < 128) {
+        const int col = lane & 15, tok = static_cast<int>(threadIdx.x) >> 4;
+        const int piece = col >> 3, c = tok & 1, l = (col & 7) * 4 + (tok >> 1);
+        float gate = 0.0f, upv = 0.0f;
+#pragma unroll
+        for (int w = 0; w < MOE_WARPS; ++w) {
+            gate += red[w][piece][c][l];
+            upv += red[w][piece][2 + c][l];
+        }
+        const float v = silu_mul(gate, upv);
+        float amax = fabsf(v);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        float inverse;
+        const float s = scale_to_half(amax, inverse);
+        const int64_t to = m.first(tok, a.top);
+        if (to >= 0) {
+            a.h[to * a.I + n0 + col] = __float2half_rn(v * s);
+            if (col == 0) a.hs[to * (a.I / 16) + n0 / 16] = inverse;
+        }
+    }
+}
+
+// Down and the weighted sum: a CTA owns 16 columns of the output for all tokens and passes
+// over the busy experts in ascending order, U of a warp's blocks on their way.  Their weights
+// and the routing are not written by the up kernel, and what came before that had ended when
+// it let this kernel start: only h waits for it.
+template <int U, int CTAS, int PW>
+__global__ void __launch_bounds__(MOE_THREADS, CTAS) bsfp8_moe_down(const MoeArgs a) {
+    __shared__ uint32_t bits[MOE_MAX_EXPERTS / 32];
+    __shared__ float red[MOE_WARPS][4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n0 = static_cast<int>(blockIdx.x) * MOE_DOWN_COLS;
+    int own[PW];
+    load_ids<PW>(a, own);
+    if (threadIdx.x < MOE_MAX_EXPERTS / 32) bits[threadIdx.x] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PW; ++i)
+        if (i % MOE_WARPS == warp && static_cast<uint32_t>(own[i]) < static_cast<uint32_t>(a.E))
+            atomicOr(&bits[own[i] >> 5], 1u << (own[i] & 31));
+    __syncthreads();
+    const int KB = (a.I + 127) / 128, NB = (a.H + 127) / 128, chunks = a.I / 16;
+    uint32_t left = bits[lane];   // experts of 32 lane .. that are still to come
+    // K block kb of expert e belongs to warp (e KB + kb) mod warps; the warp's next one
+    int e = -1, kb = KB;
+    auto next = [&]() {
+        kb += MOE_WARPS;
+        while (kb >= KB) {
+            const uint32_t any = __ballot_sync(0xFFFFFFFFu, left != 0u);
+            if (!any) return false;
+            const int src = __ffs(any) - 1;
+            const uint32_t word = __shfl_sync(0xFFFFFFFFu, left, src);
+            e = 32 * src + __ffs(word) - 1;
+            if (lane == src) left &= left - 1u;
+            kb = (warp + MOE_WARPS - (e % MOE_WARPS) * (KB % MOE_WARPS) % MOE_WARPS) % MOE_WARPS;
+        }
+        return true;
+    };
+    uint4 wa[U][2], wb[U][2];
+    float sb[U];
+    int es[U], ks[U];
+    auto load = [&](int u) {
+        es[u] = next() ? e : -1;
+        ks[u] = kb;
+        if (es[u] < 0) return;
+        const uint8_t *W = a.W2 + (static_cast<int64_t>(e) * a.H + n0 + g) * a.I + 16 * t;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = kb * 128 + 64 * j;
+            const bool in = k + 16 * t < a.I;
+            wa[u][j] = load16_if(W + k, in);
+            wb[u][j] = load16_if(W + static_cast<int64_t>(8) * a.I + k, in);
+        }
+        sb[u] = a.s2[(static_cast<int64_t>(e) * NB + n0 / 128) * KB + kb];
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        es[u] = -1;
+        if (u == 0 || es[u - 1] >= 0) load(u);
+    }
+    wait_for_previous();
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    while (es[0] >= 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (es[u] < 0) break;
+            const uint32_t mine = pairs_of<PW>(own, es[u]).of(g, a.top);   // none from T on
+            const int64_t pair = mine ? g * a.top + __ffs(mine) - 1 : -1;
+            uint32_t xh[16];
+            float sc[2], w = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int k = ks[u] * 128 + 64 * j + 16 * t;
+                const bool in = pair >= 0 && k < a.I;
+                const uint8_t *h = reinterpret_cast<const uint8_t *>(a.h + pair * a.I + k);
+                sc[j] = in ? a.hs[pair * chunks + k / 16] : 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint4 v = load16_if(h + 16 * c, in);
+                    xh[8 * j + 4 * c] = v.x, xh[8 * j + 4 * c + 1] = v.y;
+                    xh[8 * j + 4 * c + 2] = v.z, xh[8 * j + 4 * c + 3] = v.w;
+                }
+            }
+            // the sum of the token's weights for the expert
+            if (mine) w = a.w[pair];
+            for (uint32_t rest = mine & (mine - 1u); rest; rest &= rest - 1u) w += a.w[g * a.top + __ffs(rest) - 1];
+            // one scale for the block: the largest of its eight
+            float most = fmaxf(fmaxf(sc[0], sc[1]), 0x1p-126f);
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            const float r = __uint_as_float((254u << 23) - __float_as_uint(most));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const __half2 f = __float2half2_rn(sc[j] * r);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&xh[8 * j + c]), f);
+                    xh[8 * j + c] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+            }
+            float p[4];
+            block_product(p, wa[u], wb[u], xh);
+            const float s = sb[u];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float wt = __shfl_sync(0xFFFFFFFFu, w, 8 * t + 4 * c);
+                const float f = s * __shfl_sync(0xFFFFFFFFu, most, 8 * t + 4 * c);
+                const bool has = __shfl_sync(0xFFFFFFFFu, pair >= 0, 8 * t + 4 * c);
+                if (has) {   // (a token without the expert has nothing here, not zero times something)
+                    acc[c] = fmaf(wt, f * p[c], acc[c]);
+                    acc[2 + c] = fmaf(wt, f * p[2 + c], acc[2 + c]);
+                }
+            }
+            load(u);
+        }
+    }
+    launch_dependents();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) red[warp][c][lane] = acc[c];
+    __syncthreads();
+    if (threadIdx.x < 128) {   // sixteen threads a token
+        const int col = lane & 15, tok = static_cast<int>(threadIdx.x) >> 4;
+        const int c = (col >> 3) * 2 + (tok & 1), l = (col & 7) * 4 + (tok >> 1);
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < MOE_WARPS; ++w) v += red[w][c][l];
+        if (tok < a.T) a.out[static_cast<int64_t>(tok) * a.H + n0 + col] = __float2bfloat16_rn(v);
+    }
 }
 
 // The experts' tokens, in shared memory: one entry for each token of an expert, from start[e]
@@ -375,108 +502,6 @@ __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l)
         l.weight[at] = w;
     }
     __syncthreads();
-}
-
-// Shared memory of the down kernel: the lists, and sums [warps][T][columns + 8].
-__host__ __device__ inline int moe_down_shared(int T, int top, int E) {
-    return moe_lists_layout(T, top, E).bytes + 4 * MOE_WARPS * T * (MOE_DOWN_COLS + 8);
-}
-
-// Down and the weighted sum: a CTA owns 32 columns of the output for all tokens and
-// passes over the busy experts in ascending order.  Each warp adds what its K blocks give
-// to sums of its own in shared memory.
-__global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_down(const MoeArgs a) {
-    extern __shared__ __align__(16) uint8_t moe_smem[];
-    const MoeLists L = moe_lists(moe_smem, a.T, a.top, a.E);
-    float *sums = reinterpret_cast<float *>(moe_smem + moe_lists_layout(a.T, a.top, a.E).bytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int n0 = static_cast<int>(blockIdx.x) * MOE_DOWN_COLS;
-    constexpr int LD = MOE_DOWN_COLS + 8;
-    for (int i = threadIdx.x; i < MOE_WARPS * a.T * LD; i += MOE_THREADS) sums[i] = 0.0f;
-    wait_for_previous();
-    build_lists(a, L);
-    const int KB = (a.I + 127) / 128, NB = (a.H + 127) / 128, chunks = a.I / 16;
-    const bool second = n0 + 16 < a.H;   // H is a multiple of 16
-    float *mine = sums + warp * a.T * LD;
-    for (int b = 0; b < *L.experts; ++b) {
-        const int e = L.busy[b], first = L.start[e], n = L.start[e + 1] - first;
-        const uint8_t *W = a.W2 + (static_cast<int64_t>(e) * a.H + n0 + g) * a.I + 16 * t;
-        const float *s2 = a.s2 + (static_cast<int64_t>(e) * NB + n0 / 128) * KB;
-        // K block kb of expert e belongs to warp (e KB + kb) mod warps
-        for (int kb = (warp + MOE_WARPS - (e % MOE_WARPS) * (KB % MOE_WARPS) % MOE_WARPS) % MOE_WARPS; kb < KB; kb += MOE_WARPS) {
-            uint4 wa[2][2], wb[2][2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int k = kb * 128 + 64 * j;
-                const bool in = k + 16 * t < a.I;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    wa[i][j] = load16_if(W + static_cast<int64_t>(16 * i) * a.I + k, in && (i == 0 || second));
-                    wb[i][j] = load16_if(W + static_cast<int64_t>(16 * i + 8) * a.I + k, in && (i == 0 || second));
-                }
-            }
-            const float sb = s2[kb];
-            for (int m0 = 0; m0 < n; m0 += 8) {
-                uint32_t xh[1][16];
-                float sc[2];
-                const int64_t pair = m0 + g < n ? L.pair[first + m0 + g] : -1;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int k = kb * 128 + 64 * j + 16 * t;
-                    const bool in = pair >= 0 && k < a.I;
-                    const uint8_t *h = reinterpret_cast<const uint8_t *>(a.h + pair * a.I + k);
-                    sc[j] = in ? a.hs[pair * chunks + k / 16] : 0.0f;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint4 v = load16_if(h + 16 * c, in);
-                        xh[0][8 * j + 4 * c] = v.x, xh[0][8 * j + 4 * c + 1] = v.y;
-                        xh[0][8 * j + 4 * c + 2] = v.z, xh[0][8 * j + 4 * c + 3] = v.w;
-                    }
-                }
-                // one scale for the block: the largest of its eight
-                float most = fmaxf(fmaxf(sc[0], sc[1]), 0x1p-126f);
-                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-                const float r = __uint_as_float((254u << 23) - __float_as_uint(most));
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const __half2 f = __float2half2_rn(sc[j] * r);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&xh[0][8 * j + c]), f);
-                        xh[0][8 * j + c] = *reinterpret_cast<const uint32_t *>(&v);
-                    }
-                }
-                float p[1][2][4];
-                block_products<1>(p, wa, wb, xh);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float s = sb * __shfl_sync(0xFFFFFFFFu, most, 8 * t + 4 * c);
-                    const int m = m0 + 2 * t + c;
-                    if (m < n) {
-                        const float f = s * L.weight[first + m];
-                        float *to = mine + L.token[first + m] * LD + g;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            to[16 * i] = fmaf(f, p[0][i][c], to[16 * i]);
-                            to[16 * i + 8] = fmaf(f, p[0][i][2 + c], to[16 * i + 8]);
-                        }
-                    }
-                }
-                __syncwarp();
-            }
-        }
-    }
-    launch_dependents();
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T * MOE_DOWN_COLS; i += MOE_THREADS) {
-        const int tok = i / MOE_DOWN_COLS, c = i % MOE_DOWN_COLS;
-        if (n0 + c >= a.H) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < MOE_WARPS; ++w) v += sums[(w * a.T + tok) * LD + c];
-        a.out[static_cast<int64_t>(tok) * a.H + n0 + c] = __float2bfloat16_rn(v);
-    }
 }
 
 }  // namespace bsfp8
