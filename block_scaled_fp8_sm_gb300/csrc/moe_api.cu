@@ -41,6 +41,19 @@ bool set_shared(const void *kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
+template <int MT>
+bool set_down_shared() {
+    return set_shared(reinterpret_cast<const void *>(bsfp8_moe_down<MT, 2>), moe_down_smem(MT)) &&
+           set_shared(reinterpret_cast<const void *>(bsfp8_moe_down<MT, 8>), moe_down_smem(MT));
+}
+
+template <int MT>
+int launch_down(const MoeArgs &a, cudaStream_t stream) {
+    return launch(a.T * a.top <= 64 ? bsfp8_moe_down<MT, 2> : bsfp8_moe_down<MT, 8>,
+                  dim3(static_cast<unsigned>((a.H + 16 * MT - 1) / (16 * MT))), MOE_DOWN_WARPS * 32, moe_down_smem(MT), 1, a,
+                  stream);
+}
+
 template <int NG>
 bool set_tile_shared() {
     return set_shared(reinterpret_cast<const void *>(bsfp8_moe_tile<false, NG>), MT_SMEM) &&
@@ -84,7 +97,9 @@ int moe_setup() {
         for (int type : {FP8_TYPE_F32, FP8_TYPE_BF16})
             if (!set_shared(reinterpret_cast<const void *>(pick_kernel(E, type)), route_smem(E))) return FP8_ERR_CUDA;
     return set_shared(reinterpret_cast<const void *>(bsfp8_route_order), route_smem(FP8_MAX_EXPERTS)) &&
-                   set_tile_shared<2>() && set_tile_shared<4>() && set_tile_shared<8>()
+                   set_shared(reinterpret_cast<const void *>(bsfp8_moe_up<2>), MOE_UP_SMEM) &&
+                   set_shared(reinterpret_cast<const void *>(bsfp8_moe_up<8>), MOE_UP_SMEM) && set_down_shared<1>() &&
+                   set_down_shared<2>() && set_down_shared<3>() && set_tile_shared<2>() && set_tile_shared<4>() && set_tile_shared<8>()
                ? FP8_OK
                : FP8_ERR_CUDA;
 }
@@ -210,12 +225,11 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
     const MoeArgs &few = a;
     const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(T * top));
     const bool two = T * top <= 64;   // words of pairs: two, or eight
-    rc = launch(two ? bsfp8_moe_up<2> : bsfp8_moe_up<8>, grid, MOE_THREADS, 0, 1, few, stream);
+    rc = launch(two ? bsfp8_moe_up<2> : bsfp8_moe_up<8>, grid, MOE_UP_WARPS * 32, MOE_UP_SMEM, 1, few, stream);
     if (rc != FP8_OK) return rc;
-    // one wave: four blocks of a warp on their way; more: three CTAs on an SM
-    const unsigned ctas = static_cast<unsigned>(H / MOE_DOWN_COLS);
-    const auto down = !two ? bsfp8_moe_down<2, 2, 8> : ctas <= 2u * d->sm_count ? bsfp8_moe_down<4, 2, 2> : bsfp8_moe_down<2, 3, 2>;
-    return launch(down, dim3(ctas), MOE_THREADS, 0, 1, few, stream);
+    // as many columns for a CTA as let one wave have all of them (one CTA on an SM), up to 48
+    const int64_t wide = (H / 16 + d->sm_count - 1) / d->sm_count;
+    return wide <= 1 ? launch_down<1>(few, stream) : wide == 2 ? launch_down<2>(few, stream) : launch_down<3>(few, stream);
 }
 
 }  // extern "C"

@@ -5,8 +5,9 @@
 //
 // Weights are E4M3 codes with a scale for each 128 x 128 block; x is bf16 and is not
 // quantized.  A few tokens leave the call bound by reading each busy expert's weights once
-// (3 I H bytes), so the weights go from global memory straight to registers, as in the rows
-// form of the products (block128_rows.cuh), and the arithmetic has to stay out of their way.
+// (3 I H bytes), so what counts is how many bytes are on their way: each thread copies the
+// 16-byte pieces that it will multiply to shared memory of its own, some K blocks ahead, and
+// takes them from there without a barrier (held in registers, one block ahead, 4.7 TB/s).
 //
 // Codes become fp16 by one conversion for two (every E4M3 value is an fp16 number), and
 // x, h become fp16 with one power of two for a token's 128 (x) or 16 (h) values, which
@@ -30,9 +31,8 @@ namespace bsfp8 {
 
 constexpr int MOE_FEW_TOKENS = 8;   // the kernels of this file; more: moe_tile.cuh
 constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 32, MOE_MAX_EXPERTS = 1024;
-constexpr int MOE_WARPS = 8, MOE_THREADS = MOE_WARPS * 32;
+constexpr int MOE_UP_WARPS = 8, MOE_DOWN_WARPS = 16;
 constexpr int MOE_UP_COLS = 16;     // columns of h per CTA: 16 gate and 16 up rows
-constexpr int MOE_DOWN_COLS = 16;   // columns of the output per CTA
 
 struct MoeArgs {
     const __nv_bfloat16 *x;   // [T, H]
@@ -165,16 +165,35 @@ __device__ __forceinline__ void load_ids(const MoeArgs &a, int (&own)[PW]) {
     for (int i = 0; i < PW; ++i) own[i] = 32 * i + lane < pairs ? a.ids[32 * i + lane] : -1;
 }
 
+// A thread's 16-byte pieces of a K block in shared memory: N of them, DEPTH blocks.
+template <int N, int DEPTH>
+struct MoeRing {
+    uint8_t *mine;
+    __device__ __forceinline__ explicit MoeRing(uint8_t *smem)
+        : mine(smem + (threadIdx.x >> 5) * (N * DEPTH * 512) + (threadIdx.x & 31) * 16) {}
+    // Zeros where there is nothing to copy.
+    __device__ __forceinline__ void copy(int slot, int i, const uint8_t *from, bool in) const {
+        cp_async_16(smem_u32(mine + (slot * N + i) * 512), from, in ? 16u : 0u);
+    }
+    __device__ __forceinline__ uint4 get(int slot, int i) const {
+        return *reinterpret_cast<const uint4 *>(mine + (slot * N + i) * 512);
+    }
+};
+
 // Gate and up: a CTA owns 16 columns of h of one expert, for all of its tokens.  The CTAs of
 // pair blockIdx.y do this where it is the first of all with its expert, and leave otherwise.
 // MMA piece i holds gate rows 8 i .. 8 i + 7 and the up rows of the same columns, so that a
-// thread has both numbers of an h.  A warp has the weights of its next block on their way
-// while it works on one.
+// thread has both numbers of an h.
+constexpr int MOE_UP_DEPTH = 3;
+constexpr int MOE_UP_SMEM = MOE_UP_WARPS * MOE_UP_DEPTH * 8 * 512;
+
 template <int PW>
-__global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_up(const MoeArgs a) {
-    __shared__ float red[MOE_WARPS][2][4][32];
+__global__ void __launch_bounds__(MOE_UP_WARPS * 32, 2) bsfp8_moe_up(const MoeArgs a) {
+    extern __shared__ __align__(16) uint8_t moe_smem[];
+    __shared__ float red[MOE_UP_WARPS][2][4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = static_cast<int>(blockIdx.x) * MOE_UP_COLS;
+    const MoeRing<8, MOE_UP_DEPTH> ring(moe_smem);
     wait_for_previous();
     int own[PW];
     load_ids<PW>(a, own);
@@ -183,18 +202,21 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_up(const MoeArgs a) 
     const int KB = (a.H + 127) / 128, NB = (2 * a.I + 127) / 128;
     const uint8_t *W = a.W1 + (static_cast<int64_t>(e) * 2 * a.I + n0 + g) * a.H + 16 * t;
     const int64_t up = static_cast<int64_t>(a.I) * a.H, eight = static_cast<int64_t>(8) * a.H;
-    uint4 wg[2][2], wu[2][2];
-    auto load = [&](int kb) {
+    auto fetch = [&](int slot, int kb) {
+        if (kb < KB) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = kb * 128 + 64 * j;
-            const bool in = k + 16 * t < a.H;
+            for (int j = 0; j < 2; ++j) {
+                const int k = kb * 128 + 64 * j;
+                const bool in = k + 16 * t < a.H;
+                const uint8_t *from = in ? W + k : W;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                wg[i][j] = load16_if(W + i * eight + k, in);
-                wu[i][j] = load16_if(W + up + i * eight + k, in);
+                for (int i = 0; i < 2; ++i) {
+                    ring.copy(slot, 4 * j + 2 * i, from + i * eight, in);
+                    ring.copy(slot, 4 * j + 2 * i + 1, from + up + i * eight, in);
+                }
             }
         }
+        cp_async_commit();
     };
     const MoePairs<PW> m = pairs_of<PW>(own, e);
     {   // an earlier pair has this expert: its CTAs do the work
@@ -206,42 +228,51 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_up(const MoeArgs a) 
         }
         if (earlier) return;
     }
-    if (warp < KB) load(warp);
-    const int pair = m.first(g, a.top);   // of this lane's token (none from T on)
-    const __nv_bfloat16 *x = a.x + static_cast<int64_t>(g) * a.H + 16 * t;
+#pragma unroll
+    for (int d = 0; d < MOE_UP_DEPTH; ++d) fetch(d, warp + d * MOE_UP_WARPS);
+    const bool has = m.first(g, a.top) >= 0;   // this lane's token (none from T on)
+    const __nv_bfloat16 *x = a.x + (has ? static_cast<int64_t>(g) * a.H + 16 * t : 0);
     const float *sg = a.s1 + (static_cast<int64_t>(e) * NB + n0 / 128) * KB;
     const float *su = a.s1 + (static_cast<int64_t>(e) * NB + (a.I + n0) / 128) * KB;
+    uint4 xr[4];
+    float s_gate = 0.0f, s_up = 0.0f;
+    auto load_x = [&](int kb) {   // and the block's scales
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int k = kb * 128 + 64 * (c >> 1);
+            xr[c] = load16_if(reinterpret_cast<const uint8_t *>(x + k + 8 * (c & 1)), has && k + 16 * t < a.H);
+        }
+        s_gate = sg[kb];
+        s_up = su[kb];
+    };
+    if (warp < KB) load_x(warp);
     float acc[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-    for (int kb = warp; kb < KB; kb += MOE_WARPS) {
-        uint4 xr[4], now[4][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = kb * 128 + 64 * j;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                xr[2 * j + c] = load16_if(reinterpret_cast<const uint8_t *>(x + k + 8 * c), k + 16 * t < a.H && pair >= 0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) now[2 * i][j] = wg[i][j], now[2 * i + 1][j] = wu[i][j];
-        }
-        const float s_gate = sg[kb], s_up = su[kb];
-        if (kb + MOE_WARPS < KB) load(kb + MOE_WARPS);
+    int slot = 0;
+    for (int kb = warp; kb < KB; kb += MOE_UP_WARPS) {
         uint32_t xh[16];
-        const float inverse = block_to_half(xr, xh);
+        const float inverse = block_to_half(xr, xh), gate = s_gate, upward = s_up;
+        if (kb + MOE_UP_WARPS < KB) load_x(kb + MOE_UP_WARPS);
         // columns 2 t and 2 t + 1: the tokens of lanes 8 t and 8 t + 4
         const float i0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * t), i1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * t + 4);
+        cp_async_wait_group<MOE_UP_DEPTH - 1>();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            uint4 wg[2], wu[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) wg[j] = ring.get(slot, 4 * j + 2 * i), wu[j] = ring.get(slot, 4 * j + 2 * i + 1);
             float p[4];
-            block_product(p, now[2 * i], now[2 * i + 1], xh);
-            acc[i][0] = fmaf(s_gate * i0, p[0], acc[i][0]);
-            acc[i][1] = fmaf(s_gate * i1, p[1], acc[i][1]);
-            acc[i][2] = fmaf(s_up * i0, p[2], acc[i][2]);
-            acc[i][3] = fmaf(s_up * i1, p[3], acc[i][3]);
+            block_product(p, wg, wu, xh);
+            acc[i][0] = fmaf(gate * i0, p[0], acc[i][0]);
+            acc[i][1] = fmaf(gate * i1, p[1], acc[i][1]);
+            acc[i][2] = fmaf(upward * i0, p[2], acc[i][2]);
+            acc[i][3] = fmaf(upward * i1, p[3], acc[i][3]);
         }
+        fetch(slot, kb + MOE_UP_DEPTH * MOE_UP_WARPS);
+        slot = slot + 1 == MOE_UP_DEPTH ? 0 : slot + 1;
     }
     launch_dependents();
 #pragma unroll
@@ -255,7 +286,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_up(const MoeArgs a) 
         const int piece = col >> 3, c = tok & 1, l = (col & 7) * 4 + (tok >> 1);
         float gate = 0.0f, upv = 0.0f;
 #pragma unroll
-        for (int w = 0; w < MOE_WARPS; ++w) {
+        for (int w = 0; w < MOE_UP_WARPS; ++w) {
             gate += red[w][piece][c][l];
             upv += red[w][piece][2 + c][l];
         }
@@ -273,23 +304,28 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) bsfp8_moe_up(const MoeArgs a) 
     }
 }
 
-// Down and the weighted sum: a CTA owns 16 columns of the output for all tokens and passes
-// over the busy experts in ascending order, U of a warp's blocks on their way.  Their weights
+// Down and the weighted sum: a CTA owns 16 MT columns of the output for all tokens and passes
+// over the busy experts in ascending order, DEPTH of a warp's blocks on their way.  Their weights
 // and the routing are not written by the up kernel, and what came before that had ended when
 // it let this kernel start: only h waits for it.
-template <int U, int CTAS, int PW>
-__global__ void __launch_bounds__(MOE_THREADS, CTAS) bsfp8_moe_down(const MoeArgs a) {
+__host__ __device__ constexpr int moe_down_depth(int MT) { return MT == 1 ? 4 : MT == 2 ? 3 : 2; }
+__host__ __device__ constexpr int moe_down_smem(int MT) { return MOE_DOWN_WARPS * moe_down_depth(MT) * 4 * MT * 512; }
+
+template <int MT, int PW>
+__global__ void __launch_bounds__(MOE_DOWN_WARPS * 32, 1) bsfp8_moe_down(const MoeArgs a) {
+    constexpr int DEPTH = moe_down_depth(MT);
+    extern __shared__ __align__(16) uint8_t moe_smem[];
     __shared__ uint32_t bits[MOE_MAX_EXPERTS / 32];
-    __shared__ float red[MOE_WARPS][4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int n0 = static_cast<int>(blockIdx.x) * MOE_DOWN_COLS;
+    const int n0 = static_cast<int>(blockIdx.x) * 16 * MT;
+    const MoeRing<4 * MT, DEPTH> ring(moe_smem);
     int own[PW];
     load_ids<PW>(a, own);
     if (threadIdx.x < MOE_MAX_EXPERTS / 32) bits[threadIdx.x] = 0u;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PW; ++i)
-        if (i % MOE_WARPS == warp && static_cast<uint32_t>(own[i]) < static_cast<uint32_t>(a.E))
+        if (i == warp && static_cast<uint32_t>(own[i]) < static_cast<uint32_t>(a.E))
             atomicOr(&bits[own[i] >> 5], 1u << (own[i] & 31));
     __syncthreads();
     const int KB = (a.I + 127) / 128, NB = (a.H + 127) / 128, chunks = a.I / 16;
@@ -297,7 +333,7 @@ __global__ void __launch_bounds__(MOE_THREADS, CTAS) bsfp8_moe_down(const MoeArg
     // K block kb of expert e belongs to warp (e KB + kb) mod warps; the warp's next one
     int e = -1, kb = KB;
     auto next = [&]() {
-        kb += MOE_WARPS;
+        kb += MOE_DOWN_WARPS;
         while (kb >= KB) {
             const uint32_t any = __ballot_sync(0xFFFFFFFFu, left != 0u);
             if (!any) return false;
@@ -305,99 +341,128 @@ __global__ void __launch_bounds__(MOE_THREADS, CTAS) bsfp8_moe_down(const MoeArg
             const uint32_t word = __shfl_sync(0xFFFFFFFFu, left, src);
             e = 32 * src + __ffs(word) - 1;
             if (lane == src) left &= left - 1u;
-            kb = (warp + MOE_WARPS - (e % MOE_WARPS) * (KB % MOE_WARPS) % MOE_WARPS) % MOE_WARPS;
+            kb = (warp + MOE_DOWN_WARPS - (e % MOE_DOWN_WARPS) * (KB % MOE_DOWN_WARPS) % MOE_DOWN_WARPS) % MOE_DOWN_WARPS;
         }
         return true;
     };
-    uint4 wa[U][2], wb[U][2];
-    float sb[U];
-    int es[U], ks[U];
-    auto load = [&](int u) {
+    int es[DEPTH], ks[DEPTH];   // the blocks on their way (-1: none)
+    auto fetch = [&](int u) {
         es[u] = next() ? e : -1;
         ks[u] = kb;
-        if (es[u] < 0) return;
-        const uint8_t *W = a.W2 + (static_cast<int64_t>(e) * a.H + n0 + g) * a.I + 16 * t;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = kb * 128 + 64 * j;
-            const bool in = k + 16 * t < a.I;
-            wa[u][j] = load16_if(W + k, in);
-            wb[u][j] = load16_if(W + static_cast<int64_t>(8) * a.I + k, in);
-        }
-        sb[u] = a.s2[(static_cast<int64_t>(e) * NB + n0 / 128) * KB + kb];
-    };
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        es[u] = -1;
-        if (u == 0 || es[u - 1] >= 0) load(u);
-    }
-    wait_for_previous();
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    while (es[0] >= 0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (es[u] < 0) break;
-            const uint32_t mine = pairs_of<PW>(own, es[u]).of(g, a.top);   // none from T on
-            const int64_t pair = mine ? g * a.top + __ffs(mine) - 1 : -1;
-            uint32_t xh[16];
-            float sc[2], w = 0.0f;
+        if (es[u] >= 0) {
+            const uint8_t *W = a.W2 + (static_cast<int64_t>(e) * a.H + n0 + g) * a.I + 16 * t;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int k = ks[u] * 128 + 64 * j + 16 * t;
-                const bool in = pair >= 0 && k < a.I;
-                const uint8_t *h = reinterpret_cast<const uint8_t *>(a.h + pair * a.I + k);
-                sc[j] = in ? a.hs[pair * chunks + k / 16] : 0.0f;
+                const int k = kb * 128 + 64 * j;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint4 v = load16_if(h + 16 * c, in);
-                    xh[8 * j + 4 * c] = v.x, xh[8 * j + 4 * c + 1] = v.y;
-                    xh[8 * j + 4 * c + 2] = v.z, xh[8 * j + 4 * c + 3] = v.w;
+                for (int i = 0; i < 2 * MT; ++i) {   // eight rows each
+                    const bool in = k + 16 * t < a.I && n0 + 8 * i < a.H;
+                    ring.copy(u, 2 * i + j, in ? W + static_cast<int64_t>(8 * i) * a.I + k : a.W2, in);
                 }
             }
-            // the sum of the token's weights for the expert
-            if (mine) w = a.w[pair];
-            for (uint32_t rest = mine & (mine - 1u); rest; rest &= rest - 1u) w += a.w[g * a.top + __ffs(rest) - 1];
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int u = 0; u < DEPTH; ++u) fetch(u);
+    uint4 hr[4];
+    float sc[2], w = 0.0f, sb[MT];
+    bool has = false;
+    auto load_h = [&](int u) {   // a token's values, their scales, its weight and the block's scales
+        if (es[u] < 0) return;
+        const uint32_t mine = pairs_of<PW>(own, es[u]).of(g, a.top);   // none from T on
+        has = mine != 0u;
+        const int64_t pair = has ? g * a.top + __ffs(mine) - 1 : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = ks[u] * 128 + 64 * j + 16 * t;
+            const bool in = has && k < a.I;
+            const uint8_t *h = reinterpret_cast<const uint8_t *>(a.h + pair * a.I + (in ? k : 0));
+            sc[j] = in ? a.hs[pair * chunks + k / 16] : 0.0f;
+            hr[2 * j] = load16_if(h, in);
+            hr[2 * j + 1] = load16_if(h + 16, in);
+        }
+        w = has ? a.w[pair] : 0.0f;   // and its other weights for the expert
+        for (uint32_t rest = mine & (mine - 1u); rest; rest &= rest - 1u) w += a.w[g * a.top + __ffs(rest) - 1];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            sb[i] = a.s2[(static_cast<int64_t>(es[u]) * NB + min((n0 + 16 * i) / 128, NB - 1)) * KB + ks[u]];
+    };
+    wait_for_previous();
+    load_h(0);
+    float acc[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    while (es[0] >= 0) {
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) {
+            if (es[u] < 0) break;
             // one scale for the block: the largest of its eight
             float most = fmaxf(fmaxf(sc[0], sc[1]), 0x1p-126f);
             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
             const float r = __uint_as_float((254u << 23) - __float_as_uint(most));
+            uint32_t xh[16];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const __half2 f = __float2half2_rn(sc[j] * r);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&xh[8 * j + c]), f);
-                    xh[8 * j + c] = *reinterpret_cast<const uint32_t *>(&v);
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t v[4] = {hr[2 * j + c].x, hr[2 * j + c].y, hr[2 * j + c].z, hr[2 * j + c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&v[k]), f);
+                        xh[8 * j + 4 * c + k] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
                 }
             }
-            float p[4];
-            block_product(p, wa[u], wb[u], xh);
-            const float s = sb[u];
+            float wt[2], f[2], s[MT];
+            bool hs[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float wt = __shfl_sync(0xFFFFFFFFu, w, 8 * t + 4 * c);
-                const float f = s * __shfl_sync(0xFFFFFFFFu, most, 8 * t + 4 * c);
-                const bool has = __shfl_sync(0xFFFFFFFFu, pair >= 0, 8 * t + 4 * c);
-                if (has) {   // (a token without the expert has nothing here, not zero times something)
-                    acc[c] = fmaf(wt, f * p[c], acc[c]);
-                    acc[2 + c] = fmaf(wt, f * p[2 + c], acc[2 + c]);
-                }
+                wt[c] = __shfl_sync(0xFFFFFFFFu, w, 8 * t + 4 * c);
+                f[c] = __shfl_sync(0xFFFFFFFFu, most, 8 * t + 4 * c);
+                hs[c] = __shfl_sync(0xFFFFFFFFu, has, 8 * t + 4 * c);
             }
-            load(u);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) s[i] = sb[i];
+            load_h((u + 1) % DEPTH);
+            cp_async_wait_group<DEPTH - 1>();
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                uint4 wa[2], wb[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) wa[j] = ring.get(u, 4 * i + j), wb[j] = ring.get(u, 4 * i + 2 + j);
+                float p[4];
+                block_product(p, wa, wb, xh);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (hs[c]) {   // (a token without the expert has nothing here, not zero times something)
+                        acc[i][c] = fmaf(wt[c], s[i] * f[c] * p[c], acc[i][c]);
+                        acc[i][2 + c] = fmaf(wt[c], s[i] * f[c] * p[2 + c], acc[i][2 + c]);
+                    }
+            }
+            fetch(u);
         }
     }
     launch_dependents();
+    cp_async_wait_all();
+    __syncthreads();   // the ring's memory is free
+    float *red = reinterpret_cast<float *>(moe_smem);   // [warps][MT][4][32]
 #pragma unroll
-    for (int c = 0; c < 4; ++c) red[warp][c][lane] = acc[c];
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) red[((warp * MT + i) * 4 + c) * 32 + lane] = acc[i][c];
     __syncthreads();
-    if (threadIdx.x < 128) {   // sixteen threads a token
-        const int col = lane & 15, tok = static_cast<int>(threadIdx.x) >> 4;
-        const int c = (col >> 3) * 2 + (tok & 1), l = (col & 7) * 4 + (tok >> 1);
+    for (int o = threadIdx.x; o < 8 * 16 * MT; o += MOE_DOWN_WARPS * 32) {
+        const int col = o % (16 * MT), tok = o / (16 * MT);
+        const int c = (col >> 3 & 1) * 2 + (tok & 1), l = (col & 7) * 4 + (tok >> 1);
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < MOE_WARPS; ++w) v += red[w][c][l];
-        if (tok < a.T) a.out[static_cast<int64_t>(tok) * a.H + n0 + col] = __float2bfloat16_rn(v);
+        for (int x = 0; x < MOE_DOWN_WARPS; ++x) v += red[((x * MT + (col >> 4)) * 4 + c) * 32 + l];
+        if (tok < a.T && n0 + col < a.H) a.out[static_cast<int64_t>(tok) * a.H + n0 + col] = __float2bfloat16_rn(v);
     }
 }
 
