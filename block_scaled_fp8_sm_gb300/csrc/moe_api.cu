@@ -218,6 +218,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
         a.counters = reinterpret_cast<int *>(rest + int64_t(2) * MT_CTAS * T * MT_ROWS * 4);
         a.status = d->status;
         a.wait_limit = wait_limit();
+        a.withhold = withheld_stage();
         return guarded([&] {
             return T <= 16 ? launch_tiles<2>(a, stream) : T <= 32 ? launch_tiles<4>(a, stream) : launch_tiles<8>(a, stream);
         });

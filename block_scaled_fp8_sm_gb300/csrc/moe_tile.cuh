@@ -59,6 +59,7 @@ struct MoeTileArgs : MoeArgs {
     uint32_t *status;
     long long wait_limit;
     int ring;                 // bytes of shared memory for the stages
+    int withhold;             // test hook: CTA 0 never loads this stage (-1: off)
 };
 
 // DOWN, NG: groups of eight tokens that an expert can have.
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
 
     if (warp == 0) {
         if (elect_one()) {
-            int it = 0, st = 0;
+            int it = 0, st = 0, withheld = -1;
             uint32_t ph = 1;
             bool ok = true;
             while (ok && walk.next(s)) {
@@ -323,10 +324,14 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 for (int kb = s.k0; kb < s.k1; ++kb) {
                     ok = wait_moe(&ctl->empty[st], ph, ctl, a);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&ctl->full[st], MT_A_BYTES);
-                    uint8_t *da = smem + st * stage_bytes;
-                    if constexpr (DOWN) tma_load_2d(&a.tmW, &ctl->full[st], da, kb * 128, e * a.H + s.c * MT_ROWS);
-                    else tma_load_4d(&a.tmW, &ctl->full[st], da, kb * 128, 0, 0, e * (a.I / 8) + s.c * 8);
+                    if (it == a.withhold && blockIdx.x == 0) {
+                        withheld = it;
+                    } else {
+                        mbar_arrive_expect_tx(&ctl->full[st], MT_A_BYTES);
+                        uint8_t *da = smem + st * stage_bytes;
+                        if constexpr (DOWN) tma_load_2d(&a.tmW, &ctl->full[st], da, kb * 128, e * a.H + s.c * MT_ROWS);
+                        else tma_load_4d(&a.tmW, &ctl->full[st], da, kb * 128, 0, 0, e * (a.I / 8) + s.c * 8);
+                    }
                     ++it;
                     if (++st == stages) {
                         st = 0;
@@ -338,6 +343,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
             // that ran out, the limit is the time that the loads get)
             const long long t0 = clock64();
             for (int d = max(0, it - stages); d < it; ++d) {
+                if (d == withheld) continue;
                 while (!mbar_try_wait(&ctl->full[d % stages], static_cast<uint32_t>(d / stages) & 1u))
                     if (clock64() - t0 > a.wait_limit) break;
             }

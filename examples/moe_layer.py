@@ -2,12 +2,13 @@
 
     python examples/moe_layer.py [--tokens 512] [--experts 32] [--top 4] [--hidden 2048] [--inner 1024]
 
-A router picks ``top`` experts for each token; the tokens' activations are quantized in
-expert order (a gather and a quantization in one pass), multiplied by each expert's
-gate and up weights, gated and quantized again, multiplied by its down weights, and
-summed per token with the router's weights.  The layer keeps its weights as E4M3 codes
-with 128 x 128 scales.  The result is compared with the same layer in fp32 on the same
-(dequantized) weights.
+A router picks ``top`` experts for each token and puts the rows in expert order.  Up to
+FP8_MOE_MAX_TOKENS tokens (a decoding step) go through the whole layer in one call, on
+unquantized activations.  More tokens' activations are quantized in expert order (a gather
+and a quantization in one pass), multiplied by each expert's gate and up weights, gated and
+quantized again, multiplied by its down weights, and summed per token with the router's
+weights.  The layer keeps its weights as E4M3 codes with 128 x 128 scales.  The result is
+compared with the same layer in fp32 on the same (dequantized) weights.
 """
 import argparse
 import os
@@ -53,31 +54,26 @@ class MoeLayer:
         self.down = pack_weight(torch.randn(experts, hidden, inner, generator=g, device=device) * inner ** -0.5)
 
     def route(self, x):
-        """(weights [T, top], token of each row in expert order, offsets [E + 1], order)."""
-        w, e = torch.softmax(x.float() @ self.router.T, dim=1).topk(self.top, dim=1)
-        order = torch.sort(e.flatten(), stable=True).indices
-        rows = torch.zeros(self.experts, dtype=torch.int32, device=x.device)
-        rows.scatter_add_(0, e.flatten(), torch.ones_like(e.flatten(), dtype=torch.int32))
-        offsets = torch.zeros(self.experts + 1, dtype=torch.int32, device=x.device)
-        torch.cumsum(rows, 0, dtype=torch.int32, out=offsets[1:])
-        return w / w.sum(1, keepdim=True), (order // self.top).to(torch.int32), offsets, order
+        """(weights [T, top], ids [T, top], offsets [E + 1], token of each row in expert
+        order, places [T, top] of the tokens' rows there)."""
+        return bs.fp8_moe_route(x.float() @ self.router.T, self.top)
 
     def forward(self, x):
         T, hidden = x.shape
-        w, token, offsets, order = self.route(x)
+        w, ids, offsets, token, places = self.route(x)
+        if T <= bs.FP8_MOE_MAX_TOKENS:
+            return bs.fp8_moe_layer(x, w, ids, *self.gate_up, *self.down)
         A, sA = bs.fp8_quantize_tokens(x, rows=token)
         h = torch.empty(T * self.top, self.gate_up[0].shape[1], dtype=torch.bfloat16, device=x.device)
         bs.fp8_gemm_experts(A, sA, *self.gate_up, h, offsets)
         A, sA = bs.fp8_swiglu_quantize_tokens(h)
         y = torch.empty(T * self.top, hidden, dtype=torch.bfloat16, device=x.device)
         bs.fp8_gemm_experts(A, sA, *self.down, y, offsets)
-        out = torch.empty_like(y)
-        out[order] = y   # back to token order: each row has its own place
-        return (out.view(T, self.top, hidden).float() * w[:, :, None]).sum(1).to(torch.bfloat16)
+        return (y[places.long()].float() * w[:, :, None]).sum(1).to(torch.bfloat16)
 
     def reference(self, x):
         """The same layer in fp32 (the same routing and dequantized weights, no FP8 activations)."""
-        w, token, offsets, order = self.route(x)
+        w, _, offsets, token, places = self.route(x)
         ends = offsets.tolist()
         rows = x.float()[token.long()]
         y = torch.empty(rows.shape, device=x.device)
@@ -85,9 +81,7 @@ class MoeLayer:
         for e, (a, b) in enumerate(zip(ends, ends[1:])):
             gate, up = (rows[a:b] @ up_w[e].T).chunk(2, dim=1)
             y[a:b] = (torch.nn.functional.silu(gate) * up) @ down_w[e].T
-        out = torch.empty_like(y)
-        out[order] = y
-        return (out.view(x.shape[0], self.top, -1) * w[:, :, None]).sum(1)
+        return (y[places.long()] * w[:, :, None]).sum(1)
 
 
 def main():

@@ -2,6 +2,7 @@
 and how their kernels read memory."""
 import os
 import re
+import types
 
 import pytest
 import torch
@@ -110,7 +111,74 @@ def test_python_layer_refusals():
         bs.fp8_moe_layer(*args)
 
 
-@pytest.mark.parametrize("name", ["moe_layer.cuh", "moe_route.cuh", "moe_api.cu", "epilogue.cuh", "host.h"])
+class On:
+    """A tensor that says it is on CUDA device `device` (no second device is needed)."""
+    is_cuda = True
+
+    def __init__(self, t, device):
+        self._t, self._device = t, device
+        self.shape, self.dtype, self.device = t.shape, t.dtype, torch.device("cuda", device)
+
+    def get_device(self):
+        return self._device
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(list of launches, setter of the current device)"""
+    made, current = [], [0]
+    launch = lambda *a: made.append(a) or 0   # noqa: E731
+    fake = types.SimpleNamespace(codes=frozenset((torch.uint8, torch.float8_e4m3fn)), f32=F, bf16=H, i32=I32,
+                                 floats=frozenset((F, H)), stream=lambda dev: 1000 + dev, device=lambda: current[0],
+                                 fused=launch, route=launch, layer=launch)
+    monkeypatch.setattr(bs._Calls, "loaded", fake)
+    return made, lambda d: current.__setitem__(0, d)
+
+
+def fused(A, sA, B, sB, C, bias, R):
+    return bs.fp8_gemm_block128_fused(A, sA, B, sB, C, bias=bias, residual=R)
+
+
+def route(logits, weights, ids, offsets, rows, places, space):
+    return bs.fp8_moe_route(logits, 2, out=(weights, ids, offsets, rows, places), workspace=space)
+
+
+CALLS = {
+    "fused": (fused, (z(4, 256), z(4, 2, dtype=F), z(136, 256), z(2, 2, dtype=F), z(4, 136, dtype=H), z(136, dtype=F),
+                      z(4, 136, dtype=H))),
+    "route": (route, (z(4, 64, dtype=F), z(4, 2, dtype=F), z(4, 2, dtype=I32), z(65, dtype=I32), z(8, dtype=I32),
+                      z(4, 2, dtype=I32), z(64))),
+    "layer": (bs.fp8_moe_layer, (z(4, 256, dtype=H), z(4, 2, dtype=F), z(4, 2, dtype=I32), z(3, 160, 256),
+                                 z(3, 2, 2, dtype=F), z(3, 256, 80), z(3, 2, 1, dtype=F), z(4, 256, dtype=H), z(4096))),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_other_devices_are_refused(calls, name):
+    made, set_current = calls
+    call, args = CALLS[name]
+
+    def run(device, odd=None, odd_device=None):
+        return call(*[On(t, odd_device if i == odd else device) for i, t in enumerate(args)])
+
+    run(0)
+    assert len(made) == 1 and made[0][-1] == 1000   # the stream of the current device
+    for odd in range(len(args)):   # one tensor elsewhere
+        for device, elsewhere in ((0, 1), (1, 0)):
+            with pytest.raises(ValueError, match="device"):
+                run(device, odd, elsewhere)
+    with pytest.raises(ValueError, match="current device 0"):
+        run(1)
+    assert len(made) == 1, "a call with tensors of another device was launched"
+    set_current(1)
+    run(1)
+    assert len(made) == 2 and made[1][-1] == 1001
+
+
+@pytest.mark.parametrize("name", ["moe_layer.cuh", "moe_tile.cuh", "moe_route.cuh", "moe_api.cu", "epilogue.cuh", "host.h"])
 def test_no_noncoherent_load(name):
     """Kernels that may start while the one before still writes read with ordinary loads."""
     with open(os.path.join(CSRC, name), encoding="utf-8") as f:

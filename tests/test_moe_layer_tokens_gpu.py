@@ -190,3 +190,59 @@ def test_reference_values_of_the_weights():
     want = v * torch.sigmoid(v) * v
     assert bool(((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want.abs() + 2.0 ** -30).all())
     assert torch.equal(values(eye, s[0], 128), torch.eye(H, dtype=torch.float64, device="cuda"))
+
+
+@pytest.mark.parametrize("T,stage", [(12, 0), (12, 3), (40, 1)])
+def test_withheld_stage_times_out_cleanly(T, stage):
+    """Waits that run out are reported, the kernels return, and the next call is right."""
+    layer = _moe.Layer(4, 2064, 1040, 6)
+    x, w, ids = _moe.inputs(T, 3, 4, 2064, 7)
+    space = torch.empty(bs.fp8_moe_layer_workspace_bytes(T, 3, 1040), dtype=torch.uint8, device="cuda")
+    assert bs.fp8_status_query() == 0
+    bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 20_000_000)   # ~10 ms
+    bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, stage)
+    try:
+        bs.fp8_moe_layer(x, w, ids, *layer.weights, workspace=space)
+        torch.cuda.synchronize()
+        assert bs.fp8_status_query() == bs._abi.FP8_ERR_TIMEOUT
+    finally:
+        bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, -1)
+        bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 0)
+    compare(bs.fp8_moe_layer(x, w, ids, *layer.weights, workspace=space), *layer.reference(x, w, ids))
+    assert bs.fp8_status_query() == 0
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("name", ["layer", "route"])
+def test_outputs_belong_to_the_stream_that_writes_them(name, handle):
+    """Memory freed on the current stream may still be in use by its queued work: a call on
+    another stream must not be given it."""
+    layer = _moe.Layer(4, 1024, 512, 6)
+    x, w, ids = _moe.inputs(64, 2, 4, 1024, 7)
+    logits = torch.randn(2048, 256, device="cuda")
+
+    def call(stream=None):
+        if name == "layer":
+            return bs.fp8_moe_layer(x, w, ids, *layer.weights, stream=stream)
+        return bs.fp8_moe_route(logits, 8, order=False, stream=stream)[1]
+    first = call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    where = first.data_ptr()
+    want = first.clone()
+    del first
+    got = call(side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert got.data_ptr() != where and torch.equal(got, want)
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    layer = _moe.Layer(8, 1040, 528, 6)
+    sets = [_moe.inputs(T, 3, 8, 1040, T) for T in (8, 30, 64, 17)]
+    want = [bs.fp8_moe_layer(*s, *layer.weights) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [bs.fp8_moe_layer(*s, *layer.weights, stream=t) for s, t in zip(sets, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
