@@ -172,7 +172,7 @@ int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E
 int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I) {
     if (!layer_sizes(T, top, I)) return 0;
     const int64_t h = T * top * (2 * I + I / 4);
-    return T <= MOE_FEW_TOKENS ? h : (h + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + MT_CTAS * 4;
+    return T <= MOE_FEW_TOKENS ? h : (h + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + 2 * MT_CTAS * 8 + MT_CTAS * 4;
 }
 
 int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
@@ -215,7 +215,9 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
     if (T > MOE_FEW_TOKENS) {
         uint8_t *rest = static_cast<uint8_t *>(workspace) + (T * top * (2 * I + I / 4) + 255) / 256 * 256;
         a.part = reinterpret_cast<float *>(rest);
-        a.counters = reinterpret_cast<int *>(rest + int64_t(2) * MT_CTAS * T * MT_ROWS * 4);
+        rest += int64_t(2) * MT_CTAS * T * MT_ROWS * 4;
+        a.has = reinterpret_cast<unsigned long long *>(rest);
+        a.counters = reinterpret_cast<int *>(rest + 2 * MT_CTAS * 8);
         a.status = d->status;
         a.wait_limit = wait_limit();
         a.withhold = withheld_stage();

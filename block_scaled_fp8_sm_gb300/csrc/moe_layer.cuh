@@ -519,6 +519,8 @@ __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l)
     const int lane = threadIdx.x & 31, threads = blockDim.x, pairs = a.T * a.top;
     constexpr uint16_t NONE = 0xFFFF;
     for (int i = threadIdx.x; i <= a.E; i += threads) l.start[i] = 0;
+    // the thread's first pair's weight is on its way meanwhile
+    const float w0 = threadIdx.x < pairs ? a.w[threadIdx.x] : 0.0f;
     for (int p = threadIdx.x; p < pairs; p += threads) {
         const uint32_t e = static_cast<uint32_t>(a.ids[p]);
         l.id[p] = e < static_cast<uint32_t>(a.E) ? static_cast<uint16_t>(e) : NONE;
@@ -559,7 +561,7 @@ __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l)
     for (int p = threadIdx.x; p < pairs; p += threads) {
         if (l.number[p] == 255) continue;
         const int e = l.id[p], t = p / a.top, at = l.start[e] + l.number[p];
-        float w = a.w[p];
+        float w = p < threads ? w0 : a.w[p];
         for (int q = p + 1; q < (t + 1) * a.top; ++q)
             if (l.id[q] == e) w += a.w[q];
         l.pair[at] = static_cast<uint16_t>(p);

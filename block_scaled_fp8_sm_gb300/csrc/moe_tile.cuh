@@ -54,7 +54,8 @@ __device__ __forceinline__ void tma_load_4d(const CUtensorMap *m, uint64_t *bar,
 
 struct MoeTileArgs : MoeArgs {
     CUtensorMap tmW;
-    float *part;              // [2 MT_CTAS][T][256]: sums of the tiles that a cut goes through
+    float *part;              // [2 MT_CTAS][T][256]: sums of the tiles that a cut goes through,
+    unsigned long long *has;  // [2 MT_CTAS] which tokens a part has: only their rows are there
     int *counters;            // [MT_CTAS]: parts of the tile that starts in this CTA and goes on
     uint32_t *status;
     long long wait_limit;
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                         if (c * MT_ROWS + row < a.H)
                             a.out[static_cast<int64_t>(t) * a.H + c * MT_ROWS + row] = __float2bfloat16_rn(0.0f);
             for (int t = 0; t < a.T; ++t) ctl->sums[t][row] = 0.0f;
+            unsigned long long touched = 0ull;   // tokens that the sums hold something of
             MoeSeg ahead;   // the next segment, whose first scales are on their way
             const float *sw = a.s2;
             float scales = 0.0f;
@@ -589,6 +591,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                         }
                     }
                 }
+                for (int m = lane; m < n; m += 32) touched |= 1ull << L.token[first + m];
                 if (!s.end && more) continue;
                 // the tile's end, or this CTA's.  A warp whose waits ran out comes here, too, so
                 // that the others do not wait for it
@@ -599,18 +602,26 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 const int a0 = static_cast<int>(((t0 + 1) * G - 1) / all), a1 = static_cast<int>((t1 * G - 1) / all);
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == a0 ? 1 : 0);
                 // from here on a warp has a token's row, a lane eight of its columns (four and four)
+                const unsigned long long tokens =
+                    static_cast<unsigned long long>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(touched >> 32))) << 32 |
+                    __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(touched));
+                touched = 0ull;
                 const int n0 = s.c * MT_ROWS + 4 * lane;
                 float4 *sums = reinterpret_cast<float4 *>(&ctl->sums[0][4 * lane]);
                 float4 *parts = reinterpret_cast<float4 *>(a.part + 4 * lane);
                 constexpr int LD = MT_ROWS / 4;   // 16-byte pieces of a row
-                for (int t = warp - 4; t < a.T; t += MT_EPI_WARPS)
+                for (int t = warp - 4; t < a.T; t += MT_EPI_WARPS) {
+                    const bool there = tokens >> t & 1ull;
+                    if (part && !there) continue;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float4 v = sums[t * LD + 32 * h];
-                        sums[t * LD + 32 * h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (there) sums[t * LD + 32 * h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (part) parts[(slot * a.T + t) * LD + 32 * h] = v;
                         else if (n0 + 128 * h < a.H) store_bf16x4(a.out + static_cast<int64_t>(t) * a.H + n0 + 128 * h, v);
                     }
+                }
+                if (part && warp == 4 && lane == 0) a.has[slot] = tokens;
                 if (part) __threadfence();
                 named_bar_sync(1, 256);
                 if (!part) continue;
@@ -620,32 +631,34 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 named_bar_sync(1, 256);
                 if (!last) continue;
                 __threadfence();
-                // two tokens and four parts at a time are on their way
-                for (int t = warp - 4; t < a.T; t += 2 * MT_EPI_WARPS) {
-                    float4 v[4];
+                // a warp for a token: the parts that have it, in order, four at a time on their way
+                for (int t = warp - 4; t < a.T; t += MT_EPI_WARPS) {
+                    float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+                    for (int i0 = a0; i0 <= a1; i0 += 32) {
+                        const int i = i0 + lane;
+                        uint32_t left = __ballot_sync(0xFFFFFFFFu, i <= a1 && (__ldcg(a.has + 2 * min(i, a1) + (i == a0 ? 1 : 0)) >> t & 1ull));
+                        while (left) {
+                            float4 w[4][2];
+                            bool any[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    const int u1 = min(t + MT_EPI_WARPS, a.T - 1);
-                    for (int i = a0; i <= a1; i += 4) {
-                        float4 w[4][4];
+                            for (int x = 0; x < 4; ++x) {
+                                any[x] = left != 0u;
+                                const int from = i0 + (any[x] ? __ffs(left) - 1 : 0);
+                                left &= left - 1u;
+                                const float4 *at = parts + ((static_cast<int64_t>(from) * 2 + (from == a0 ? 1 : 0)) * a.T + t) * LD;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int from = min(i + x, a1);
-                            const float4 *at = parts + (static_cast<int64_t>(from) * 2 + (from == a0 ? 1 : 0)) * a.T * LD;
+                                for (int h = 0; h < 2; ++h) w[x][h] = any[x] ? __ldcg(at + 32 * h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) w[x][k] = __ldcg(at + (k >> 1 ? u1 : t) * LD + 32 * (k & 1));
+                            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    v[h].x += w[x][h].x, v[h].y += w[x][h].y, v[h].z += w[x][h].z, v[h].w += w[x][h].w;
                         }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (i + x <= a1)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) v[k].x += w[x][k].x, v[k].y += w[x][k].y, v[k].z += w[x][k].z, v[k].w += w[x][k].w;
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int u = t + (k >> 1) * MT_EPI_WARPS, c = n0 + 128 * (k & 1);
-                        if (u < a.T && c < a.H) store_bf16x4(a.out + static_cast<int64_t>(u) * a.H + c, v[k]);
-                    }
+                    for (int h = 0; h < 2; ++h)
+                        if (n0 + 128 * h < a.H) store_bf16x4(a.out + static_cast<int64_t>(t) * a.H + n0 + 128 * h, v[h]);
                 }
             }
         }
