@@ -476,13 +476,14 @@ struct MoeLists {
     uint16_t *token;     // [pairs]
     float *weight;       // [pairs] the sum of the token's weights for the expert
     uint16_t *id;        // [pairs] while the lists are made: the pairs' experts,
-    uint8_t *number;     // [pairs] and their numbers among the expert's
+    uint8_t *number;     // [pairs] and their numbers among the expert's,
+    int *count;          // [E] which has so many
 };
 
 __host__ __device__ constexpr int moe_pad16(int v) { return (v + 15) / 16 * 16; }
 
 struct MoeListsLayout {
-    int start, busy, pair, token, weight, id, number, bytes;   // offsets
+    int start, busy, pair, token, weight, id, number, count, bytes;   // offsets
 };
 
 __host__ __device__ inline MoeListsLayout moe_lists_layout(int T, int top, int E) {
@@ -494,7 +495,8 @@ __host__ __device__ inline MoeListsLayout moe_lists_layout(int T, int top, int E
     s.weight = s.token + moe_pad16(2 * T * top);
     s.id = s.weight + moe_pad16(4 * T * top);
     s.number = s.id + moe_pad16(2 * T * top);
-    s.bytes = s.number + moe_pad16(T * top);
+    s.count = s.number + moe_pad16(T * top);
+    s.bytes = s.count + moe_pad16(4 * E);
     return s;
 }
 
@@ -509,6 +511,7 @@ __device__ __forceinline__ MoeLists moe_lists(uint8_t *at, int T, int top, int E
     l.weight = reinterpret_cast<float *>(at + o.weight);
     l.id = reinterpret_cast<uint16_t *>(at + o.id);
     l.number = at + o.number;
+    l.count = reinterpret_cast<int *>(at + o.count);
     return l;
 }
 
@@ -518,50 +521,63 @@ __device__ __forceinline__ MoeLists moe_lists(uint8_t *at, int T, int top, int E
 __device__ __forceinline__ void build_lists(const MoeArgs &a, const MoeLists &l) {
     const int lane = threadIdx.x & 31, threads = blockDim.x, pairs = a.T * a.top;
     constexpr uint16_t NONE = 0xFFFF;
-    for (int i = threadIdx.x; i <= a.E; i += threads) l.start[i] = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.E; i += threads) l.count[i] = 0;
+    if (threadIdx.x == 0) l.start[0] = 0;
     // the thread's first pair's weight is on its way meanwhile
     const float w0 = threadIdx.x < pairs ? a.w[threadIdx.x] : 0.0f;
+#pragma unroll 1
     for (int p = threadIdx.x; p < pairs; p += threads) {
         const uint32_t e = static_cast<uint32_t>(a.ids[p]);
         l.id[p] = e < static_cast<uint32_t>(a.E) ? static_cast<uint16_t>(e) : NONE;
     }
     __syncthreads();
+#pragma unroll 1
     for (int p = threadIdx.x; p < pairs; p += threads) {
         const uint16_t e = l.id[p];
         bool first = e != NONE;
+#pragma unroll 1
         for (int q = p - p % a.top; q < p; ++q) first &= l.id[q] != e;
-        l.number[p] = first ? static_cast<uint8_t>(atomicAdd(&l.start[e], 1)) : 255;
+        l.number[p] = first ? static_cast<uint8_t>(atomicAdd(&l.count[e], 1)) : 255;
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
+    // a warp for 32 experts adds up those before them by itself
+#pragma unroll 1
+    for (int e0 = threadIdx.x & ~31; e0 < a.E; e0 += threads) {
         int base = 0, used = 0, most = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane, c = e < a.E ? l.start[e] : 0;
+#pragma unroll 1
+        for (int e = lane; e < e0; e += 32) {
+            const int c = l.count[e];
+            base += c;
+            used += c > 0;
             most = max(most, c);
-            int sum = c;
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, k);
-                if (lane >= k) sum += v;
-            }
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, c > 0);
-            if (e < a.E) l.start[e] = base + sum - c;
-            if (c > 0) l.busy[used + __popc(mask & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
-            base += __shfl_sync(0xFFFFFFFFu, sum, 31);
-            used += __popc(mask);
         }
+        const int e = e0 + lane, c = e < a.E ? l.count[e] : 0;
+        most = max(most, c);
+        base = __reduce_add_sync(0xFFFFFFFFu, base);
+        used = __reduce_add_sync(0xFFFFFFFFu, used);
+        int sum = base + c;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, k) - base;
+            if (lane >= k) sum += v;
+        }
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, c > 0);
+        if (e < a.E) l.start[e + 1] = sum;
+        if (c > 0) l.busy[used + __popc(mask & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
         most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if (lane == 0) {
-            l.experts[0] = used;
+        if (e == a.E - 1) {
+            l.experts[0] = used + __popc(mask);
             l.experts[1] = most;
-            l.start[a.E] = base;
         }
     }
     __syncthreads();
+#pragma unroll 1
     for (int p = threadIdx.x; p < pairs; p += threads) {
         if (l.number[p] == 255) continue;
         const int e = l.id[p], t = p / a.top, at = l.start[e] + l.number[p];
         float w = p < threads ? w0 : a.w[p];
+#pragma unroll 1
         for (int q = p + 1; q < (t + 1) * a.top; ++q)
             if (l.id[q] == e) w += a.w[q];
         l.pair[at] = static_cast<uint16_t>(p);
