@@ -90,6 +90,23 @@ bool layer_sizes(int64_t T, int32_t top, int64_t I) {
     return T >= 0 && T <= FP8_MOE_MAX_TOKENS && top >= 1 && top <= FP8_MAX_TOP && I >= 0 && I < kLim && I % 16 == 0;
 }
 
+// Whether the tile form (moe_tile.cuh) serves the call, else the one for few tokens
+// (moe_layer.cuh), whose set-up is some 12 us shorter and whose rate falls as the tokens grow.  By
+// the weights that even routing reads; few-token form against tiles, us (hidden x inner):
+//   4 tokens up from 90 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 14.6, 20.1; 8 of them (66)
+//     18.1, 20.5; 4, 8 of 256 of 2048 x 512 (96) 27.7, 25.9; 8 of them (181) 49.2, 42.6; 8, 2 of 8
+//     of 4096 x 14336 (1270) 225, 191; 8, 8 of 64 of 7168 x 2048 (1850) 289, 274
+//   fewer from 400 MB: 1, 4 of 32 of 2048 x 1024 (25) 8.5, 19.5; 2, 8 of 64 of 4096 x 1536 (283)
+//     55.0, 57.7; 1, 8 of 64 of 7168 x 2048 (352) 64.0, 66.0; 3, 1 of 8 of 4096 x 14336 (465) 98.8,
+//     91.9; 2, 8 of 64 of 7168 x 2048 (660) 116.5, 115.4
+bool takes_tiles(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
+    if (T > MOE_FEW_TOKENS) return true;
+    double without = 1.0;   // an expert without tokens, when routing is even
+    for (int64_t t = 0; t < T; ++t) without *= 1.0 - static_cast<double>(top < E ? top : E) / E;
+    const double bytes = (1.0 - without) * E * 3.0 * static_cast<double>(H) * static_cast<double>(I);
+    return bytes >= (T < 4 ? 400e6 : 90e6);
+}
+
 }  // namespace
 
 int moe_setup() {
@@ -99,7 +116,7 @@ int moe_setup() {
     return set_shared(reinterpret_cast<const void *>(bsfp8_route_order), route_smem(FP8_MAX_EXPERTS)) &&
                    set_shared(reinterpret_cast<const void *>(bsfp8_moe_up<2>), MOE_UP_SMEM) &&
                    set_shared(reinterpret_cast<const void *>(bsfp8_moe_up<8>), MOE_UP_SMEM) && set_down_shared<1>() &&
-                   set_down_shared<2>() && set_down_shared<3>() && set_tile_shared<2>() && set_tile_shared<4>() && set_tile_shared<8>()
+                   set_down_shared<2>() && set_down_shared<3>() && set_tile_shared<1>() && set_tile_shared<2>() && set_tile_shared<4>() && set_tile_shared<8>()
                ? FP8_OK
                : FP8_ERR_CUDA;
 }
@@ -171,8 +188,7 @@ int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E
 
 int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I) {
     if (!layer_sizes(T, top, I)) return 0;
-    const int64_t h = T * top * (2 * I + I / 4);
-    return T <= MOE_FEW_TOKENS ? h : (h + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + 2 * MT_CTAS * 8 + MT_CTAS * 4;
+    return (T * top * (2 * I + I / 4) + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + 2 * MT_CTAS * 8 + MT_CTAS * 4;
 }
 
 int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
@@ -212,7 +228,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
     a.E = E;
     a.H = static_cast<int>(H);
     a.I = static_cast<int>(I);
-    if (T > MOE_FEW_TOKENS) {
+    if (takes_tiles(T, top, E, H, I)) {
         uint8_t *rest = static_cast<uint8_t *>(workspace) + (T * top * (2 * I + I / 4) + 255) / 256 * 256;
         a.part = reinterpret_cast<float *>(rest);
         rest += int64_t(2) * MT_CTAS * T * MT_ROWS * 4;
@@ -222,7 +238,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
         a.wait_limit = wait_limit();
         a.withhold = withheld_stage();
         return guarded([&] {
-            return T <= 16 ? launch_tiles<2>(a, stream) : T <= 32 ? launch_tiles<4>(a, stream) : launch_tiles<8>(a, stream);
+            return T <= 8 ? launch_tiles<1>(a, stream) : T <= 16 ? launch_tiles<2>(a, stream) : T <= 32 ? launch_tiles<4>(a, stream) : launch_tiles<8>(a, stream);
         });
     }
     const MoeArgs &few = a;

@@ -466,8 +466,8 @@ int64_t fp8_moe_route_workspace_bytes(int64_t T, int32_t E, int32_t top);
  *        names twice counts with the sum of its weights.
  * The products' sums, the gated activation and the weighted sum are fp32; between the two
  * products the activation is held in 11 bits (fp16 with a power-of-two scale for 16 values).
- * The sums' order is fixed: calls repeat bit for bit.  Up to 8 tokens a token's result
- * does not depend on the other tokens of the call; with more, its last bits may.
+ * The sums' order is fixed: calls repeat bit for bit.  A token's last bits may depend on
+ * the other tokens of the call and on how many there are.
  * Values below 2^-14 of the largest of the 128 around them (k / 128) lose bits: what is
  * lost is at most 2^-22 of that largest value.
  * T <= FP8_MOE_MAX_TOKENS (more: fp8_quantize_tokens, fp8_gemm_experts and

@@ -48,7 +48,7 @@ def test_route_refusals(lib):
 def test_layer_refusals(lib):
     def call(**kw):
         a = dict(x=16, w=16, ids=16, W1=16, s1=16, W2=16, s2=16, out=16, T=8, top=4, E=32, H=256, I=128, space=16,
-                 bytes=1 << 20)
+                 bytes=1 << 23)
         a.update(kw)
         return lib.fp8_moe_layer(a["x"], a["w"], a["ids"], a["W1"], a["s1"], a["W2"], a["s2"], a["out"], a["T"],
                                  a["top"], a["E"], a["H"], a["I"], a["space"], a["bytes"], None)
@@ -60,7 +60,7 @@ def test_layer_refusals(lib):
         wide = name in ("x", "W1", "W2", "out", "space")
         assert call(**{name: 8 if wide else 18}) == _abi.FP8_ERR_ALIGN, name
     assert call(T=0) == _abi.FP8_OK and call(H=0) == _abi.FP8_OK
-    assert bs.fp8_moe_layer_workspace_bytes(8, 4, 128) == 8 * 4 * (256 + 32)
+    assert bs.fp8_moe_layer_workspace_bytes(8, 4, 128) >= 8 * 4 * (256 + 32)   # h and its scales, and more
     for bad in ((65, 4, 128), (8, 0, 128), (8, 4, 24), (-1, 4, 128)):
         assert bs.fp8_moe_layer_workspace_bytes(*bad) == 0
 

@@ -55,6 +55,25 @@ def test_padding_and_repeated_experts(T):
     assert not out[0].any()
 
 
+# weights that tiles read faster, however few the tokens are
+@pytest.mark.parametrize("T,top,E,H,I", [(1, 32, 32, 2064, 2064), (4, 8, 9, 2064, 2032), (7, 3, 24, 2048, 1296)])
+def test_few_tokens_of_large_weights(T, top, E, H, I):   # noqa: E741
+    layer = _moe.Layer(E, H, I, T + H)
+    x, w, ids = _moe.inputs(T, top, E, H, I)
+    if T > 1:
+        ids[0] = -1                                      # a token without any expert
+        ids[1, 1:] = ids[1, 0]                           # one expert only, several times
+        ids[2, 0] = E
+    out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    bs.fp8_moe_layer(x, w, ids, *layer.weights, out)
+    ref, bound = layer.reference(x, w, ids)
+    compare(out, ref, bound, f"{T} {top} {E} {H} {I}")
+    for _ in range(5):
+        assert torch.equal(bs.fp8_moe_layer(x, w, ids, *layer.weights), out)
+    bs.fp8_moe_layer(x, w, torch.full_like(ids, -1), *layer.weights, out)
+    assert not out.any()
+
+
 def test_no_expert_at_all():
     layer = _moe.Layer(3, 64, 32, 1)
     x, w, ids = _moe.inputs(5, 2, 3, 64, 1)
