@@ -1,5 +1,6 @@
-// moe_tile.cuh -- the mixture-of-experts layer of moe_layer.cuh for more than eight tokens,
-// on the tensor cores (tcgen05): the weights come by TMA and are never touched by a register.
+// moe_tile.cuh -- the mixture-of-experts layer of moe_layer.cuh for more than eight tokens, or
+// fewer with large weights, on the tensor cores (tcgen05): the weights come by TMA and are never
+// touched by a register.
 //
 // A weight tile's 256 rows are the M side of two MMAs, an expert's tokens their N side, in
 // E4M3: a number v of the activations becomes two (x) or three (h) codes,
@@ -12,6 +13,16 @@
 //
 // The call is bound by the weights' bytes as long as every role keeps a K block (32 KB, 1430
 // cycles of an SM's share of HBM) under that, each of them a chain of dependent instructions.
+// 8 of 64 experts of 7168 x 2048: 16 tokens 352 us (6.9 TB/s), 32 tokens 409, 64 tokens 464 (6.1
+// TB/s of 6.8: the makers' and the epilogue's 64 columns).  64 tokens before: mma.sync with the
+// weights through registers 992, tiles of 128 rows 523 (an MMA costs ~60 cycles for its A side
+// whatever N is, a TMA request ~70 of its thread), 256 481, an expert's K blocks walked without
+// divisions and several parts of a cut tile on their way 465.  Small weights pay the set-up:
+// 19 tokens, 3 of 16 of 2064 x 1040 (98 MB) 33 us, of which 1.5 to 2 are the lists, 3 the change of
+// kernels, 2 to 3 the sum of the cut tiles.
+//
+// NG (groups of eight tokens that the call has: 1, 2, 4, 8) sets the registers and the memory of
+// the sums: with 8 for all of them 12 tokens, 2 of 16 of 2048 x 1024, take 27.8 us for 22.3.
 //
 // Roles (512 threads): warp 0 TMA, warp 1 MMA (one lane each), warps 4-11 epilogue (a thread
 // owns a row of the tile and all tokens), six make the codes, four tokens of each eight of a K
