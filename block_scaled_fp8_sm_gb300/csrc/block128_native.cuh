@@ -252,7 +252,12 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_native(const _
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(p[2 * x + (j >> 4)][j & 15]);
-                    fuse_rows32(a, lane_bias(a, col), v);
+                    if (a.ep.bias) {
+                        const float bias = lane_bias(a, col);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] += __shfl_sync(0xFFFFFFFFu, bias, c);
+                    }
+                    activate(v, a.ep.act);
                     add_residual(a, tt, q, col, v);
                     uint32_t w[16];
 #pragma unroll

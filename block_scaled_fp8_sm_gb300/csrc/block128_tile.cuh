@@ -37,6 +37,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "block128_rows.cuh"
 #include "ptx.cuh"
@@ -94,8 +95,13 @@ struct Ctrl128 {
 
 // FUSED kernels are for one product: no expert table, and the residual's pieces of 32 rows x 32
 // columns (2 KB for each epilogue warp) beside the staging.
+template <int BN>
+struct CtrlFused128 : Ctrl128<BN, 0> {
+    uint64_t ready, taken;   // the tile's bias and first piece of the residual
+    alignas(16) float bias[BN];
+};
 template <int BN, bool FUSED>
-using Control128 = Ctrl128<BN, FUSED ? 0 : T128_MAX_EXPERTS>;
+using Control128 = std::conditional_t<FUSED, CtrlFused128<BN>, Ctrl128<BN>>;
 constexpr int T128_RESIDUAL = T128_EPI_WARPS * 32 * 64;
 
 template <int BN, bool FUSED>
@@ -267,7 +273,7 @@ __device__ __forceinline__ int lane_here() {
 __device__ __forceinline__ void prefetch_residual(const Tile128Args &a, const Tile128 &tt, int cols) {
     if (!a.ep.R) return;
     const int bytes = min(cols, a.N - tt.n0) * 2, rows = min(T128_BM, tt.hi - tt.m0);
-    for (int r = 0; r < rows; ++r)
+    for (int r = lane_here(); r < rows; r += 32)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.ep.R + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0),
                      "r"(bytes)
                      : "memory");
@@ -288,10 +294,13 @@ __device__ __forceinline__ void fetch_residual(uint8_t *res, const Tile128Args &
 // What is written here, and below, so that the K loop keeps its registers (with any of these it
 // took 16 to 26 % longer, moving or spilling its sums): the residual's row 16 bytes at a time,
 // its fetch after the K loop, and arithmetic in place, the sums not exchanged in fp32.
-__device__ __forceinline__ void fuse_rows32(const Tile128Args &a, float bias, float (&v)[32]) {
+__device__ __forceinline__ void fuse_rows32(const Tile128Args &a, const float *bias, float (&v)[32]) {
     if (a.ep.bias) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] += __shfl_sync(0xFFFFFFFFu, bias, c);
+        for (int c = 0; c < 32; c += 4) {
+            const float4 w = *reinterpret_cast<const float4 *>(bias + c);
+            v[c] += w.x, v[c + 1] += w.y, v[c + 2] += w.z, v[c + 3] += w.w;
+        }
     }
     activate(v, a.ep.act);
 }
@@ -416,6 +425,10 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             mbar_init(&ctl->tempty[b], T128_EPI_WARPS);
         }
         mbar_init(&ctl->drain, 1);
+        if constexpr (FUSED) {
+            mbar_init(&ctl->ready, 1);
+            mbar_init(&ctl->taken, T128_EPI_WARPS);
+        }
         ctl->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&a.tmA);
@@ -449,7 +462,6 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 bool ok = true;
                 for (int t = unit; t < tiles && ok; t += units) {
                     const Tile128 tt = tile128<BN>(a, ctl, t);
-                    if constexpr (FUSED && !SPLIT) prefetch_residual(a, tt, BN);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         ok = wait128(&ctl->empty[s], ph, ctl, a);
                         if (!ok) break;
@@ -506,6 +518,27 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&ctl->drain, 0))
                     if (clock64() - t0 > a.wait_limit) break;
+            }
+        } else if (warp == 2) {
+            if constexpr (FUSED && !SPLIT) {
+                // a tile's bias, its residual to L2 and the first pieces of it, while the tile's K loop runs
+                if (a.ep.bias || a.ep.R) {
+                    uint32_t ph = 1;
+                    for (int t = unit; t < tiles; t += units) {
+                        const Tile128 tt = tile128<BN>(a, ctl, t);
+                        prefetch_residual(a, tt, BN);
+                        if (!__all_sync(0xFFFFFFFFu, wait128(&ctl->taken, ph, ctl, a))) break;
+                        ph ^= 1u;
+#pragma unroll 1
+                        for (int w = 0; w < T128_EPI_WARPS; ++w)
+                            fetch_residual(stg + C::STG + w * (32 * 64), a, tt, w & 3, tt.n0 + (w >> 2) * C::COLS);
+#pragma unroll 1
+                        for (int c = 0; c < BN; c += 32) ctl->bias[c + lane] = lane_bias(a, tt.n0 + c);
+                        cp_async_wait_all();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->ready);
+                    }
+                }
             }
         }
     } else {
@@ -576,15 +609,25 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                     red[r * (BN / 4) + ((h * (C::COLS / 4) + j) ^ (r & 7))] =
                         make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
             } else {
-                if constexpr (FUSED) fetch_residual(res, a, cur, q, cur.n0 + h * C::COLS);
+                if constexpr (FUSED) {
+                    if (a.ep.bias || a.ep.R) {
+                        ok = __all_sync(0xFFFFFFFFu, wait128(&ctl->ready, static_cast<uint32_t>((t - unit) / units) & 1u, ctl, a));
+                        if (!ok) break;
+                    }
+                }
 #pragma unroll
                 for (int x = 0; x < C::COLS / 32; ++x) {
                     const int col = cur.n0 + h * C::COLS + 32 * x;
                     if constexpr (FUSED) {
                         float(&v)[32] = *reinterpret_cast<float (*)[32]>(acc + 32 * x);
-                        fuse_rows32(a, lane_bias(a, col), v);
+                        fuse_rows32(a, ctl->bias + h * C::COLS + 32 * x, v);
                         add_fetched_residual(res, a, v);
-                        if (x + 1 < C::COLS / 32) fetch_residual(res, a, cur, q, col + 32);
+                        if (x + 1 < C::COLS / 32) {
+                            fetch_residual(res, a, cur, q, col + 32);
+                        } else {
+                            __syncwarp();
+                            if (lane_here() == 0) mbar_arrive(&ctl->taken);
+                        }
                     }
                     uint32_t w[16];
 #pragma unroll
