@@ -93,8 +93,8 @@ struct Ctrl128 {
     int2 rows[EXPERTS + 1];   // and its rows
 };
 
-// FUSED kernels are for one product: no expert table, and the residual's pieces of 32 rows x 32
-// columns (2 KB for each epilogue warp) beside the staging.
+// FUSED kernels are for one product: no expert table, and beside the staging as much again for
+// pieces of the residual (32 rows x 32 columns, 2 KB, for each epilogue warp).
 template <int BN>
 struct CtrlFused128 : Ctrl128<BN, 0> {
     uint64_t ready, taken;   // the tile's bias and first piece of the residual
@@ -268,8 +268,14 @@ __device__ __forceinline__ int lane_here() {
     return lane;
 }
 
-// The residual of a tile comes to L2 (the producer, a tile ahead of its epilogue), and a piece
-// of it (32 rows, 32 columns) to shared memory while the epilogue does something else.
+// FUSED, unsplit: the epilogue must not wait for memory, because the tensor pipe waits for the
+// epilogue.  Warp 2, idle otherwise, brings a tile's residual to L2 a tile ahead, and while the
+// tile's K loop runs its bias and each epilogue warp's first piece of the residual (32 rows, 32
+// columns) to shared memory.  The epilogue warps fetch their other pieces, each into the buffer that
+// the piece two before has left, one piece ahead; a piece's results are staged where its
+// residual was.  4096^3: nothing to do 67 us, bias 70, residual 74, bias, gelu_tanh and residual 84
+// (the epilogue warps fetching by themselves: 74, 78, 91), bias and gelu 81: issue of the activation
+// by 256 threads between one K loop and the next.
 __device__ __forceinline__ void prefetch_residual(const Tile128Args &a, const Tile128 &tt, int cols) {
     if (!a.ep.R) return;
     const int bytes = min(cols, a.N - tt.n0) * 2, rows = min(T128_BM, tt.hi - tt.m0);
@@ -290,7 +296,7 @@ __device__ __forceinline__ void fetch_residual(uint8_t *res, const Tile128Args &
     }
 }
 
-// Bias and activation of 32 columns of each lane's row, in place; bias: the lane's column's.
+// Bias (the same for all lanes) and activation of 32 columns of each lane's row, in place.
 // What is written here, and below, so that the K loop keeps its registers (with any of these it
 // took 16 to 26 % longer, moving or spilling its sums): the residual's row 16 bytes at a time,
 // its fetch after the K loop, and arithmetic in place, the sums not exchanged in fp32.
@@ -305,7 +311,7 @@ __device__ __forceinline__ void fuse_rows32(const Tile128Args &a, const float *b
     activate(v, a.ep.act);
 }
 
-// The bias of column col + lane.
+// The bias of column col + lane, 0 past the end.
 __device__ __forceinline__ float lane_bias(const Tile128Args &a, int col) {
     const int n = col + lane_here();
     if (!a.ep.bias || n >= a.N) return 0.0f;
@@ -323,10 +329,11 @@ __device__ __forceinline__ void add8(float *v, const uint4 r) {
 }
 
 // The residual of these columns: of a piece that was fetched, or straight from memory.
+template <bool LAST>
 __device__ __forceinline__ void add_fetched_residual(const uint8_t *res, const Tile128Args &a, float (&v)[32]) {
     if (!a.ep.R) return;
     const int lane = lane_here();
-    cp_async_wait_all();
+    cp_async_wait_group<LAST ? 0 : 1>();
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c) add8(v + 8 * c, *reinterpret_cast<const uint4 *>(res + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)));
@@ -620,20 +627,22 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                     const int col = cur.n0 + h * C::COLS + 32 * x;
                     if constexpr (FUSED) {
                         float(&v)[32] = *reinterpret_cast<float (*)[32]>(acc + 32 * x);
-                        fuse_rows32(a, ctl->bias + h * C::COLS + 32 * x, v);
-                        add_fetched_residual(res, a, v);
-                        if (x + 1 < C::COLS / 32) {
-                            fetch_residual(res, a, cur, q, col + 32);
-                        } else {
-                            __syncwarp();
-                            if (lane_here() == 0) mbar_arrive(&ctl->taken);
+                        constexpr int LAST = C::COLS / 32 - 1;
+                        if (x < LAST) {
+                            fetch_residual(x & 1 ? res : mine, a, cur, q, col + 32);
+                            cp_async_commit();
                         }
+                        fuse_rows32(a, ctl->bias + h * C::COLS + 32 * x, v);
+                        if (x < LAST) add_fetched_residual<false>(x & 1 ? mine : res, a, v);
+                        else add_fetched_residual<true>(x & 1 ? mine : res, a, v);
                     }
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = bf16_pair(acc[32 * x + 2 * j], acc[32 * x + 2 * j + 1]);
-                    store_rows32(mine, a, cur, q, col, w);
+                    store_rows32(FUSED && !(x & 1) ? res : mine, a, cur, q, col, w);
                 }
+                if constexpr (FUSED)
+                    if (lane_here() == 0) mbar_arrive(&ctl->taken);
             }
             if (t + units < tiles) begin(t + units);
         }
