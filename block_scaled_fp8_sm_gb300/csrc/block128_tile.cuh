@@ -328,7 +328,8 @@ __device__ __forceinline__ void add8(float *v, const uint4 r) {
     }
 }
 
-// The residual of these columns: of a piece that was fetched, or straight from memory.
+// The residual of these columns, from a piece that was fetched (LAST: with none behind it on its
+// way), or straight from memory.
 template <bool LAST>
 __device__ __forceinline__ void add_fetched_residual(const uint8_t *res, const Tile128Args &a, float (&v)[32]) {
     if (!a.ep.R) return;

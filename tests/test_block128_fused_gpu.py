@@ -157,3 +157,36 @@ def test_replayed_in_a_graph_and_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(C, D)
     del graph
+
+
+@pytest.mark.parametrize("bias,residual", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("M,N,K,mode", [(2500, 4360, 144, None), (2500, 4360, 144, bs.FP8_PATH_NATIVE),
+                                        (150, 19464, 272, bs.FP8_PATH_PROMOTE)])
+def test_many_tiles_of_a_cta_in_place(M, N, K, mode, bias, residual):
+    """More tiles than CTAs: what is staged for one tile is not taken for another's."""
+    ops, b, R = operands(M, N, K, 29, pow2=mode == bs.FP8_PATH_NATIVE)
+    b = b if bias else None
+    want, bound = _fused.fused(*ops, b, "none", R if residual else None)
+    bs.fp8_gemm_block128_fused(*ops, R, bias=b, residual=R if residual else None, mode=mode)
+    compare(R, want, bound, f"{M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("stage", [0, 2, 7])
+def test_withheld_stage_times_out_cleanly(stage):
+    """Waits that run out are reported, the kernel returns, and the next call is right."""
+    M, N, K = 1300, 3608, 1040
+    ops, bias, R = operands(M, N, K, 31)
+    C = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert bs.fp8_status_query() == 0
+    bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 20_000_000)   # ~10 ms
+    bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, stage)
+    try:
+        bs.fp8_gemm_block128_fused(*ops, C, bias=bias, act=ACT["silu"], residual=R)
+        torch.cuda.synchronize()
+        assert bs.fp8_status_query() == bs._abi.FP8_ERR_TIMEOUT
+    finally:
+        bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, -1)
+        bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 0)
+    bs.fp8_gemm_block128_fused(*ops, C, bias=bias, act=ACT["silu"], residual=R)
+    compare(C, *_fused.fused(*ops, bias, "silu", R), "after the time-out")
+    assert bs.fp8_status_query() == 0
