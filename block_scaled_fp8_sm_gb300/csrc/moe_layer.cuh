@@ -11,8 +11,7 @@
 // busy: 120 us, 5.9 TB/s; held in registers, one block ahead, 143).  1 token, 4 of 32 of 2048 x
 // 1024: 8.7 us, 25 MB; there the two launches and the first loads of each are most of it.
 //
-// Two launches and not one: the down product needs all of h, and blocks that waited for one
-// another would need a cooperative launch, which does not overlap the kernel before it.
+// Two launches and not one: the down product needs all of h, and no CTA waits for another.
 //
 // Codes become fp16 by one conversion for two (every E4M3 value is an fp16 number), and
 // x, h become fp16 with one power of two for a token's 128 (x) or 16 (h) values, which
