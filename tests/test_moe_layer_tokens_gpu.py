@@ -74,6 +74,47 @@ def test_few_tokens_of_large_weights(T, top, E, H, I):   # noqa: E741
     assert not out.any()
 
 
+# the form for few tokens, tiles for few tokens of large weights, tiles
+@pytest.mark.parametrize("T,top,E,H,I", [(6, 3, 5, 272, 400), (4, 8, 9, 2064, 2032), (20, 2, 6, 528, 272)])
+def test_nan_and_infinity_stay_with_their_tokens(T, top, E, H, I):   # noqa: E741
+    layer = _moe.Layer(E, H, I, 12)
+    x, w, ids = _moe.inputs(T, top, E, H, 13)
+    out = bs.fp8_moe_layer(x, w, ids, *layer.weights)
+    x[1, 5], x[2, H - 1], w[T - 1, 0] = float("nan"), float("-inf"), float("nan")
+    bad = bs.fp8_moe_layer(x, w, ids, *layer.weights)
+    mine = torch.zeros(T, dtype=torch.bool, device="cuda")
+    mine[1] = mine[2] = mine[T - 1] = True
+    assert torch.equal(bad[~mine], out[~mine])
+    assert not bool(bad[mine].isfinite().any())
+    # a weight that is NaN spoils its row's results for the expert's tokens
+    x, w, ids = _moe.inputs(T, top, E, H, 13)
+    e = int(ids[0, 0])
+    layer.down[e, 17, 3] = 0x7F
+    bad = bs.fp8_moe_layer(x, w, ids, *layer.weights)
+    mine = (ids == e).any(1)
+    want = torch.zeros(T, H, dtype=torch.bool, device="cuda")
+    want[mine, 17] = True
+    assert torch.equal(bad.isnan(), want) and torch.equal(bad[~want], out[~want])
+    layer.gate_up[e, 3, H - 1] = 0xFF
+    assert torch.equal(bs.fp8_moe_layer(x, w, ids, *layer.weights).isnan().all(1), mine)
+
+
+@pytest.mark.parametrize("T", [1, 5, 30])
+def test_weights_past_32_bits(T):
+    """Codes of more than 2^32 bytes, the last expert's at their end."""
+    E, H, I = 300, 4096, 2048   # noqa: E741
+    free = torch.cuda.mem_get_info()[0]
+    if free < 20 << 30:
+        pytest.skip("not enough memory")
+    part = _moe.Layer(2, H, I, 14)
+    gate_up = torch.zeros(E, 2 * I, H, dtype=torch.uint8, device="cuda")
+    down = torch.zeros(E, H, I, dtype=torch.uint8, device="cuda")
+    s_gate_up, s_down = torch.zeros(E, 2 * I // 128, H // 128, device="cuda"), torch.zeros(E, H // 128, I // 128, device="cuda")
+    gate_up[-2:], s_gate_up[-2:], down[-2:], s_down[-2:] = part.weights
+    x, w, ids = _moe.inputs(T, 2, 2, H, 15)
+    compare(bs.fp8_moe_layer(x, w, ids + E - 2, gate_up, s_gate_up, down, s_down), *part.reference(x, w, ids))
+
+
 def test_no_expert_at_all():
     layer = _moe.Layer(3, 64, 32, 1)
     x, w, ids = _moe.inputs(5, 2, 3, 64, 1)
