@@ -47,11 +47,15 @@ bool set_down_shared() {
            set_shared(reinterpret_cast<const void *>(bsfp8_moe_down<MT, 8>), moe_down_smem(MT));
 }
 
+// The form for few tokens takes eight at a time: how often, and the pairs of eight tokens.
+unsigned eights(int64_t T) { return static_cast<unsigned>((T + MOE_FEW_TOKENS - 1) / MOE_FEW_TOKENS); }
+int64_t few_pairs(int64_t T, int64_t top) { return (T < MOE_FEW_TOKENS ? T : MOE_FEW_TOKENS) * top; }
+
 template <int MT>
 int launch_down(const MoeArgs &a, cudaStream_t stream) {
-    return launch(a.T * a.top <= 64 ? bsfp8_moe_down<MT, 2> : bsfp8_moe_down<MT, 8>,
-                  dim3(static_cast<unsigned>((a.H + 16 * MT - 1) / (16 * MT))), MOE_DOWN_WARPS * 32, moe_down_smem(MT), 1, a,
-                  stream);
+    return launch(few_pairs(a.T, a.top) <= 64 ? bsfp8_moe_down<MT, 2> : bsfp8_moe_down<MT, 8>,
+                  dim3(static_cast<unsigned>((a.H + 16 * MT - 1) / (16 * MT)), 1, eights(a.T)), MOE_DOWN_WARPS * 32,
+                  moe_down_smem(MT), 1, a, stream);
 }
 
 template <int NG>
@@ -92,21 +96,34 @@ bool layer_sizes(int64_t T, int32_t top, int64_t I) {
     return T >= 0 && T <= FP8_MOE_MAX_TOKENS && top >= 1 && top <= FP8_MAX_TOP && I >= 0 && I < kLim && I % 16 == 0;
 }
 
+// The bytes of weights that T tokens read where routing is even.
+double even_bytes(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
+    double without = 1.0;   // an expert without tokens
+    for (int64_t t = 0; t < T; ++t) without *= 1.0 - static_cast<double>(top < E ? top : E) / E;
+    return (1.0 - without) * E * 3.0 * static_cast<double>(H) * static_cast<double>(I);
+}
+
 // Whether the tile form (moe_tile.cuh) serves the call, else the one for few tokens
-// (moe_layer.cuh), whose set-up is some 12 us shorter and whose rate falls as the tokens grow.  By
-// the weights that even routing reads; few-token form against tiles, us (hidden x inner):
-//   4 tokens up from 90 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 14.6, 20.1; 8 of them (66)
-//     18.1, 20.5; 4, 8 of 256 of 2048 x 512 (96) 27.7, 25.9; 8 of them (181) 49.2, 42.6; 8, 2 of 8
-//     of 4096 x 14336 (1270) 225, 191; 8, 8 of 64 of 7168 x 2048 (1850) 289, 274
+// (moe_layer.cuh), whose set-up is some 12 us shorter, whose rate falls as the tokens grow, and
+// which reads an expert's weights again for each eight tokens.  By the weights that even routing
+// reads; few-token form against tiles, us (hidden x inner):
+//   4 to 8 tokens up from 95 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 14.6, 20.1; 8 of them
+//     (66) 18.1, 20.5; 8, 2 of 8 of 4096 x 1024 (91) 22.0, 25.5; 4, 8 of 256 of 2048 x 512 (96) 27.7,
+//     25.9; 8 of them (181) 49.2, 42.6; 8, 2 of 8 of 4096 x 14336 (1270) 225, 191; 8, 8 of 64 of
+//     7168 x 2048 (1850) 289, 274
 //   fewer from 400 MB: 1, 4 of 32 of 2048 x 1024 (25) 8.5, 19.5; 2, 8 of 64 of 4096 x 1536 (283)
 //     55.0, 57.7; 1, 8 of 64 of 7168 x 2048 (352) 64.0, 66.0; 3, 1 of 8 of 4096 x 14336 (465) 98.8,
 //     91.9; 2, 8 of 64 of 7168 x 2048 (660) 116.5, 115.4
+//   more where 6.5 us and 0.2 for each MB that all eights read exceed the tiles' 13.5, 0.3 a token
+//     and 0.09 for each MB: 4 of 24 of 768 x 256, 9 tokens 10.5, 17.9, 32 18.2, 23.3, 64 29.3, 34.1;
+//     3 of 11 of 1344 x 512, 16 tokens 16.3, 20.5, 32 25.1, 26.8, 48 39.0, 35.1; 2 of 6 of 2048 x 1024,
+//     16 tokens 20.4, 24.1, 32 37.4, 28.4; 8 of 32 of 1024 x 512, 12 tokens 27.9, 22.9
 bool takes_tiles(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
-    if (T > MOE_FEW_TOKENS) return true;
-    double without = 1.0;   // an expert without tokens, when routing is even
-    for (int64_t t = 0; t < T; ++t) without *= 1.0 - static_cast<double>(top < E ? top : E) / E;
-    const double bytes = (1.0 - without) * E * 3.0 * static_cast<double>(H) * static_cast<double>(I);
-    return bytes >= (T < 4 ? 400e6 : 90e6);
+    const double bytes = even_bytes(T, top, E, H, I);
+    if (T <= MOE_FEW_TOKENS) return bytes >= (T < 4 ? 400e6 : 95e6);
+    const double few = static_cast<double>(T / MOE_FEW_TOKENS) * even_bytes(MOE_FEW_TOKENS, top, E, H, I) +
+                       even_bytes(T % MOE_FEW_TOKENS, top, E, H, I);
+    return 6.5 + 0.2e-6 * few > 13.5 + 0.3 * static_cast<double>(T) + 0.09e-6 * bytes;
 }
 
 }  // namespace
@@ -244,15 +261,15 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
         });
     }
     const MoeArgs &few = a;
-    const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(T * top));
     // words of pairs: two, or eight (8 tokens, 2 of 16 experts of 2048 x 1024: 17.8 us, 20.3)
-    const bool two = T * top <= 64;
-    rc = launch(two ? bsfp8_moe_up<2> : bsfp8_moe_up<8>, grid, MOE_UP_WARPS * 32, MOE_UP_SMEM, 1, few, stream);
+    const int64_t pairs = few_pairs(T, top);
+    const dim3 grid(static_cast<unsigned>(I / MOE_UP_COLS), static_cast<unsigned>(pairs), eights(T));
+    rc = launch(pairs <= 64 ? bsfp8_moe_up<2> : bsfp8_moe_up<8>, grid, MOE_UP_WARPS * 32, MOE_UP_SMEM, 1, few, stream);
     if (rc != FP8_OK) return rc;
     // as many columns for a CTA as let one wave have all of them (one CTA on an SM), up to 48: 1
     // token, 8 of 64 experts of 7168 x 2048, 48 columns 63.6 us, 16 columns 73.5; 2 of 8 of 4096 x
     // 14336, 32 columns 70.2, 16 columns 76.9
-    const int64_t wide = (H / 16 + d->sm_count - 1) / d->sm_count;
+    const int64_t wide = (H / 16 * eights(T) + d->sm_count - 1) / d->sm_count;
     return wide <= 1 ? launch_down<1>(few, stream) : wide == 2 ? launch_down<2>(few, stream) : launch_down<3>(few, stream);
 }
 

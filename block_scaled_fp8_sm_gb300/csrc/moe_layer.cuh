@@ -1,4 +1,5 @@
-// moe_layer.cuh -- a whole mixture-of-experts layer for a few tokens, in two kernels.
+// moe_layer.cuh -- a whole mixture-of-experts layer for a few tokens, eight at a time, in two
+// kernels.
 //
 //   h[t,e] = silu(G_e x_t) * (U_e x_t)           gate and up rows of W1[e]
 //   out[t] = bf16( sum over the token's experts w[t,e] * (D_e h[t,e]) )
@@ -10,6 +11,9 @@
 // takes them from there without a barrier (3 tokens, 8 of 64 experts of 7168 x 2048, 16 of them
 // busy: 120 us, 5.9 TB/s; held in registers, one block ahead, 143).  1 token, 4 of 32 of 2048 x
 // 1024: 8.7 us, 25 MB; there the two launches and the first loads of each are most of it.
+//
+// More than eight tokens are as many calls side by side (the grid's z), which share the weights in
+// L2: with small weights that costs less than the set-up of moe_tile.cuh (the rule of moe_api.cu).
 //
 // Two launches and not one: the down product needs all of h, and no CTA waits for another.
 //
@@ -33,7 +37,7 @@
 
 namespace bsfp8 {
 
-constexpr int MOE_FEW_TOKENS = 8;   // the most for the kernels of this file: the MMA's columns
+constexpr int MOE_FEW_TOKENS = 8;   // tokens of a CTA of this file: the MMA's columns
 constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 32, MOE_MAX_EXPERTS = 1024;
 constexpr int MOE_UP_WARPS = 8, MOE_DOWN_WARPS = 16;
 constexpr int MOE_UP_COLS = 16;     // columns of h per CTA: 16 gate and 16 up rows
@@ -162,11 +166,12 @@ __device__ __forceinline__ MoePairs<PW> pairs_of(const int (&own)[PW], int e) {
     return m;
 }
 
+// Ids of the pairs p0 .. p0 + pairs - 1.
 template <int PW>
-__device__ __forceinline__ void load_ids(const MoeArgs &a, int (&own)[PW]) {
-    const int pairs = a.T * a.top, lane = threadIdx.x & 31;
+__device__ __forceinline__ void load_ids(const MoeArgs &a, int p0, int pairs, int (&own)[PW]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < PW; ++i) own[i] = 32 * i + lane < pairs ? a.ids[32 * i + lane] : -1;
+    for (int i = 0; i < PW; ++i) own[i] = 32 * i + lane < pairs ? a.ids[p0 + 32 * i + lane] : -1;
 }
 
 // A thread's 16-byte pieces of a K block in shared memory: N of them, DEPTH blocks.
@@ -184,8 +189,8 @@ struct MoeRing {
     }
 };
 
-// Gate and up: a CTA owns 16 columns of h of one expert, for all of its tokens.  The CTAs of
-// pair blockIdx.y do this where it is the first of all with its expert, and leave otherwise.
+// Gate and up: a CTA owns 16 columns of h of one expert, for all of its tokens among eight.  The
+// CTAs of pair blockIdx.y do this where it is the first of all with its expert, and leave otherwise.
 // MMA piece i holds gate rows 8 i .. 8 i + 7 and the up rows of the same columns, so that a
 // thread has both numbers of an h.
 constexpr int MOE_UP_DEPTH = 3;
@@ -199,9 +204,12 @@ __global__ void __launch_bounds__(MOE_UP_WARPS * 32, 2) bsfp8_moe_up(const MoeAr
     const int n0 = static_cast<int>(blockIdx.x) * MOE_UP_COLS;
     const MoeRing<8, MOE_UP_DEPTH> ring(moe_smem);
     wait_for_previous();
+    const int t0 = static_cast<int>(blockIdx.z) * MOE_FEW_TOKENS, p0 = t0 * a.top;
+    const int pairs = min(MOE_FEW_TOKENS, a.T - t0) * a.top;
+    if (static_cast<int>(blockIdx.y) >= pairs) return;   // the last eight may be fewer
     int own[PW];
-    load_ids<PW>(a, own);
-    const int e = a.ids[blockIdx.y];
+    load_ids<PW>(a, p0, pairs, own);
+    const int e = a.ids[p0 + blockIdx.y];
     if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.E)) return;
     const int KB = (a.H + 127) / 128, NB = (2 * a.I + 127) / 128;
     const uint8_t *W = a.W1 + (static_cast<int64_t>(e) * 2 * a.I + n0 + g) * a.H + 16 * t;
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(MOE_UP_WARPS * 32, 2) bsfp8_moe_up(const MoeAr
 #pragma unroll
     for (int d = 0; d < MOE_UP_DEPTH; ++d) fetch(d, warp + d * MOE_UP_WARPS);
     const bool has = m.first(g, a.top) >= 0;   // this lane's token (none from T on)
-    const __nv_bfloat16 *x = a.x + (has ? static_cast<int64_t>(g) * a.H + 16 * t : 0);
+    const __nv_bfloat16 *x = a.x + (has ? static_cast<int64_t>(t0 + g) * a.H + 16 * t : 0);
     const float *sg = a.s1 + (static_cast<int64_t>(e) * NB + n0 / 128) * KB;
     const float *su = a.s1 + (static_cast<int64_t>(e) * NB + (a.I + n0) / 128) * KB;
     uint4 xr[4];
@@ -300,15 +308,16 @@ __global__ void __launch_bounds__(MOE_UP_WARPS * 32, 2) bsfp8_moe_up(const MoeAr
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
         float inverse;
         const float s = scale_to_half(amax, inverse);
-        const int64_t to = m.first(tok, a.top);
-        if (to >= 0) {
+        const int first = m.first(tok, a.top);
+        if (first >= 0) {
+            const int64_t to = p0 + first;
             a.h[to * a.I + n0 + col] = __float2half_rn(v * s);
             if (col == 0) a.hs[to * (a.I / 16) + n0 / 16] = inverse;
         }
     }
 }
 
-// Down and the weighted sum: a CTA owns 16 MT columns of the output for all tokens and passes
+// Down and the weighted sum: a CTA owns 16 MT columns of the output for eight tokens and passes
 // over the busy experts in ascending order, DEPTH of a warp's blocks on their way.  Their weights
 // and the routing are not written by the up kernel, and what came before that had ended when
 // it let this kernel start: only h waits for it.
@@ -323,8 +332,9 @@ __global__ void __launch_bounds__(MOE_DOWN_WARPS * 32, 1) bsfp8_moe_down(const M
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = static_cast<int>(blockIdx.x) * 16 * MT;
     const MoeRing<4 * MT, DEPTH> ring(moe_smem);
+    const int t0 = static_cast<int>(blockIdx.z) * MOE_FEW_TOKENS, p0 = t0 * a.top, tokens = min(MOE_FEW_TOKENS, a.T - t0);
     int own[PW];
-    load_ids<PW>(a, own);
+    load_ids<PW>(a, p0, tokens * a.top, own);
     if (threadIdx.x < MOE_MAX_EXPERTS / 32) bits[threadIdx.x] = 0u;
     __syncthreads();
 #pragma unroll
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(MOE_DOWN_WARPS * 32, 1) bsfp8_moe_down(const M
         if (es[u] < 0) return;
         const uint32_t mine = pairs_of<PW>(own, es[u]).of(g, a.top);   // none from T on
         has = mine != 0u;
-        const int64_t pair = has ? g * a.top + __ffs(mine) - 1 : 0;
+        const int64_t pair = has ? p0 + g * a.top + __ffs(mine) - 1 : 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int k = ks[u] * 128 + 64 * j + 16 * t;
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(MOE_DOWN_WARPS * 32, 1) bsfp8_moe_down(const M
             hr[2 * j + 1] = load16_if(h + 16, in);
         }
         w = has ? a.w[pair] : 0.0f;   // and its other weights for the expert
-        for (uint32_t rest = mine & (mine - 1u); rest; rest &= rest - 1u) w += a.w[g * a.top + __ffs(rest) - 1];
+        for (uint32_t rest = mine & (mine - 1u); rest; rest &= rest - 1u) w += a.w[p0 + g * a.top + __ffs(rest) - 1];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             sb[i] = a.s2[(static_cast<int64_t>(es[u]) * NB + min((n0 + 16 * i) / 128, NB - 1)) * KB + ks[u]];
@@ -466,7 +476,7 @@ __global__ void __launch_bounds__(MOE_DOWN_WARPS * 32, 1) bsfp8_moe_down(const M
         float v = 0.0f;
 #pragma unroll
         for (int x = 0; x < MOE_DOWN_WARPS; ++x) v += red[((x * MT + (col >> 4)) * 4 + c) * 32 + l];
-        if (tok < a.T && n0 + col < a.H) a.out[static_cast<int64_t>(tok) * a.H + n0 + col] = __float2bfloat16_rn(v);
+        if (tok < tokens && n0 + col < a.H) a.out[static_cast<int64_t>(t0 + tok) * a.H + n0 + col] = __float2bfloat16_rn(v);
     }
 }
 

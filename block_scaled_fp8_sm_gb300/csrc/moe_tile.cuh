@@ -1,5 +1,5 @@
-// moe_tile.cuh -- the mixture-of-experts layer of moe_layer.cuh for more than eight tokens, or
-// fewer with large weights, on the tensor cores (tcgen05): the weights come by TMA and are never
+// moe_tile.cuh -- the mixture-of-experts layer of moe_layer.cuh for more tokens or larger weights,
+// on the tensor cores (tcgen05): the weights come by TMA and are never
 // touched by a register.
 //
 // A weight tile's 256 rows are the M side of two MMAs, an expert's tokens their N side, in

@@ -21,16 +21,22 @@ def compare(out, ref, bound, what=""):
     assert bool((err <= bound).all()), f"{what}: worst {float((err / bound).max()):.3f} of the bound"
 
 
-# T, top, E, H, I: one token, one expert, blocks that end early, sizes below a block, more
-# tokens of an expert than one and two groups of columns, fewer blocks of K than warps and more
+# T, top, E, H, I: one token, one expert, blocks that end early, sizes below a block, eights of
+# tokens that are full and not, fewer blocks of K than warps and more (small weights)
 SIZES = [(1, 1, 1, 16, 16), (1, 4, 32, 2048, 1024), (3, 8, 64, 512, 272), (8, 2, 4, 1040, 400), (9, 3, 5, 144, 2064),
          (19, 3, 16, 2064, 1040), (64, 8, 16, 528, 256), (64, 2, 2, 272, 48), (33, 32, 40, 256, 128),
          (64, 1, 1024, 64, 32), (17, 1, 1, 4112, 1296), (16, 2, 3, 144, 80), (25, 4, 5, 400, 1040), (32, 8, 9, 1040, 144),
          (57, 7, 8, 272, 2064), (48, 1, 2, 16, 16),
          (64, 4, 4, 4096, 1024), (40, 8, 12, 2048, 2048)]
 
+# large weights, which tiles read: one, two, four and eight groups of eight tokens of an expert, one
+# row of tiles, tiles and blocks that end early, many experts, every pair of a token
+TILES = [(9, 8, 20, 2064, 1040), (12, 8, 30, 2064, 1040), (33, 32, 40, 1040, 528), (64, 32, 1024, 256, 272),
+         (17, 1, 1, 4112, 4112), (48, 1, 2, 4112, 2064), (57, 7, 8, 528, 4112), (25, 4, 5, 1040, 4112),
+         (30, 4, 48, 144, 5136), (30, 4, 48, 5136, 144), (64, 8, 256, 528, 272), (16, 2, 40, 1040, 2064)]
 
-@pytest.mark.parametrize("T,top,E,H,I", SIZES)
+
+@pytest.mark.parametrize("T,top,E,H,I", SIZES + TILES)
 def test_sizes(T, top, E, H, I):   # noqa: E741
     layer = _moe.Layer(E, H, I, T + H)
     x, w, ids = _moe.inputs(T, top, E, H, I)
@@ -39,10 +45,10 @@ def test_sizes(T, top, E, H, I):   # noqa: E741
     compare(out, *layer.reference(x, w, ids), f"{T} {top} {E} {H} {I}")
 
 
-@pytest.mark.parametrize("T", [2, 8, 21])
-def test_padding_and_repeated_experts(T):
-    layer = _moe.Layer(6, 272, 144, 3)
-    x, w, ids = _moe.inputs(T, 4, 6, 272, 5)
+@pytest.mark.parametrize("T,H,I", [(2, 272, 144), (8, 272, 144), (21, 272, 144), (21, 2064, 2064)])
+def test_padding_and_repeated_experts(T, H, I):   # noqa: E741
+    layer = _moe.Layer(6, H, I, 3)
+    x, w, ids = _moe.inputs(T, 4, 6, H, 5)
     ids[0] = -1                                           # a token without any expert
     ids[1] = torch.tensor([2, 2, -1, 2])                  # one expert three times
     ids[T - 1] = torch.tensor([5, 6, -7, 2 ** 31 - 1])    # numbers that no expert has
@@ -74,8 +80,9 @@ def test_few_tokens_of_large_weights(T, top, E, H, I):   # noqa: E741
     assert not out.any()
 
 
-# the form for few tokens, tiles for few tokens of large weights, tiles
-@pytest.mark.parametrize("T,top,E,H,I", [(6, 3, 5, 272, 400), (4, 8, 9, 2064, 2032), (20, 2, 6, 528, 272)])
+# the form for few tokens, tiles for few tokens, several eights, tiles
+@pytest.mark.parametrize("T,top,E,H,I", [(6, 3, 5, 272, 400), (4, 8, 9, 2064, 2032), (20, 2, 6, 528, 272),
+                                         (20, 2, 6, 2064, 2064)])
 def test_nan_and_infinity_stay_with_their_tokens(T, top, E, H, I):   # noqa: E741
     layer = _moe.Layer(E, H, I, 12)
     x, w, ids = _moe.inputs(T, top, E, H, 13)
@@ -137,7 +144,8 @@ def test_a_tokens_bits_do_not_depend_on_the_others(T, top, E, H, I):   # noqa: E
     assert torch.equal(bs.fp8_moe_layer(x[turn], w[turn], ids[turn], *layer.weights), out[turn])
 
 
-@pytest.mark.parametrize("T,top,E,H,I", [(9, 3, 5, 144, 2064), (64, 8, 32, 256, 272), (30, 4, 8, 2064, 400)])
+@pytest.mark.parametrize("T,top,E,H,I", [(9, 3, 5, 144, 2064), (64, 8, 32, 256, 272), (30, 4, 8, 2064, 400),
+                                         (30, 4, 8, 2064, 2064), (64, 8, 256, 528, 272)])
 def test_calls_repeat_bit_for_bit(T, top, E, H, I):   # noqa: E741
     layer = _moe.Layer(E, H, I, 8)
     x, w, ids = _moe.inputs(T, top, E, H, 9)
@@ -146,11 +154,12 @@ def test_calls_repeat_bit_for_bit(T, top, E, H, I):   # noqa: E741
         assert torch.equal(bs.fp8_moe_layer(x, w, ids, *layer.weights), out)
 
 
-@pytest.mark.parametrize("T", [6, 14, 40])
-def test_ranges(T):
+@pytest.mark.parametrize("T,E,H,I", [(6, 4, 256, 128), (14, 4, 256, 128), (40, 4, 256, 128), (14, 8, 2048, 2064),
+                                     (40, 8, 2048, 1040)])
+def test_ranges(T, E, H, I):   # noqa: E741
     """Activations near the ends of bf16's range, one token beside another."""
-    layer = _moe.Layer(4, 256, 128, 2)
-    x, w, ids = _moe.inputs(T, 2, 4, 256, 4)
+    layer = _moe.Layer(E, H, I, 2)
+    x, w, ids = _moe.inputs(T, 2, E, H, 4)
     x[1] *= 2.0 ** -100
     x[2] *= 2.0 ** 55
     x[3, :128] *= 2.0 ** -60
@@ -184,18 +193,19 @@ def test_deep_gates():
         assert not out[1].any() and not out[0, 16:].any()
 
 
-def test_replays_in_a_graph_and_on_another_stream():
-    layer = _moe.Layer(8, 272, 144, 3)
+@pytest.mark.parametrize("H,I", [(272, 144), (2064, 2064)])
+def test_replays_in_a_graph_and_on_another_stream(H, I):   # noqa: E741
+    layer = _moe.Layer(8, H, I, 3)
     T, top = 12, 3
-    x, w, ids = _moe.inputs(T, top, 8, 272, 1)
+    x, w, ids = _moe.inputs(T, top, 8, H, 1)
     out = torch.empty_like(x)
-    space = torch.empty(bs.fp8_moe_layer_workspace_bytes(T, top, 144), dtype=torch.uint8, device="cuda")
+    space = torch.empty(bs.fp8_moe_layer_workspace_bytes(T, top, I), dtype=torch.uint8, device="cuda")
     bs.fp8_moe_layer(x, w, ids, *layer.weights, out, space)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         bs.fp8_moe_layer(x, w, ids, *layer.weights, out, space)
     for seed in (2, 3):
-        for old, new in zip((x, w, ids), _moe.inputs(T, top, 8, 272, seed)):
+        for old, new in zip((x, w, ids), _moe.inputs(T, top, 8, H, seed)):
             old.copy_(new)
         graph.replay()
         torch.cuda.synchronize()
@@ -208,7 +218,7 @@ def test_replays_in_a_graph_and_on_another_stream():
     del graph
 
 
-@pytest.mark.parametrize("T,top,E,H,I", [(5, 2, 8, 272, 144), (64, 4, 16, 512, 272)])
+@pytest.mark.parametrize("T,top,E,H,I", [(5, 2, 8, 272, 144), (64, 4, 16, 512, 272), (40, 4, 16, 2048, 1040)])
 def test_routed_chain(T, top, E, H, I):   # noqa: E741
     """Router, layer, and the same layer by the operators for many tokens, called as a
     program does, without a synchronization between them: the layer against 64 bits, the
@@ -255,9 +265,9 @@ def test_reference_values_of_the_weights():
 @pytest.mark.parametrize("T,stage", [(12, 0), (12, 3), (40, 1)])
 def test_withheld_stage_times_out_cleanly(T, stage):
     """Waits that run out are reported, the kernels return, and the next call is right."""
-    layer = _moe.Layer(4, 2064, 1040, 6)
+    layer = _moe.Layer(4, 2064, 2064, 6)
     x, w, ids = _moe.inputs(T, 3, 4, 2064, 7)
-    space = torch.empty(bs.fp8_moe_layer_workspace_bytes(T, 3, 1040), dtype=torch.uint8, device="cuda")
+    space = torch.empty(bs.fp8_moe_layer_workspace_bytes(T, 3, 2064), dtype=torch.uint8, device="cuda")
     assert bs.fp8_status_query() == 0
     bs.fp8_debug_set(bs.FP8_DEBUG_WAIT_LIMIT_CYCLES, 20_000_000)   # ~10 ms
     bs.fp8_debug_set(bs.FP8_DEBUG_WITHHOLD_STAGE, stage)
@@ -296,9 +306,10 @@ def test_outputs_belong_to_the_stream_that_writes_them(name, handle):
     assert got.data_ptr() != where and torch.equal(got, want)
 
 
-def test_two_calls_at_once_with_workspaces_of_their_own():
-    layer = _moe.Layer(8, 1040, 528, 6)
-    sets = [_moe.inputs(T, 3, 8, 1040, T) for T in (8, 30, 64, 17)]
+@pytest.mark.parametrize("H,I", [(1040, 528), (2064, 1040)])
+def test_two_calls_at_once_with_workspaces_of_their_own(H, I):   # noqa: E741
+    layer = _moe.Layer(8, H, I, 6)
+    sets = [_moe.inputs(T, 3, 8, H, T) for T in (8, 30, 64, 17)]
     want = [bs.fp8_moe_layer(*s, *layer.weights) for s in sets]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in sets]
