@@ -276,13 +276,17 @@ __device__ __forceinline__ int lane_here() {
 // residual was.  4096^3: nothing to do 67 us, bias 70, residual 74, bias, gelu_tanh and residual 84
 // (the epilogue warps fetching by themselves: 74, 78, 91), bias and gelu 81: issue of the activation
 // by 256 threads between one K loop and the next.
-__device__ __forceinline__ void prefetch_residual(const Tile128Args &a, const Tile128 &tt, int cols) {
+template <int COLS>
+__device__ __forceinline__ void prefetch_residual(const Tile128Args &a, const Tile128 &tt) {
     if (!a.ep.R) return;
-    const int bytes = min(cols, a.N - tt.n0) * 2, rows = min(T128_BM, tt.hi - tt.m0);
-    for (int r = lane_here(); r < rows; r += 32)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.ep.R + static_cast<int64_t>(tt.m0 + r) * a.N + tt.n0),
-                     "r"(bytes)
-                     : "memory");
+    constexpr int LINES = COLS / 64;   // 128 bytes each
+    const int lines = min(T128_BM, tt.hi - tt.m0) * LINES;
+#pragma unroll 1
+    for (int i = lane_here(); i < lines; i += 32) {
+        const int n = tt.n0 + i % LINES * 64;
+        if (n < a.N)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.ep.R + static_cast<int64_t>(tt.m0 + i / LINES) * a.N + n));
+    }
 }
 
 __device__ __forceinline__ void fetch_residual(uint8_t *res, const Tile128Args &a, const Tile128 &tt, int q, int col) {
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                     uint32_t ph = 1;
                     for (int t = unit; t < tiles; t += units) {
                         const Tile128 tt = tile128<BN>(a, ctl, t);
-                        prefetch_residual(a, tt, BN);
+                        prefetch_residual<BN>(a, tt);
                         if (!__all_sync(0xFFFFFFFFu, wait128(&ctl->taken, ph, ctl, a))) break;
                         ph ^= 1u;
 #pragma unroll 1
