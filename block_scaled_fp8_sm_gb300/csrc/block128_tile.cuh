@@ -269,7 +269,8 @@ __device__ __forceinline__ int lane_here() {
 }
 
 // FUSED, unsplit: the epilogue must not wait for memory, because the tensor pipe waits for the
-// epilogue.  Warp 2, idle otherwise, brings a tile's residual to L2 a tile ahead, and while the
+// epilogue.  Warp 2, idle otherwise, brings a tile's residual to L2 a tile ahead (by lines: bulk
+// prefetches stand before the operands' loads, 433 x 5496 x 1968 29 us for 20), and while the
 // tile's K loop runs its bias and each epilogue warp's first piece of the residual (32 rows, 32
 // columns) to shared memory.  The epilogue warps fetch their other pieces, each into the buffer that
 // the piece two before has left, one piece ahead; a piece's results are staged where its
