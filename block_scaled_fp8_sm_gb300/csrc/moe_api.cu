@@ -64,7 +64,7 @@ bool set_tile_shared() {
            set_shared(reinterpret_cast<const void *>(bsfp8_moe_tile<true, NG>), MT_SMEM);
 }
 
-// Both kernels of the layer for up to 8 NG tokens.
+// The kernels of the layer for up to 8 NG tokens.
 template <int NG>
 int launch_tiles(MoeTileArgs &a, cudaStream_t stream) {
     int rc = encode_gate_up(&a.tmW, a.W1, a.E, a.I, a.H);
@@ -75,7 +75,10 @@ int launch_tiles(MoeTileArgs &a, cudaStream_t stream) {
     rc = encode_kmajor(&a.tmW, a.W2, static_cast<int64_t>(a.E) * a.H, a.I, MT_ROWS);
     if (rc != FP8_OK) return rc;
     a.ring = (MT_SMEM - smem_moe_fixed<true, NG>(a.T, a.top, a.E)) / 1024 * 1024;
-    return launch(bsfp8_moe_tile<true, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
+    rc = launch(bsfp8_moe_tile<true, NG>, dim3(MT_CTAS), MT_THREADS, MT_SMEM, 1, a, stream);
+    if (rc != FP8_OK) return rc;
+    const dim3 grid(static_cast<unsigned>((a.H + MT_ROWS - 1) / MT_ROWS), static_cast<unsigned>(a.T));
+    return launch(bsfp8_moe_join, grid, MT_JOIN_THREADS, 0, 1, a, stream);
 }
 
 // Tokens whose whole order one CTA makes.  8 of 64 experts in a graph, one CTA against two
@@ -207,7 +210,7 @@ int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E
 
 int64_t fp8_moe_layer_workspace_bytes(int64_t T, int32_t top, int64_t I) {
     if (!layer_sizes(T, top, I)) return 0;
-    return (T * top * (2 * I + I / 4) + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + 2 * MT_CTAS * 8 + MT_CTAS * 4;
+    return (T * top * (2 * I + I / 4) + 255) / 256 * 256 + int64_t(2) * MT_CTAS * T * MT_ROWS * 4 + 2 * MT_CTAS * 8 + 8;
 }
 
 int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const void *W1, const float *s1,
@@ -252,7 +255,7 @@ int fp8_moe_layer(const void *x, const float *weights, const int32_t *ids, const
         a.part = reinterpret_cast<float *>(rest);
         rest += int64_t(2) * MT_CTAS * T * MT_ROWS * 4;
         a.has = reinterpret_cast<unsigned long long *>(rest);
-        a.counters = reinterpret_cast<int *>(rest + 2 * MT_CTAS * 8);
+        a.busy = reinterpret_cast<int *>(rest + 2 * MT_CTAS * 8);
         a.status = d->status;
         a.wait_limit = wait_limit();
         a.withhold = withheld_stage();

@@ -17,9 +17,9 @@
 // TB/s of 6.8: the makers' and the epilogue's 64 columns).  64 tokens before: mma.sync with the
 // weights through registers 992, tiles of 128 rows 523 (an MMA costs ~60 cycles for its A side
 // whatever N is, a TMA request ~70 of its thread), 256 481, an expert's K blocks walked without
-// divisions and several parts of a cut tile on their way 465.  Small weights pay the set-up:
-// 19 tokens, 3 of 16 of 2064 x 1040 (98 MB) 33 us, of which 1.5 to 2 are the lists, 3 the change of
-// kernels, 2 to 3 the sum of the cut tiles.
+// divisions 465, the parts of the cut tiles added by a kernel of their own 459.  Small weights pay
+// the set-up: 19 tokens, 3 of 16 of 2064 x 1040 (98 MB) 27 us, of which 1.5 to 2 are the lists and 3
+// each change of kernels.
 //
 // NG (groups of eight tokens that the call has: 1, 2, 4, 8) sets the registers and the memory of
 // the sums: with 8 for all of them 12 tokens, 2 of 16 of 2048 x 1024, take 27.8 us for 22.3.
@@ -32,8 +32,8 @@
 // both; CTAs take tiles in turn.  Down: a tile is 256 columns of the output with all busy
 // experts one after the other, summed in shared memory; the K blocks of all tiles are one
 // line, cut into equal pieces for the CTAs.  Where a cut goes through a tile, the parts go to
-// the workspace and the CTA that comes last adds them in order: no CTA waits for another,
-// and calls repeat bit for bit.
+// the workspace and a third kernel adds them in order: no CTA waits for another, and calls repeat
+// bit for bit.
 //
 // Every wait is bounded as in the other kernels.
 #pragma once
@@ -67,7 +67,7 @@ struct MoeTileArgs : MoeArgs {
     CUtensorMap tmW;
     float *part;              // [2 MT_CTAS][T][256]: sums of the tiles that a cut goes through,
     unsigned long long *has;  // [2 MT_CTAS] which tokens a part has: only their rows are there
-    int *counters;            // [MT_CTAS]: parts of the tile that starts in this CTA and goes on
+    int *busy;                // how many experts have tokens
     uint32_t *status;
     long long wait_limit;
     int ring;                 // bytes of shared memory for the stages
@@ -84,7 +84,7 @@ struct CtrlMoe {
     uint64_t full[MT_MAX_STAGES], empty[MT_MAX_STAGES];   // full: the weights and the codes
     uint64_t tfull[MT_MAX_BUFS], tempty[MT_MAX_BUFS], drain;
     uint32_t tmem;
-    int abort, last;
+    int abort;
     alignas(16) float sx[MT_SX_RING][8 * NG];   // read four at a time
     alignas(16) float sums[DOWN ? 8 * NG : 1][MT_ROWS];
 };
@@ -300,11 +300,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
     // when it let this one start.
     if constexpr (!DOWN) wait_for_previous();
     build_lists(a, L);
-    if constexpr (!DOWN) {
-        if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < MT_CTAS; i += MT_THREADS) a.counters[i] = 0;
-        launch_dependents();
-    }
+    if constexpr (!DOWN) launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -564,6 +560,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                     for (int t = 0; t < a.T; ++t)
                         if (c * MT_ROWS + row < a.H)
                             a.out[static_cast<int64_t>(t) * a.H + c * MT_ROWS + row] = __float2bfloat16_rn(0.0f);
+            if (blockIdx.x == 0 && row == 0) *a.busy = busy;
             for (int t = 0; t < a.T; ++t) ctl->sums[t][row] = 0.0f;
             unsigned long long touched = 0ull;   // tokens that the sums hold something of
             MoeSeg ahead;   // the next segment, whose first scales are on their way
@@ -610,7 +607,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                 const int64_t t0 = s.c * per, t1 = t0 + per;   // the tile's K blocks in the line
                 const bool part = t0 < whole.begin || t1 > whole.end;
                 // part: slot 1 of the CTA in which the tile starts, slot 0 of the others
-                const int a0 = static_cast<int>(((t0 + 1) * G - 1) / all), a1 = static_cast<int>((t1 * G - 1) / all);
+                const int a0 = static_cast<int>(((t0 + 1) * G - 1) / all);
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == a0 ? 1 : 0);
                 // from here on a warp has a token's row, a lane eight of its columns (four and four)
                 const unsigned long long tokens =
@@ -633,44 +630,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                     }
                 }
                 if (part && warp == 4 && lane == 0) a.has[slot] = tokens;
-                if (part) __threadfence();
-                named_bar_sync(1, 256);
-                if (!part) continue;
-                if (warp == 4 && lane == 0) ctl->last = atomicAdd(&a.counters[a0], 1) == a1 - a0;
-                named_bar_sync(1, 256);
-                const bool last = ctl->last;
-                named_bar_sync(1, 256);
-                if (!last) continue;
-                __threadfence();
-                // a warp for a token: the parts that have it, in order, four at a time on their way
-                for (int t = warp - 4; t < a.T; t += MT_EPI_WARPS) {
-                    float4 v[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-                    for (int i0 = a0; i0 <= a1; i0 += 32) {
-                        const int i = i0 + lane;
-                        uint32_t left = __ballot_sync(0xFFFFFFFFu, i <= a1 && (__ldcg(a.has + 2 * min(i, a1) + (i == a0 ? 1 : 0)) >> t & 1ull));
-                        while (left) {
-                            float4 w[4][2];
-                            bool any[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                any[x] = left != 0u;
-                                const int from = i0 + (any[x] ? __ffs(left) - 1 : 0);
-                                left &= left - 1u;
-                                const float4 *at = parts + ((static_cast<int64_t>(from) * 2 + (from == a0 ? 1 : 0)) * a.T + t) * LD;
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) w[x][h] = any[x] ? __ldcg(at + 32 * h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            }
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    v[h].x += w[x][h].x, v[h].y += w[x][h].y, v[h].z += w[x][h].z, v[h].w += w[x][h].w;
-                        }
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (n0 + 128 * h < a.H) store_bf16x4(a.out + static_cast<int64_t>(t) * a.H + n0 + 128 * h, v[h]);
-                }
+                named_bar_sync(1, 256);   // the sums are zeros again
             }
         }
     }
@@ -682,6 +642,44 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// The tiles that a cut goes through: a CTA adds the parts of one token and one tile in their
+// order, eight on their way, four columns a thread.  A kernel of its own, because it is all latency:
+// by the CTA that came last to a tile, the layer took 34.7 us for 28.6 (44 tokens, 2 of 9 experts of
+// 1376 x 1584, 6 tiles of 25 parts), 32.1 for 26.8 (19 tokens, 3 of 16 of 2064 x 1040) and 468 for 459
+// (64 tokens, 8 of 64 of 7168 x 2048).
+constexpr int MT_JOIN_THREADS = MT_ROWS / 4;
+
+__global__ void __launch_bounds__(MT_JOIN_THREADS) bsfp8_moe_join(const MoeTileArgs a) {
+    const int c = blockIdx.x, t = blockIdx.y, n = c * MT_ROWS + 4 * static_cast<int>(threadIdx.x);
+    wait_for_previous();
+    launch_dependents();
+    // the cuts of MoeWalk<true>
+    const int64_t per = static_cast<int64_t>(*a.busy) * ((a.I + 127) / 128), all = per * gridDim.x;
+    if (all == 0) return;
+    const int64_t G = min(all, static_cast<int64_t>(MT_CTAS)), t0 = c * per, t1 = t0 + per;
+    const int a0 = static_cast<int>(((t0 + 1) * G - 1) / all), a1 = static_cast<int>((t1 * G - 1) / all);
+    if (a0 == a1) return;   // the tile is one CTA's
+    const float4 *parts = reinterpret_cast<const float4 *>(a.part) + threadIdx.x;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = a0; i0 <= a1; i0 += 32) {
+        const int i = i0 + static_cast<int>(threadIdx.x & 31);
+        uint32_t left = __ballot_sync(0xFFFFFFFFu, i <= a1 && (a.has[2 * min(i, a1) + (i == a0 ? 1 : 0)] >> t & 1ull));
+        while (left) {
+            float4 w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int from = i0 + __ffs(left) - 1;
+                w[x] = left ? parts[((static_cast<int64_t>(from) * 2 + (from == a0 ? 1 : 0)) * a.T + t) * MT_JOIN_THREADS]
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                left &= left - 1u;
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v.x += w[x].x, v.y += w[x].y, v.z += w[x].z, v.w += w[x].w;
+        }
+    }
+    if (n < a.H) store_bf16x4(a.out + static_cast<int64_t>(t) * a.H + n, v);
 }
 
 }  // namespace bsfp8
