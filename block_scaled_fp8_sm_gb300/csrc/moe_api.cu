@@ -107,26 +107,28 @@ double even_bytes(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
 }
 
 // Whether the tile form (moe_tile.cuh) serves the call, else the one for few tokens
-// (moe_layer.cuh), whose set-up is some 12 us shorter, whose rate falls as the tokens grow, and
+// (moe_layer.cuh), whose set-up is some 10 us shorter, whose rate falls as the tokens grow, and
 // which reads an expert's weights again for each eight tokens.  By the weights that even routing
 // reads; few-token form against tiles, us (hidden x inner):
-//   4 to 8 tokens up from 95 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 14.6, 20.1; 8 of them
-//     (66) 18.1, 20.5; 8, 2 of 8 of 4096 x 1024 (91) 22.0, 25.5; 4, 8 of 256 of 2048 x 512 (96) 27.7,
-//     25.9; 8 of them (181) 49.2, 42.6; 8, 2 of 8 of 4096 x 14336 (1270) 225, 191; 8, 8 of 64 of
-//     7168 x 2048 (1850) 289, 274
+//   4 to 8 tokens up from 120 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 14.6, 20.1; 8, 2 of 8 of
+//     4096 x 1024 (91) 21.9, 26.7; 8, 7 of 7 of 6864 x 816 (118) 33.0, 39.1; 8, 4 of 32 of 2048 x 1024
+//     (132) 40.5, 36.2; 8, 8 of 256 of 2048 x 512 (181) 49.2, 42.6; 8, 2 of 8 of 4096 x 14336 (1270)
+//     225, 191; 8, 8 of 64 of 7168 x 2048 (1850) 289, 274
 //   fewer from 400 MB: 1, 4 of 32 of 2048 x 1024 (25) 8.5, 19.5; 2, 8 of 64 of 4096 x 1536 (283)
 //     55.0, 57.7; 1, 8 of 64 of 7168 x 2048 (352) 64.0, 66.0; 3, 1 of 8 of 4096 x 14336 (465) 98.8,
 //     91.9; 2, 8 of 64 of 7168 x 2048 (660) 116.5, 115.4
-//   more where 6.5 us and 0.2 for each MB that all eights read exceed the tiles' 13.5, 0.3 a token
-//     and 0.09 for each MB: 4 of 24 of 768 x 256, 9 tokens 10.5, 17.9, 32 18.2, 23.3, 64 29.3, 34.1;
-//     3 of 11 of 1344 x 512, 16 tokens 16.3, 20.5, 32 25.1, 26.8, 48 39.0, 35.1; 2 of 6 of 2048 x 1024,
-//     16 tokens 20.4, 24.1, 32 37.4, 28.4; 8 of 32 of 1024 x 512, 12 tokens 27.9, 22.9
+//   more by what both cost: 6.5 us, 0.17 for each MB that all eights read and 1.5 for 1000 CTAs of
+//     the up product, against 13.5, 0.8 for each token of an expert and 0.09 for each MB.  4 of 24 of
+//     768 x 256: 9 tokens 10.3, 15.9, 32 18.1, 19.2, 64 29.3, 24.1; 3 of 11 of 1344 x 512: 16 tokens
+//     16.3, 18.8, 32 25.0, 22.7; 2 of 6 of 2048 x 1024: 9 tokens 16.3, 19.6, 24 25.1, 24.4; 8 of 32 of
+//     1024 x 512: 9 tokens 24.2, 19.8
 bool takes_tiles(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
     const double bytes = even_bytes(T, top, E, H, I);
-    if (T <= MOE_FEW_TOKENS) return bytes >= (T < 4 ? 400e6 : 95e6);
+    if (T <= MOE_FEW_TOKENS) return bytes >= (T < 4 ? 400e6 : 120e6);
+    const double pairs = static_cast<double>(T) * top, ctas = pairs * static_cast<double>(I / MOE_UP_COLS);
     const double few = static_cast<double>(T / MOE_FEW_TOKENS) * even_bytes(MOE_FEW_TOKENS, top, E, H, I) +
                        even_bytes(T % MOE_FEW_TOKENS, top, E, H, I);
-    return 6.5 + 0.2e-6 * few > 13.5 + 0.3 * static_cast<double>(T) + 0.09e-6 * bytes;
+    return 6.5 + 0.17e-6 * few + 1.5e-3 * ctas > 13.5 + 0.8 * pairs / E + 0.09e-6 * bytes;
 }
 
 }  // namespace
