@@ -451,8 +451,8 @@ int fp8_moe_route(const void *logits, int64_t ld, int type, int64_t T, int32_t E
                   void *workspace, int64_t workspace_bytes, cudaStream_t stream);
 int64_t fp8_moe_route_workspace_bytes(int64_t T, int32_t E, int32_t top);
 
-/* A whole mixture-of-experts layer for a few tokens (a decoding step), in two
- * launches, on activations that are not quantized:
+/* A whole mixture-of-experts layer for a few tokens (a decoding step), in two or
+ * three launches, on activations that are not quantized:
  *
  *   out[t] = bf16( sum_j weights[t][j] * D_e ( silu(G_e x_t) * (U_e x_t) ) ),  e = ids[t][j]
  *
