@@ -55,7 +55,8 @@ __device__ __forceinline__ float sigmoid_gate(float y, float a, float b) {
 }
 
 // The polynomial has 32 added, taken back after ex2, so that Phi may be a subnormal number; at
-// z = 15 it is 0, however large y is.
+// z = 15 it is 0, however large y is.  On the positive side it is taken times z: 0 times +inf would
+// be NaN (-inf gives that, as the formula does).
 __device__ __forceinline__ float gelu(float y) {
     const float z = fminf(fabsf(y), 15.0f);
     float q = -0x1.98ee82p-30f;
@@ -68,8 +69,8 @@ __device__ __forceinline__ float gelu(float y) {
     q = fmaf(q, z, -0x1.d69808p-2f);
     q = fmaf(q, z, -0x1.268e82p+0f);
     q = fmaf(q, z, 31.0f - 0x1.e6p-15f);
-    const float p = ex2(q) * 0x1p-32f * y;   // NaN stays NaN
-    return y < 0.0f ? p : y - p;
+    const float tail = ex2(q) * 0x1p-32f;
+    return y < 0.0f ? tail * y : fmaf(-tail, z, y);   // NaN stays NaN
 }
 
 // The activation of N values; one branch for all of them.

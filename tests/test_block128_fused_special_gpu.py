@@ -57,6 +57,25 @@ def test_nan_stays_in_its_column(M, N, K, mode, act):
 
 @pytest.mark.parametrize("act", _fused.ACTS)
 @pytest.mark.parametrize("M,N,K,mode", FORMS)
+def test_infinities_by_the_formula(M, N, K, mode, act):
+    """+inf stays; -inf becomes 0 by relu and 0 times infinity, NaN, by the gates."""
+    ops, bias, R = operands(M, N, K)
+    clean = call(ops, bias, act, R, mode)
+    at = torch.tensor([0, 9, 32, N - 1], device="cuda")
+    y = torch.tensor([INF, -INF, -INF, INF], device="cuda")
+    bias[at] = y
+    got = call(ops, bias, act, R, mode)
+    want = _fused.activation(y.double(), act).float()
+    assert (float(want[0]), float(want[3])) == (INF, INF)
+    want = torch.where(want == 0, R[:, at].float(), want.expand(M, 4))   # relu's 0 and the residual
+    torch.testing.assert_close(got[:, at].float(), want, rtol=0, atol=0, equal_nan=True)
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert torch.equal(got[:, rest].view(torch.int16), clean[:, rest].view(torch.int16))
+
+
+@pytest.mark.parametrize("act", _fused.ACTS)
+@pytest.mark.parametrize("M,N,K,mode", FORMS)
 def test_infinite_residual(M, N, K, mode, act):
     ops, bias, R = operands(M, N, K)
     clean = call(ops, bias, act, R, mode)
@@ -65,3 +84,16 @@ def test_infinite_residual(M, N, K, mode, act):
     assert float(got[0, 8]) == INF and float(got[M - 1, 17]) == -INF
     got[0, 8], got[M - 1, 17] = clean[0, 8], clean[M - 1, 17]
     assert torch.equal(got.view(torch.int16), clean.view(torch.int16))
+
+
+@pytest.mark.parametrize("act", _fused.ACTS)
+def test_every_bf16_without_k(act):
+    """All 65536 bf16 numbers side by side, NaN among them (no K: the bias alone)."""
+    y = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda()
+    N, z = y.numel(), torch.empty(9, 0, device="cuda")
+    got = bs.fp8_gemm_block128_fused(z.to(torch.uint8), z, torch.empty(N, 0, dtype=torch.uint8, device="cuda"),
+                                     torch.empty(N // 128, 0, device="cuda"),
+                                     torch.empty(9, N, dtype=torch.bfloat16, device="cuda"), bias=y, act=ACT[act])
+    want = _fused.activation(y.double(), act)
+    assert torch.equal(got.isnan(), want.isnan().expand(9, N))
+    assert torch.equal(got == INF, (want > 3.3961e38).expand(9, N))   # past bf16's range: infinite
