@@ -78,12 +78,13 @@ __device__ __forceinline__ uint32_t half2_rn(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The power of two that brings amax to [2^14, 2^15), and its inverse.  Below 2^-112 the
-// same one is taken (the values get subnormal steps of 2^-136 then).
+// The power of two that brings amax to [2^TOP, 2^(TOP + 1)), and its inverse.  Below 2^(TOP - 126)
+// the same one is taken (14: the values get subnormal steps of 2^-136 then).
+template <int TOP = 14>
 __device__ __forceinline__ float scale_to_half(float amax, float &inverse) {
-    const uint32_t e = max(__float_as_uint(amax) >> 23, 15u);
-    inverse = __uint_as_float((e - 14u) << 23);
-    return __uint_as_float((268u - e) << 23);
+    const uint32_t e = max(__float_as_uint(amax) >> 23, TOP + 1u);
+    inverse = __uint_as_float((e - TOP) << 23);
+    return __uint_as_float((254u + TOP - e) << 23);
 }
 
 // A lane's 32 values of a token's 128-K block (the quad holds all of them) as fp16; returns

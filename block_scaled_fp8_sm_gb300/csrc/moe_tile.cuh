@@ -452,17 +452,18 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
                     if (more) load(0);
                 }
                 for (int g = 0; g < ng; ++g) {
-                    // fp16 with the block's largest in [2^7, 2^8): exact down to 2^-22 of it
+                    // fp16 with the block's largest in [2^7, 2^8): sixteen values of h go to 0 below 2^-24 of it,
+                    // and fp16's own smallest step is 2^-31 of it
                     __half2 f[4][2];
                     float inverse[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if constexpr (DOWN) {   // h's own scales (of the largest of 16 in [2^14, 2^15)) say enough
+                        if constexpr (DOWN) {   // h's own scales (of the largest of 16 in [2^7, 2^8)) say enough
                             const float top = fmaxf(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hs[i]))), 0x1p-126f);
-                            const __half2 k = __float2half2_rn(hs[i] * __uint_as_float((247u << 23) - __float_as_uint(top)));
+                            const __half2 k = __float2half2_rn(hs[i] * __uint_as_float((254u << 23) - __float_as_uint(top)));
                             f[i][0] = __hmul2(*reinterpret_cast<const __half2 *>(&v[i].x), k);
                             f[i][1] = __hmul2(*reinterpret_cast<const __half2 *>(&v[i].y), k);
-                            inverse[i] = top < 0x1p114f ? top * 128.0f : INFINITY;   // 2^114: of an infinite h
+                            inverse[i] = top < 0x1p121f ? top : INFINITY;   // 2^121: of an infinite h
                         } else {
                             uint32_t a0, a1;
                             asm("abs.bf16x2 %0, %1;" : "=r"(a0) : "r"(v[i].x));
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
 #pragma unroll
                             for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
                             float inverse;
-                            const float sc = scale_to_half(amax, inverse);
+                            const float sc = scale_to_half<7>(amax, inverse);   // as the codes are made from
                             const int m = 8 * g + j + (low ? 0 : 4);
                             if (m < n && col < a.I) {
                                 const int64_t pair = L.pair[first + m];
