@@ -611,6 +611,10 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
             }
             if (!ok) break;
             const Tile128 cur = tt;
+            // the next tile's first scales are on their way while this one is stored (8192 x 8192 x 256
+            // 36.0 us, asked for after it 39.9; FUSED: after it, for want of registers in the epilogue)
+            if constexpr (!FUSED)
+                if (t + units < tiles) begin(t + units);
             if constexpr (SPLIT) {
                 // the partial sums go to the operand ring's memory (nothing is in
                 // flight there any more: the last partial came after the last load),
@@ -650,7 +654,8 @@ __global__ void __launch_bounds__(T128_THREADS, 1) bsfp8_block128_tile(const __g
                 if constexpr (FUSED)
                     if (lane_here() == 0) mbar_arrive(&ctl->taken);
             }
-            if (t + units < tiles) begin(t + units);
+            if constexpr (FUSED)
+                if (t + units < tiles) begin(t + units);
         }
     }
 
