@@ -107,21 +107,24 @@ double even_bytes(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
 }
 
 // Whether the tile form (moe_tile.cuh) serves the call, else the one for few tokens
-// (moe_layer.cuh), whose set-up is some 10 us shorter, whose rate falls as the tokens grow, and
-// which reads an expert's weights again for each eight tokens.  By the weights that even routing
-// reads; few-token form against tiles, us (hidden x inner):
-//   4 to 8 tokens up from 120 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 14.6, 20.1; 8, 2 of 8 of
-//     4096 x 1024 (91) 21.9, 26.7; 8, 7 of 7 of 6864 x 816 (118) 33.0, 39.1; 8, 4 of 32 of 2048 x 1024
-//     (132) 40.5, 36.2; 8, 8 of 256 of 2048 x 512 (181) 49.2, 42.6; 8, 2 of 8 of 4096 x 14336 (1270)
-//     225, 191; 8, 8 of 64 of 7168 x 2048 (1850) 289, 274
-//   fewer from 400 MB: 1, 4 of 32 of 2048 x 1024 (25) 8.5, 19.5; 2, 8 of 64 of 4096 x 1536 (283)
-//     55.0, 57.7; 1, 8 of 64 of 7168 x 2048 (352) 64.0, 66.0; 3, 1 of 8 of 4096 x 14336 (465) 98.8,
-//     91.9; 2, 8 of 64 of 7168 x 2048 (660) 116.5, 115.4
-//   more by what both cost: 6.5 us, 0.17 for each MB that all eights read and 1.5 for 1000 CTAs of
-//     the up product, against 13.5, 0.8 for each token of an expert and 0.09 for each MB.  4 of 24 of
-//     768 x 256: 9 tokens 10.3, 15.9, 32 18.1, 19.2, 64 29.3, 24.1; 3 of 11 of 1344 x 512: 16 tokens
-//     16.3, 18.8, 32 25.0, 22.7; 2 of 6 of 2048 x 1024: 9 tokens 16.3, 19.6, 24 25.1, 24.4; 8 of 32 of
-//     1024 x 512: 9 tokens 24.2, 19.8
+// (moe_layer.cuh), whose set-up is 5 to 12 us shorter, whose rate falls as the tokens grow, and
+// which reads an expert's weights again for each eight tokens (from L2).  By the weights that even
+// routing reads; few-token form against tiles, us (hidden x inner), weights from HBM (and in L2, one
+// call repeated):
+//   4 to 8 tokens up from 120 MB: 5, 2 of 16 experts of 2048 x 1024 (49 MB) 18.1, 23.9 (15.1, 20.9); 8,
+//     2 of 8 of 4096 x 1024 (91) 26.4, 31.8 (21.7, 27.3); 8, 7 of 7 of 6864 x 816 (118) 34.5, 42.1
+//     (32.8, 39.3); 8, 4 of 32 of 2048 x 1024 (132) 38.4, 35.6; 8, 8 of 256 of 2048 x 512 (181) 48.7,
+//     43.1; 8, 2 of 8 of 4096 x 14336 (1270) 225, 191; 8, 8 of 64 of 7168 x 2048 (1850) 289, 274
+//   fewer from 400 MB: 1, 4 of 32 of 2048 x 1024 (25) 11.0, 21.8 (8.8, 20.8); 2, 8 of 64 of 4096 x 1536
+//     (283) 60.8, 63.1; 1, 8 of 64 of 7168 x 2048 (352) 64.0, 66.0; 3, 1 of 8 of 4096 x 14336 (465)
+//     98.8, 91.9; 2, 8 of 64 of 7168 x 2048 (660) 116.5, 115.4
+//   more by what both cost with weights in L2 (HBM adds about as much to either): 6.5 us, 0.17 for each
+//     MB that all eights read and 1.5 for 1000 CTAs of the up product, against 13.5, 0.8 for each token
+//     of an expert and 0.09 for each MB.  4 of 24 of 768 x 256: 9 tokens 11.0, 16.7 (9.9, 15.2), 32 19.4,
+//     20.2 (17.8, 18.8), 64 31.4, 25.2 (29.1, 24.6); 3 of 11 of 1344 x 512: 16 tokens 17.7, 21.0 (15.6,
+//     19.7), 32 26.9, 24.1 (24.6, 22.7); 2 of 6 of 2048 x 1024: 9 tokens 18.6, 23.2 (16.6, 20.7), 24 29.2,
+//     26.6 (25.2, 24.7); 8 of 32 of 1024 x 512: 9 tokens 26.5, 24.1 (24.1, 20.6); 2 of 16 of 2048 x 1024:
+//     12 tokens 31.3, 27.7 (24.7, 22.0)
 bool takes_tiles(int64_t T, int32_t top, int32_t E, int64_t H, int64_t I) {
     const double bytes = even_bytes(T, top, E, H, I);
     if (T <= MOE_FEW_TOKENS) return bytes >= (T < 4 ? 400e6 : 120e6);

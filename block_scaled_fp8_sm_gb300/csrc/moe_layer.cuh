@@ -10,7 +10,8 @@
 // 16-byte pieces that it will multiply to shared memory of its own, some K blocks ahead, and
 // takes them from there without a barrier (3 tokens, 8 of 64 experts of 7168 x 2048, 16 of them
 // busy: 120 us, 5.9 TB/s; held in registers, one block ahead, 143).  1 token, 4 of 32 of 2048 x
-// 1024: 8.7 us, 25 MB; there the two launches and the first loads of each are most of it.
+// 1024: 11.0 us, 25 MB (8.8 with the weights in L2); there the two launches and the first loads of
+// each are most of it.
 //
 // More than eight tokens are as many calls side by side (the grid's z), which share the weights in
 // L2: with small weights that costs less than the set-up of moe_tile.cuh (the rule of moe_api.cu).

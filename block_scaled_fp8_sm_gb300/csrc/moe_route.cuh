@@ -18,6 +18,10 @@
 // and few others do; those that do (up to 32) come to a lane each, which counts the ones
 // before it (16001 tokens, 8 of 256: 19 us; by picks of sorted lanes 22, of unsorted ones 37).
 //
+// Weights: expf, a sum over the lanes and __fdividef, off by 4.0e-8 to 6.7e-8 of the weights' norm
+// (plain fp32 3.8e-8 to 6.0e-8); with correctly rounded quotients 3.8e-8 to 6.6e-8, and 16001
+// tokens, 8 of 256 by sigmoids, take 19.5 us for 18.8.
+//
 // The expert order is a counting sort: integer counts of each CTA's tokens, and in the second
 // kernel each CTA's base from the counts of the CTAs before it; nothing depends on the order in
 // which atomics arrive.

@@ -18,8 +18,8 @@
 // weights through registers 992, tiles of 128 rows 523 (an MMA costs ~60 cycles for its A side
 // whatever N is, a TMA request ~70 of its thread), 256 481, an expert's K blocks walked without
 // divisions 465, the parts of the cut tiles added by a kernel of their own 459.  Small weights pay
-// the set-up: 19 tokens, 3 of 16 of 2064 x 1040 (98 MB) 27 us, of which 1.5 to 2 are the lists and 3
-// each change of kernels.
+// the set-up: 19 tokens, 3 of 16 of 2064 x 1040 (98 MB) 32 us (27.7 with the weights in L2), of which
+// 1.5 to 2 are the lists and 3 each change of kernels.
 //
 // NG (groups of eight tokens that the call has: 1, 2, 4, 8) sets the registers and the memory of
 // the sums: with 8 for all of them 12 tokens, 2 of 16 of 2048 x 1024, take 27.8 us for 22.3.
@@ -648,8 +648,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1) bsfp8_moe_tile(const __grid_con
 // The tiles that a cut goes through: a CTA adds the parts of one token and one tile in their
 // order, eight on their way, four columns a thread.  A kernel of its own, because it is all latency:
 // by the CTA that came last to a tile, the layer took 34.7 us for 28.6 (44 tokens, 2 of 9 experts of
-// 1376 x 1584, 6 tiles of 25 parts), 32.1 for 26.8 (19 tokens, 3 of 16 of 2064 x 1040) and 468 for 459
-// (64 tokens, 8 of 64 of 7168 x 2048).
+// 1376 x 1584, 6 tiles of 25 parts, weights in L2), 32.1 for 26.8 (19 tokens, 3 of 16 of 2064 x 1040,
+// in L2) and 468 for 459 (64 tokens, 8 of 64 of 7168 x 2048).
 constexpr int MT_JOIN_THREADS = MT_ROWS / 4;
 
 __global__ void __launch_bounds__(MT_JOIN_THREADS) bsfp8_moe_join(const MoeTileArgs a) {
